@@ -364,6 +364,156 @@ int swiglu_act_bwd_fp8(int dtype, int64_t rows, int64_t cols,
                        uint8_t* q_dgate, uint8_t* scale_dgate, uint8_t* q_dup, uint8_t* scale_dup,
                        float* weight_grad, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The routed block around the stage: router, few-token experts, block norms.
+ * ------------------------------------------------------------------------ */
+
+/* Router scores. */
+enum swiglu_score {
+  SWIGLU_SCORE_SOFTMAX = 0,   /* s = softmax(logits) over all experts     */
+  SWIGLU_SCORE_SIGMOID = 1    /* s = sigmoid(logits), expert by expert    */
+};
+
+/* Sizes of the routed entry points: at most SWIGLU_MAX_TOPK experts per
+ * token out of at most SWIGLU_MAX_EXPERTS, and, for swiglu_moe_fwd, at most
+ * SWIGLU_MOE_MAX_TOKENS tokens. */
+#define SWIGLU_MAX_TOPK 16
+#define SWIGLU_MAX_EXPERTS 1024
+#define SWIGLU_MOE_MAX_TOKENS 64
+
+/* Router: the k best experts of each token and their weights.
+ *   ids[t, j]      the expert with the j-th greatest logit of token t, equal
+ *                  logits in order of their index; a logit of -infinity
+ *                  masks its expert, and where fewer than k are left the
+ *                  remaining ids are -1
+ *   weights[t, j]  scale * s[ids[t, j]], or with renorm != 0
+ *                  scale * s[ids[t, j]] / sum_i s[ids[t, i]];  0 where the id
+ *                  is -1 (a token with every expert masked: all 0)
+ * with the scores s of `score`.  The renormalised forms divide scores by the
+ * greatest one's exponential, so they stay finite where every chosen score
+ * underflows.  A NaN logit is never chosen and makes all k weights of its
+ * token NaN; so does +infinity under softmax (inf - inf).
+ *
+ *   logits   [T, E] fp32 or bf16 (dtype), 16-byte aligned
+ *   weights  [T, k] fp32,  ids [T, k] int32 (outputs, 4-byte aligned)
+ * 1 <= E <= SWIGLU_MAX_EXPERTS, 1 <= k <= min(E, SWIGLU_MAX_TOPK), else
+ * SWIGLU_ERR_SHAPE; unknown score, or scale not finite: SWIGLU_ERR_ARG. */
+int swiglu_route_fwd(int score, int renorm, int dtype, int64_t T, int64_t E, int64_t k,
+                     const void* logits, float scale, float* weights, int32_t* ids, void* stream);
+
+/* Gradient of swiglu_route_fwd's weights: given ids as it chose them (ids
+ * themselves have no gradient) and dweights,
+ *   dlogits[t, e] = sum_j dweights[t, j] * d weights[t, j] / d logits[t, e].
+ * With q the weights before `scale` and d = scale * dweights:
+ *   softmax           p_e (d_e - sum_j q_j d_j) over all e (d_e = 0 if not chosen)
+ *   softmax, renorm   q_j (d_j - sum_i q_i d_i) at the chosen, 0 elsewhere
+ *   sigmoid           d_j s_j (1 - s_j)
+ *   sigmoid, renorm   q_j (d_j - sum_i q_i d_i) (1 - s_j)
+ * Masked experts (-infinity) get 0.  Entries with an id outside [0, E) are
+ * skipped, dweights included; an expert named twice in a row gets both
+ * terms.  A token whose weights are NaN gets NaN in all of dlogits.
+ *
+ *   logits [T, E] and scale, score, renorm, as given to swiglu_route_fwd
+ *   ids [T, k] int32, dweights [T, k] fp32
+ *   dlogits [T, E] (output, dtype, 16-byte aligned; written whole)
+ * Sizes and errors as swiglu_route_fwd. */
+int swiglu_route_bwd(int score, int renorm, int dtype, int64_t T, int64_t E, int64_t k,
+                     const void* logits, float scale, const int32_t* ids, const float* dweights,
+                     void* dlogits, void* stream);
+
+/* Bytes of device workspace swiglu_moe_fwd needs (0 for sizes it rejects). */
+size_t swiglu_moe_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t k);
+
+/* The routed MLP for a few tokens, bf16: with e = ids[t, j],
+ *   y[t] = sum_j weights[t, j] * Wd_e (act(Wg_e x[t]) * (Wu_e x[t]))
+ * The weights of each expert that some token names are read once for all its
+ * tokens; other experts are not read.  Products accumulate in fp32 in a fixed
+ * order (results are deterministic), the hidden activations are kept to 16
+ * significant bits, and y is rounded once.  Entries with an id outside [0, E)
+ * are skipped (no expert had room; a token without experts gets 0); an expert
+ * named twice by a token counts twice.
+ *
+ *   act           SWIGLU_ACT_SILU or SWIGLU_ACT_GELU_TANH
+ *   x             [T, K] bf16;  ids [T, k] int32, weights [T, k] fp32
+ *   wg, wu        expert e's [N, K] at wg + e * wg_stride, wu + e * wu_stride
+ *                 (elements), so that stacked [E, 2 N, K] weights are wg and
+ *                 wg + N * K with strides of 2 * N * K
+ *   wd            expert e's [K, N] at wd + e * wd_stride
+ *   y             [T, K] bf16 (output)
+ *   workspace     at least swiglu_moe_workspace_bytes(T, N, K, k) bytes,
+ *                 256-byte aligned; contents are scratch (they need not be
+ *                 cleared, and calls that overlap need one each)
+ * Layout rules: K % 8 == 0, N % 8 == 0, strides that are multiples of 8, at
+ * least N * K or 0 where E == 1, else SWIGLU_ERR_SHAPE; T <=
+ * SWIGLU_MOE_MAX_TOKENS, k and E as swiglu_route_fwd; K, N <= 2^20, else
+ * SWIGLU_ERR_UNSUPPORTED. */
+int swiglu_moe_fwd(int act, int64_t T, int64_t E, int64_t k, int64_t N, int64_t K,
+                   const void* x, const int32_t* ids, const float* weights,
+                   const void* wg, int64_t wg_stride, const void* wu, int64_t wu_stride,
+                   const void* wd, int64_t wd_stride, void* y,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norms around a block in one pass: a block's output y joins the residual
+ * stream through its own norm, a gate and the residual scale, and the next
+ * block's norm follows.  With RMS(v) = v / sqrt(mean(v^2) + eps) per row:
+ *   n       = RMS(y) * (w_offset + w_out)      (n = y where w_out is NULL)
+ *   res_out = skip * res + scale * gate[g] * n (gate = 1 where gate is NULL)
+ *   z       = RMS(res_out) * (w_offset + w_in) (no z where w_in is NULL)
+ * z is formed from res_out before its rounding.  Where y is NULL there is no
+ * block to join: z = RMS(res) * (w_offset + w_in), and w_out, gate and
+ * res_out must be NULL.  Arithmetic is fp32, sums of squares included (rows
+ * whose sum of squares passes the fp32 range are not supported); each output
+ * is rounded once.
+ *
+ *   res, y      [rows, cols] (dtype)
+ *   w_out, w_in [cols] (dtype)
+ *   gate        [groups, cols] (dtype): row r uses gate[r / (rows / groups)],
+ *               so groups = 1 is a gate per channel and groups = batch one per
+ *               sample; groups is 0 where gate is NULL
+ *   res_out, z  [rows, cols] (outputs, dtype)
+ * Any cols from 1 to 16384 (else SWIGLU_ERR_UNSUPPORTED) and pointers aligned
+ * to an element; rows % groups == 0, else SWIGLU_ERR_SHAPE; eps > 0 and
+ * finite skip, scale, w_offset, eps, else SWIGLU_ERR_ARG; y and w_in not both
+ * NULL. */
+int swiglu_block_norm_fwd(int dtype, int64_t rows, int64_t cols, int64_t groups,
+                          const void* res, const void* y, const void* w_out, const void* gate, const void* w_in,
+                          float skip, float scale, float w_offset, float eps,
+                          void* res_out, void* z, void* stream);
+
+/* Bytes of device workspace swiglu_block_norm_bwd needs (0 for sizes it rejects). */
+size_t swiglu_block_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t groups);
+
+/* Gradients of swiglu_block_norm_fwd.  With t = dres_out + (d z / d res_out)^T dz
+ * and r(v) = 1 / sqrt(mean(v^2) + eps):
+ *   RMS^T(v, d) = r(v) (d - RMS(v) mean(d RMS(v)))
+ *   t     = dres_out + RMS^T(res_out, dz * (w_offset + w_in))
+ *   dw_in = sum over rows of dz * RMS(res_out)
+ *   dres  = skip * t
+ *   dgate = sum over a group's rows of scale * t * n
+ *   dw_out = sum over rows of scale * t * gate * RMS(y)
+ *   dy    = RMS^T(y, scale * t * gate * (w_offset + w_out))
+ *           (scale * t * gate where w_out is NULL)
+ * Sums over rows are fp32 in a fixed order (results are deterministic).
+ *
+ *   res_out     the forward's (rounded) output, or res where y is NULL; not
+ *               read where w_in is NULL (may be NULL there)
+ *   y, w_out, gate, w_in, groups, skip, scale, w_offset, eps as the forward's
+ *   dres_out    [rows, cols], or NULL for 0;  dz [rows, cols], NULL exactly
+ *               where w_in is
+ *   dres        [rows, cols] output (where y is NULL: dres = t)
+ *   dy, dw_out, dgate, dw_in  outputs shaped as y, w_out, gate, w_in, NULL
+ *               exactly where those are
+ *   workspace   at least swiglu_block_norm_bwd_workspace_bytes(...) bytes,
+ *               256-byte aligned; contents are scratch
+ * rows == 0 gives zero weight gradients.  Errors as the forward's, and
+ * SWIGLU_ERR_WORKSPACE. */
+int swiglu_block_norm_bwd(int dtype, int64_t rows, int64_t cols, int64_t groups,
+                          const void* res_out, const void* y, const void* w_out, const void* gate, const void* w_in,
+                          const void* dres_out, const void* dz,
+                          float skip, float scale, float w_offset, float eps,
+                          void* dres, void* dy, void* dw_out, void* dgate, void* dw_in,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Measurement aid: the decode kernel's read-only twin.  The same launch as
  * swiglu_gemv_fwd for (M, N, K) -- the same kernel's grid, LDS footprint,
  * x loads and weight loads (and, for M >= 4, the weights' trip through LDS),

@@ -17,7 +17,12 @@ SWIGLU_F32 = 0
 SWIGLU_BF16 = 1
 SWIGLU_ACT_SILU = 0
 SWIGLU_ACT_GELU_TANH = 1
+SWIGLU_SCORE_SOFTMAX = 0
+SWIGLU_SCORE_SIGMOID = 1
 SWIGLU_ERR_SCRATCH = 9
+MAX_TOPK = 16                        # SWIGLU_MAX_TOPK
+MAX_EXPERTS = 1024                   # SWIGLU_MAX_EXPERTS
+MOE_MAX_TOKENS = 64                  # SWIGLU_MOE_MAX_TOKENS
 NOALLOC_SCRATCH_BYTES = 128 << 20    # SWIGLU_NOALLOC_SCRATCH_BYTES
 
 _c_i64 = ctypes.c_int64
@@ -61,6 +66,22 @@ SIGNATURES = {
                                          ctypes.c_float, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
     "swiglu_act_bwd_fp8": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
                                           ctypes.c_float, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+    "swiglu_route_fwd": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr,
+                                        ctypes.c_float, _c_ptr, _c_ptr, _c_ptr]),
+    "swiglu_route_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr,
+                                        ctypes.c_float, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+    "swiglu_moe_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64, _c_i64]),
+    "swiglu_moe_fwd": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr,
+                                      _c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr,
+                                      ctypes.c_size_t, _c_ptr]),
+    "swiglu_block_norm_fwd": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                             _c_ptr, ctypes.c_float, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                                             _c_ptr, _c_ptr, _c_ptr]),
+    "swiglu_block_norm_bwd_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64]),
+    "swiglu_block_norm_bwd": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                             _c_ptr, _c_ptr, _c_ptr, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                                             ctypes.c_float, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                             ctypes.c_size_t, _c_ptr]),
     "swiglu_probe_mfma": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _c_ptr, _c_ptr]),
     "swiglu_probe_gemv_read": (ctypes.c_int, [_c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
     "swiglu_probe_act_quant_stream": (ctypes.c_int, [_c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),

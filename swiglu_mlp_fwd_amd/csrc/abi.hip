@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "block.hpp"
 #include "gemm.hpp"
 #include "swiglu.h"
 #include "validate.hpp"
@@ -321,6 +322,89 @@ int swiglu_act_bwd(int64_t rows, int64_t cols, const float* gate, const float* u
                    float* weight_grad, void* stream) {
   return swiglu_act_bwd_dt(SWIGLU_F32, rows, cols, gate, up, dy, weights, clamp_limit, dgate, dup,
                            weight_grad, stream);
+}
+
+int swiglu_route_fwd(int score, int renorm, int dtype, int64_t T, int64_t E, int64_t k, const void* logits,
+                     float scale, float* weights, int32_t* ids, void* stream) {
+  int st = swg::validate_route(score, dtype, T, E, k, logits, scale, weights, ids, nullptr, false);
+  if (st != SWIGLU_OK || T == 0) return st;
+  swg::RouteArgs a{};
+  a.logits = logits; a.T = (int)T; a.E = (int)E; a.k = (int)k;
+  a.renorm = renorm != 0; a.scale = scale;
+  a.weights = weights; a.ids = ids;
+  return hip_status(swg::launch_route_fwd(as_dt(dtype), static_cast<swg::Score>(score), a, as_stream(stream)));
+}
+
+int swiglu_route_bwd(int score, int renorm, int dtype, int64_t T, int64_t E, int64_t k, const void* logits,
+                     float scale, const int32_t* ids, const float* dweights, void* dlogits, void* stream) {
+  int st = swg::validate_route(score, dtype, T, E, k, logits, scale, dweights, ids, dlogits, true);
+  if (st != SWIGLU_OK || T == 0) return st;
+  swg::RouteArgs a{};
+  a.logits = logits; a.T = (int)T; a.E = (int)E; a.k = (int)k;
+  a.renorm = renorm != 0; a.scale = scale;
+  a.ids_in = ids; a.dweights = dweights; a.dlogits = dlogits;
+  return hip_status(swg::launch_route_bwd(as_dt(dtype), static_cast<swg::Score>(score), a, as_stream(stream)));
+}
+
+size_t swiglu_moe_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t k) {
+  return swg::moe_workspace_total(T, N, K, k);
+}
+
+int swiglu_moe_fwd(int act, int64_t T, int64_t E, int64_t k, int64_t N, int64_t K, const void* x, const int32_t* ids,
+                   const float* weights, const void* wg, int64_t wg_stride, const void* wu, int64_t wu_stride,
+                   const void* wd, int64_t wd_stride, void* y, void* workspace, size_t workspace_bytes, void* stream) {
+  if (act != SWIGLU_ACT_SILU && act != SWIGLU_ACT_GELU_TANH) return SWIGLU_ERR_ARG;
+  int st = swg::validate_moe(T, E, k, N, K, x, ids, weights, wg, wg_stride, wu, wu_stride, wd, wd_stride, y,
+                             workspace, workspace_bytes);
+  if (st != SWIGLU_OK || T == 0 || K == 0) return st;
+  if (N == 0) return hip_status(fill_zero(SWIGLU_BF16, y, T, K, as_stream(stream)));
+  const swg::MoeLayout L = swg::moe_layout(T, N, K, k);
+  char* ws = static_cast<char*>(workspace);
+  swg::MoeArgs a{};
+  a.x = x; a.ids = ids; a.weights = weights;
+  a.wg = wg; a.wu = wu; a.wd = wd;
+  a.wg_stride = wg_stride; a.wu_stride = wu_stride; a.wd_stride = wd_stride;
+  a.y = y;
+  a.h_hi = ws + L.off_hi; a.h_lo = ws + L.off_lo; a.part = reinterpret_cast<float*>(ws + L.off_part);
+  a.T = (int)T; a.E = (int)E; a.k = (int)k; a.N = (int)N; a.K = (int)K;
+  return hip_status(swg::launch_moe(static_cast<swg::Act>(act), a, as_stream(stream)));
+}
+
+int swiglu_block_norm_fwd(int dtype, int64_t rows, int64_t cols, int64_t groups, const void* res, const void* y,
+                          const void* w_out, const void* gate, const void* w_in, float skip, float scale,
+                          float w_offset, float eps, void* res_out, void* z, void* stream) {
+  int st = swg::validate_norm_fwd(dtype, rows, cols, groups, res, y, w_out, gate, w_in, skip, scale, w_offset, eps,
+                                  res_out, z);
+  if (st != SWIGLU_OK || rows == 0) return st;
+  swg::NormArgs a{};
+  a.rows = rows; a.cols = (int)cols; a.groups = groups;
+  a.res = res; a.y = y; a.w_out = w_out; a.gate = gate; a.w_in = w_in;
+  a.skip = skip; a.scale = scale; a.w_offset = w_offset; a.eps = eps;
+  a.res_out = res_out; a.z = z;
+  return hip_status(swg::launch_norm_fwd(as_dt(dtype), a, as_stream(stream)));
+}
+
+size_t swiglu_block_norm_bwd_workspace_bytes(int64_t rows, int64_t cols, int64_t groups) {
+  return swg::norm_bwd_workspace_total(rows, cols, groups);
+}
+
+int swiglu_block_norm_bwd(int dtype, int64_t rows, int64_t cols, int64_t groups, const void* res_out, const void* y,
+                          const void* w_out, const void* gate, const void* w_in, const void* dres_out,
+                          const void* dz, float skip, float scale, float w_offset, float eps, void* dres, void* dy,
+                          void* dw_out, void* dgate, void* dw_in, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  int st = swg::validate_norm_bwd(dtype, rows, cols, groups, res_out, y, w_out, gate, w_in, dres_out, dz, skip, scale,
+                                  w_offset, eps, dres, dy, dw_out, dgate, dw_in, workspace, workspace_bytes);
+  if (st != SWIGLU_OK) return st;
+  swg::NormArgs a{};
+  a.rows = rows; a.cols = (int)cols; a.groups = groups;
+  a.res = res_out; a.y = y; a.w_out = w_out; a.gate = gate; a.w_in = w_in;
+  a.skip = skip; a.scale = scale; a.w_offset = w_offset; a.eps = eps;
+  a.dres_out = dres_out; a.dz = dz;
+  a.dres = dres; a.dy = dy; a.dw_out = dw_out; a.dgate = dgate; a.dw_in = dw_in;
+  a.part = static_cast<float*>(workspace);
+  a.per_group = (int)swg::norm_per_group(rows, groups);
+  return hip_status(swg::launch_norm_bwd(as_dt(dtype), a, as_stream(stream)));
 }
 
 int swiglu_probe_mfma(int iters, int blocks, float* sink, void* stream) {

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "swiglu.h"
 
 namespace swg {
@@ -246,6 +248,174 @@ inline int validate_act_bwd_fp8(int dtype, int64_t rows, int64_t cols, const voi
   if ((st = check_ptr(qg))) return st;
   if ((st = check_ptr(qu))) return st;
   if (sg == nullptr || su == nullptr) return SWIGLU_ERR_NULL;
+  return SWIGLU_OK;
+}
+
+// ---- routed block
+
+inline int check_route(int64_t T, int64_t E, int64_t k) {
+  if (T < 0 || T > kMaxDim || E < 1 || E > SWIGLU_MAX_EXPERTS) return SWIGLU_ERR_SHAPE;
+  if (k < 1 || k > E || k > SWIGLU_MAX_TOPK) return SWIGLU_ERR_SHAPE;
+  return SWIGLU_OK;
+}
+
+inline bool finite_f(float v) { return v - v == 0.0f; }
+
+// weights / dweights: `f`; ids: `i`; dlogits: `d` (nullptr in the forward's
+// check, which has no such argument: has_d says whether it must be there).
+inline int validate_route(int score, int dtype, int64_t T, int64_t E, int64_t k, const void* logits, float scale,
+                          const void* f, const void* i, const void* d, bool has_d) {
+  if (score != SWIGLU_SCORE_SOFTMAX && score != SWIGLU_SCORE_SIGMOID) return SWIGLU_ERR_ARG;
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if ((st = check_route(T, E, k))) return st;
+  if (!finite_f(scale)) return SWIGLU_ERR_ARG;
+  if (T == 0) return SWIGLU_OK;
+  if ((st = check_ptr(logits))) return st;
+  if (f == nullptr || i == nullptr) return SWIGLU_ERR_NULL;
+  if (!aligned(f, 4) || !aligned(i, 4)) return SWIGLU_ERR_ALIGN;
+  if (has_d && (st = check_ptr(d))) return st;
+  return SWIGLU_OK;
+}
+
+// Workspace of the few-token experts, regions on 256-byte boundaries: the
+// hidden activations' high and low halves [T k, N] bf16 and the expert
+// outputs [T k, K] fp32.
+struct MoeLayout {
+  size_t off_hi, off_lo, off_part, total;
+};
+
+constexpr int64_t kMoeMaxDim = int64_t(1) << 20;
+
+inline int moe_shape_status(int64_t T, int64_t N, int64_t K, int64_t k) {
+  if (T < 0 || T > SWIGLU_MOE_MAX_TOKENS || N < 0 || K < 0) return SWIGLU_ERR_SHAPE;
+  if (k < 1 || k > SWIGLU_MAX_TOPK) return SWIGLU_ERR_SHAPE;
+  if (K % 8 != 0 || N % 8 != 0) return SWIGLU_ERR_SHAPE;
+  if (N > kMoeMaxDim || K > kMoeMaxDim) return SWIGLU_ERR_UNSUPPORTED;
+  return SWIGLU_OK;
+}
+
+inline MoeLayout moe_layout(int64_t T, int64_t N, int64_t K, int64_t k) {
+  auto a256 = [](size_t v) { return (v + 255) / 256 * 256; };
+  MoeLayout L;
+  size_t off = 0;
+  L.off_hi = off;   off += a256((size_t)T * k * N * 2);
+  L.off_lo = off;   off += a256((size_t)T * k * N * 2);
+  L.off_part = off; off += a256((size_t)T * k * K * 4);
+  L.total = off;
+  return L;
+}
+
+inline size_t moe_workspace_total(int64_t T, int64_t N, int64_t K, int64_t k) {
+  return moe_shape_status(T, N, K, k) == SWIGLU_OK ? moe_layout(T, N, K, k).total : 0;
+}
+
+inline int validate_moe(int64_t T, int64_t E, int64_t k, int64_t N, int64_t K, const void* x, const void* ids,
+                        const void* weights, const void* wg, int64_t wg_stride, const void* wu,
+                        int64_t wu_stride, const void* wd, int64_t wd_stride, const void* y, const void* ws, size_t ws_bytes) {
+  int st = moe_shape_status(T, N, K, k);
+  if (st) return st;
+  if ((st = check_route(T, E, k))) return st;
+  for (int64_t stride : {wg_stride, wu_stride, wd_stride}) {
+    if (stride < 0 || stride % 8 != 0 || stride > (int64_t(1) << 48)) return SWIGLU_ERR_SHAPE;
+    if (stride < N * K && E > 1) return SWIGLU_ERR_SHAPE;
+  }
+  if (T == 0 || K == 0) return SWIGLU_OK;
+  if ((st = check_ptr(y))) return st;
+  if (N == 0) return SWIGLU_OK;                       // y is zero-filled
+  if ((st = check_ptr(x))) return st;
+  if (ids == nullptr || weights == nullptr) return SWIGLU_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(weights, 4)) return SWIGLU_ERR_ALIGN;
+  if ((st = check_ptr(wg))) return st;
+  if ((st = check_ptr(wu))) return st;
+  if ((st = check_ptr(wd))) return st;
+  if (ws == nullptr) return SWIGLU_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return SWIGLU_ERR_ALIGN;
+  if (ws_bytes < moe_layout(T, N, K, k).total) return SWIGLU_ERR_WORKSPACE;
+  return SWIGLU_OK;
+}
+
+constexpr int64_t kNormMaxCols = 16384;
+// Parts the backward's row sums are split into, over all groups (each group
+// has at least one).
+constexpr int64_t kNormParts = 512;
+
+inline int norm_shape_status(int64_t rows, int64_t cols, int64_t groups) {
+  if (rows < 0 || rows > kMaxDim || cols < 1 || groups < 0 || groups > kMaxDim) return SWIGLU_ERR_SHAPE;
+  if (groups > 0 && rows % groups != 0) return SWIGLU_ERR_SHAPE;
+  if (cols > kNormMaxCols) return SWIGLU_ERR_UNSUPPORTED;
+  return SWIGLU_OK;
+}
+
+// Parts per group: as many as kNormParts allows, at most one per row.
+inline int64_t norm_per_group(int64_t rows, int64_t groups) {
+  const int64_t g = groups > 0 ? groups : 1, rpg = rows / g;
+  int64_t per = (kNormParts + g - 1) / g;
+  if (per > rpg) per = rpg;
+  return per < 1 ? 1 : per;
+}
+
+// Two fp32 sums of [cols] per part.
+inline size_t norm_bwd_workspace_total(int64_t rows, int64_t cols, int64_t groups) {
+  if (norm_shape_status(rows, cols, groups) != SWIGLU_OK) return 0;
+  const int64_t g = groups > 0 ? groups : 1;
+  const size_t n = (size_t)2 * g * norm_per_group(rows, groups) * cols * 4;
+  return (n + 255) / 256 * 256;
+}
+
+inline int validate_norm(int dtype, int64_t rows, int64_t cols, int64_t groups, const void* y, const void* w_out,
+                         const void* gate, const void* w_in, float skip, float scale, float w_offset, float eps) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if ((st = norm_shape_status(rows, cols, groups))) return st;
+  if (!finite_f(skip) || !finite_f(scale) || !finite_f(w_offset) || !finite_f(eps) || !(eps > 0.0f))
+    return SWIGLU_ERR_ARG;
+  // Without rows y is empty, and an empty tensor may be NULL.
+  if (rows > 0 && y == nullptr && (w_out != nullptr || gate != nullptr || w_in == nullptr)) return SWIGLU_ERR_ARG;
+  if ((gate == nullptr) != (groups == 0)) return SWIGLU_ERR_ARG;
+  return SWIGLU_OK;
+}
+
+// Each pointer aligned to an element; `need`ed ones not NULL, the others NULL.
+struct PtrRule { const void* p; bool need; };
+inline int check_elems(int dtype, const PtrRule* r, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (r[i].need && r[i].p == nullptr) return SWIGLU_ERR_NULL;
+    if (!r[i].need && r[i].p != nullptr) return SWIGLU_ERR_ARG;
+    if (r[i].p != nullptr && !aligned(r[i].p, (uintptr_t)elem_size(dtype))) return SWIGLU_ERR_ALIGN;
+  }
+  return SWIGLU_OK;
+}
+
+inline int validate_norm_fwd(int dtype, int64_t rows, int64_t cols, int64_t groups, const void* res, const void* y,
+                             const void* w_out, const void* gate, const void* w_in, float skip, float scale,
+                             float w_offset, float eps, const void* res_out, const void* z) {
+  int st = validate_norm(dtype, rows, cols, groups, y, w_out, gate, w_in, skip, scale, w_offset, eps);
+  if (st || rows == 0) return st;
+  const PtrRule r[] = {{res, true}, {y, y != nullptr}, {w_out, w_out != nullptr}, {gate, gate != nullptr},
+                       {w_in, w_in != nullptr}, {res_out, y != nullptr}, {z, w_in != nullptr}};
+  return check_elems(dtype, r, 7);
+}
+
+inline int validate_norm_bwd(int dtype, int64_t rows, int64_t cols, int64_t groups, const void* res_out,
+                             const void* y, const void* w_out, const void* gate, const void* w_in,
+                             const void* dres_out, const void* dz, float skip, float scale, float w_offset, float eps,
+                             const void* dres, const void* dy, const void* dw_out, const void* dgate,
+                             const void* dw_in, const void* ws, size_t ws_bytes) {
+  int st = validate_norm(dtype, rows, cols, groups, y, w_out, gate, w_in, skip, scale, w_offset, eps);
+  if (st) return st;
+  const PtrRule grads[] = {{dw_out, w_out != nullptr}, {dgate, gate != nullptr}, {dw_in, w_in != nullptr}};
+  if ((st = check_elems(dtype, grads, 3))) return st;
+  if (rows == 0) return SWIGLU_OK;                    // the weights' gradients are zero-filled
+  const PtrRule r[] = {{y, y != nullptr}, {w_out, w_out != nullptr}, {gate, gate != nullptr},
+                       {w_in, w_in != nullptr}, {dz, w_in != nullptr}, {dres, true}, {dy, y != nullptr},
+                       {res_out, w_in != nullptr || res_out != nullptr},
+                       {dres_out, dres_out != nullptr}};
+  if ((st = check_elems(dtype, r, 9))) return st;
+  if (w_out == nullptr && gate == nullptr && w_in == nullptr) return SWIGLU_OK;   // nothing is summed over rows
+  if (ws == nullptr) return SWIGLU_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return SWIGLU_ERR_ALIGN;
+  if (ws_bytes < norm_bwd_workspace_total(rows, cols, groups)) return SWIGLU_ERR_WORKSPACE;
   return SWIGLU_OK;
 }
 
