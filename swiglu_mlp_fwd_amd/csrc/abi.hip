@@ -403,7 +403,6 @@ int swiglu_block_norm_bwd(int dtype, int64_t rows, int64_t cols, int64_t groups,
   a.dres_out = dres_out; a.dz = dz;
   a.dres = dres; a.dy = dy; a.dw_out = dw_out; a.dgate = dgate; a.dw_in = dw_in;
   a.part = static_cast<float*>(workspace);
-  a.per_group = (int)swg::norm_per_group(rows, groups);
   return hip_status(swg::launch_norm_bwd(as_dt(dtype), a, as_stream(stream)));
 }
 

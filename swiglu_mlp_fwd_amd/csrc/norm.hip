@@ -12,12 +12,20 @@
 // dw_in = b: one sum serves both dgate and dw_out.
 //
 // The work is bound by HBM: 2 to 4 tensors forward, 4 to 6 backward.  A row
-// is held in registers by kNT threads (one wave, or a whole workgroup) as
-// kCH 16-byte chunks each, so each tensor is read once; rows need not be
-// aligned (chunks load at any element's address, and the last chunk of a row
-// that is not whole goes element by element).
+// is held in registers by `nt` threads as kCH 16-byte chunks each, so each
+// tensor is read once: 16 lanes or one wave of a row for short rows (several
+// rows per workgroup), otherwise a whole workgroup of as many waves as the
+// row has chunks for.
+//
+// Rows need not be aligned nor a whole number of chunks: chunks load at any
+// element's address, and the chunk that would pass the row's end is loaded
+// from cols - kN instead, with the elements it shares with its neighbour
+// (`skip` of them) set to zero on use and left to that neighbour, so every
+// load is full and none is behind a branch.  Threads past the last chunk skip all
+// of theirs.
 #include "block.hpp"
 #include "common.hpp"
+#include "validate.hpp"
 
 namespace swg {
 
@@ -50,53 +58,77 @@ template <> struct Ch<bf16> {
   }
 };
 
-// Chunk c of the row at p; elements past cols read as zero.
-template <typename T>
-__device__ __forceinline__ u32x4 load_chunk(const T* p, int c, int cols) {
-  constexpr int kN = Ch<T>::kN;
-  const int c0 = c * kN;
-  if (c0 + kN <= cols) return *reinterpret_cast<const u32x4_any*>(p + c0);
-  u32x4 w = {0u, 0u, 0u, 0u};
-  if (c0 < cols) {
-    T tmp[kN] = {};
-#pragma unroll
-    for (int i = 0; i < kN - 1; ++i)
-      if (c0 + i < cols) tmp[i] = p[c0 + i];
-    w = __builtin_bit_cast(u32x4, tmp);
+// The chunk a thread holds: kN elements from `start`, of which the first
+// `skip` are another's.  kTiny: rows shorter than a chunk (start 0; elements
+// from cols on read as zero and are not stored).
+template <typename T, bool kTiny>
+struct Span {
+  static constexpr int kN = Ch<T>::kN;
+  int start, skip;
+  __device__ __forceinline__ Span(int c, int cols) {
+    const int c0 = c * kN;
+    if constexpr (kTiny) {
+      start = 0;
+      skip = c == 0 ? 0 : kN;
+    } else {
+      start = c0 + kN <= cols ? c0 : cols - kN;
+      const int d = c0 - start;
+      skip = d < kN ? d : kN;
+    }
   }
-  return w;
-}
-
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* p, int c, int cols, const u32x4& w) {
-  constexpr int kN = Ch<T>::kN;
-  const int c0 = c * kN;
-  if (c0 + kN <= cols) {
-    *reinterpret_cast<u32x4_any*>(p + c0) = w;
-  } else if (c0 < cols) {
-    T tmp[kN];
-    __builtin_memcpy(tmp, &w, 16);
+  // As it lies in memory: shared elements and all (kTiny: zeros past the end).
+  __device__ __forceinline__ u32x4 load(const T* row, int cols) const {
+    if constexpr (kTiny) {
+      T tmp[kN] = {};
 #pragma unroll
-    for (int i = 0; i < kN - 1; ++i)
-      if (c0 + i < cols) p[c0 + i] = tmp[i];
+      for (int i = 0; i < kN - 1; ++i)
+        if (skip == 0 && i < cols) tmp[i] = row[i];
+      return __builtin_bit_cast(u32x4, tmp);
+    } else {
+      return *reinterpret_cast<const u32x4_any*>(row + start);
+    }
   }
-}
-
-// Threads per workgroup for rows of kNT threads: 4 rows of one wave each, or
-// one row of the whole workgroup.
-template <int kNT> constexpr int kBlock = kNT == 64 ? 256 : kNT;
-
-// Sums of kS values over the kNT threads of a row, in a fixed order.  The
-// caller alternates `slot` between 0 and 1, so one barrier per sum suffices:
-// a buffer is rewritten only after every thread passed the other one's.
-template <int kNT, int kS>
-__device__ __forceinline__ void row_sum(float (&v)[kS], float (*buf)[kS][kNT / 64], int slot) {
+  // Without the elements to skip.  Apart from load, so that a row's loads are
+  // all requested before the first is waited for.
+  __device__ __forceinline__ u32x4 own(u32x4 w) const {
+    constexpr int kPer = kN / 4;                 // elements per word
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1)
+    for (int i = 0; i < 4; ++i) {
+      if (kPer == 2 && skip == 2 * i + 1) w[i] &= 0xFFFF0000u;
+      if (skip >= kPer * (i + 1)) w[i] = 0;
+    }
+    return w;
+  }
+  __device__ __forceinline__ void store(T* row, int cols, const u32x4& w) const {
+    if (!kTiny && skip == 0) {
+      *reinterpret_cast<u32x4_any*>(row + start) = w;
+    } else if (skip < kN) {
+      T tmp[kN];
+      __builtin_memcpy(tmp, &w, 16);
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (i >= skip && start + i < cols) row[start + i] = tmp[i];
+    }
+  }
+};
+
+// Lanes of a row: 16 or 64 of a wave, or (kWide) every thread of the workgroup.
+constexpr int kWide = 0;
+constexpr int kThreads = 512;                    // workgroups of several rows
+constexpr int kMaxThreads = 1024;
+
+// Sums of kS values over a row's threads, in a fixed order.  The caller
+// alternates `slot` between 0 and 1, so one barrier per sum suffices: a
+// buffer is rewritten only after every thread passed the other one's.
+template <int kL, int kS>
+__device__ __forceinline__ void row_sum(float (&v)[kS], float (*buf)[kS][kMaxThreads / 64], int slot) {
+  constexpr int kLanes = kL == kWide ? 64 : kL;
+#pragma unroll
+  for (int off = kLanes / 2; off >= 1; off >>= 1)
 #pragma unroll
     for (int s = 0; s < kS; ++s) v[s] += __shfl_xor(v[s], off);
-  if constexpr (kNT > 64) {
-    const int wave = threadIdx.x >> 6;
+  if constexpr (kL == kWide) {
+    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
       for (int s = 0; s < kS; ++s) buf[slot][s][wave] = v[s];
@@ -104,8 +136,7 @@ __device__ __forceinline__ void row_sum(float (&v)[kS], float (*buf)[kS][kNT / 6
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
       float sum = buf[slot][s][0];
-#pragma unroll
-      for (int w = 1; w < kNT / 64; ++w) sum += buf[slot][s][w];
+      for (int w = 1; w < waves; ++w) sum += buf[slot][s][w];
       v[s] = sum;
     }
   }
@@ -118,21 +149,39 @@ __device__ __forceinline__ float rstd_of(float sumsq, int cols, float eps) {
 // What a row's block adds: nothing, y itself, or y's norm.
 enum class Join { kNone, kPlain, kNorm };
 
-template <typename T, int kNT, int kCH, Join J, bool kZ>
-__global__ __launch_bounds__(kBlock<kNT>) void norm_fwd_kernel(NormArgs a) {
+template <typename T, int kL, int kCH, Join J, bool kZ, bool kTiny>
+__global__ __launch_bounds__(kMaxThreads) void norm_fwd_kernel(NormArgs a) {
   constexpr int kN = Ch<T>::kN;
-  __shared__ float buf[2][1][kNT / 64];
-  const int tid = threadIdx.x % kNT;
-  const uint32_t row = kNT == 64 ? blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  if (row >= a.rows) return;                     // a whole wave of a one-wave row
+  __shared__ float buf[2][1][kMaxThreads / 64];
+  const int nt = kL == kWide ? blockDim.x : kL;
+  const int tid = kL == kWide ? threadIdx.x : threadIdx.x % nt;
+  const uint32_t row = kL == kWide ? blockIdx.x : blockIdx.x * (blockDim.x / nt) + threadIdx.x / nt;
+  if (row >= a.rows) return;                     // whole rows, and no barrier follows where a workgroup has several
   const int64_t at = (int64_t)row * a.cols;
-  const T* w_out = static_cast<const T*>(a.w_out);
-  const T* w_in = static_cast<const T*>(a.w_in);
-  u32x4 res[kCH], y[kCH];
+  const bool gated = a.groups > 0;
+  const T* gate = static_cast<const T*>(a.gate);
+  if (gated) gate += (int64_t)(row / (uint32_t)(a.rows / a.groups)) * a.cols;
+  u32x4 res[kCH], y[kCH], wo[kCH], g[kCH], wi[kCH];
 #pragma unroll
   for (int i = 0; i < kCH; ++i) {
-    res[i] = load_chunk(static_cast<const T*>(a.res) + at, i * kNT + tid, a.cols);
-    if constexpr (J != Join::kNone) y[i] = load_chunk(static_cast<const T*>(a.y) + at, i * kNT + tid, a.cols);
+    const Span<T, kTiny> sp(i * nt + tid, a.cols);
+    res[i] = sp.load(static_cast<const T*>(a.res) + at, a.cols);
+    if constexpr (J != Join::kNone) y[i] = sp.load(static_cast<const T*>(a.y) + at, a.cols);
+  }
+#pragma unroll
+  for (int i = 0; i < kCH; ++i) {
+    const Span<T, kTiny> sp(i * nt + tid, a.cols);
+    if constexpr (J == Join::kNorm) wo[i] = sp.load(static_cast<const T*>(a.w_out), a.cols);
+    if (J != Join::kNone && gated) g[i] = sp.load(gate, a.cols);
+    if constexpr (kZ) wi[i] = sp.load(static_cast<const T*>(a.w_in), a.cols);
+  }
+#pragma unroll
+  for (int i = 0; i < kCH; ++i) {
+    const Span<T, kTiny> sp(i * nt + tid, a.cols);
+    if (sp.skip != 0) {
+      res[i] = sp.own(res[i]);
+      if constexpr (J != Join::kNone) y[i] = sp.own(y[i]);
+    }
   }
   float r[kCH][kN];
   if constexpr (J == Join::kNone) {
@@ -151,26 +200,20 @@ __global__ __launch_bounds__(kBlock<kNT>) void norm_fwd_kernel(NormArgs a) {
           const float v = Ch<T>::get(y[i], e);
           ss[0] = __builtin_fmaf(v, v, ss[0]);
         }
-      row_sum<kNT, 1>(ss, buf, 0);
+      row_sum<kL, 1>(ss, buf, 0);
       k = a.scale * rstd_of(ss[0], a.cols, a.eps);
     }
-    const T* gate = nullptr;
-    if (a.groups > 0) gate = static_cast<const T*>(a.gate) + (int64_t)(row / (uint32_t)(a.rows / a.groups)) * a.cols;
 #pragma unroll
     for (int i = 0; i < kCH; ++i) {
-      const int c = i * kNT + tid;
-      u32x4 w = {0u, 0u, 0u, 0u}, g = w;
-      if constexpr (J == Join::kNorm) w = load_chunk(w_out, c, a.cols);
-      if (gate != nullptr) g = load_chunk(gate, c, a.cols);
-      float o[kN];
+      const Span<T, kTiny> sp(i * nt + tid, a.cols);
 #pragma unroll
       for (int e = 0; e < kN; ++e) {
         float n = k * Ch<T>::get(y[i], e);
-        if constexpr (J == Join::kNorm) n *= a.w_offset + Ch<T>::get(w, e);
-        if (gate != nullptr) n *= Ch<T>::get(g, e);
-        r[i][e] = o[e] = __builtin_fmaf(a.skip, Ch<T>::get(res[i], e), n);
+        if constexpr (J == Join::kNorm) n *= a.w_offset + Ch<T>::get(wo[i], e);
+        if (gated) n *= Ch<T>::get(g[i], e);
+        r[i][e] = __builtin_fmaf(a.skip, Ch<T>::get(res[i], e), n);
       }
-      store_chunk(static_cast<T*>(a.res_out) + at, c, a.cols, Ch<T>::pack(o));
+      sp.store(static_cast<T*>(a.res_out) + at, a.cols, Ch<T>::pack(r[i]));
     }
   }
   if constexpr (kZ) {
@@ -178,230 +221,364 @@ __global__ __launch_bounds__(kBlock<kNT>) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < kCH; ++i)
 #pragma unroll
-      for (int e = 0; e < kN; ++e) ss[0] = __builtin_fmaf(r[i][e], r[i][e], ss[0]);   // 0 past the row's end
-    row_sum<kNT, 1>(ss, buf, 1);
+      for (int e = 0; e < kN; ++e) ss[0] = __builtin_fmaf(r[i][e], r[i][e], ss[0]);
+    row_sum<kL, 1>(ss, buf, 1);
     const float k = rstd_of(ss[0], a.cols, a.eps);
 #pragma unroll
     for (int i = 0; i < kCH; ++i) {
-      const int c = i * kNT + tid;
-      const u32x4 w = load_chunk(w_in, c, a.cols);
+      const Span<T, kTiny> sp(i * nt + tid, a.cols);
       float o[kN];
 #pragma unroll
-      for (int e = 0; e < kN; ++e) o[e] = r[i][e] * k * (a.w_offset + Ch<T>::get(w, e));
-      store_chunk(static_cast<T*>(a.z) + at, c, a.cols, Ch<T>::pack(o));
+      for (int e = 0; e < kN; ++e) o[e] = r[i][e] * k * (a.w_offset + Ch<T>::get(wi[i], e));
+      sp.store(static_cast<T*>(a.z) + at, a.cols, Ch<T>::pack(o));
     }
   }
 }
 
-// Part p of the rows: those of group p / per_group whose index in the group
-// is p % per_group modulo per_group.  A part is walked by the kNT threads of
-// one row; its sums a and b go to part[0][p] and part[1][p].
-template <typename T, int kNT, int kCH, Join J, bool kZ>
-__global__ __launch_bounds__(kBlock<kNT>) void norm_bwd_kernel(NormArgs a) {
+// Backward.  A workgroup walks one part of the rows: of group p / per_group,
+// those whose turn is p % per_group when the group's rows are dealt out R at
+// a time (R rows of the workgroup in parallel).  Its sums a and b (over its R
+// rows at a time, joined in LDS at the end) go to part[0][p] and part[1][p].
+// The weights stay in registers for the whole walk, and with kAhead the next
+// row's tensors are requested before the present row's sums, so the loads
+// are in flight over the barriers.
+template <typename T, int kL, int kCH, Join J, bool kZ, bool kTiny, bool kAhead>
+__global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
   constexpr int kN = Ch<T>::kN;
-  __shared__ float buf[2][2][kNT / 64];
-  const int tid = threadIdx.x % kNT;
-  const int64_t groups = a.groups > 0 ? a.groups : 1;
-  const int64_t parts = groups * a.per_group;
-  const int64_t p = kNT == 64 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-  if (p >= parts) return;
-  const int64_t rpg = a.rows / groups, g = p / a.per_group;
-  const T* gate = a.groups > 0 ? static_cast<const T*>(a.gate) + g * a.cols : nullptr;
-  const bool sum_a = J == Join::kNorm || gate != nullptr;
+  __shared__ float buf[2][2][kMaxThreads / 64];
+  extern __shared__ float joined[];              // several rows per workgroup: [R][cols]
+  const int nt = kL == kWide ? blockDim.x : kL;
+  const int tid = kL == kWide ? threadIdx.x : threadIdx.x % nt;
+  const int R = kL == kWide ? 1 : blockDim.x / nt, mine = kL == kWide ? 0 : threadIdx.x / nt;
+  const uint32_t groups = a.groups > 0 ? (uint32_t)a.groups : 1u;
+  const uint32_t p = blockIdx.x, grp = p / (uint32_t)a.per_group, turn = p % (uint32_t)a.per_group;
+  const int64_t rpg = (uint32_t)a.rows / groups;
+  const bool gated = a.groups > 0;
+  const bool sum_a = J == Join::kNorm || gated;
+  const bool need_y = J == Join::kNorm || (J == Join::kPlain && gated);
+  u32x4 wo[kCH], g[kCH], wi[kCH];
+#pragma unroll
+  for (int i = 0; i < kCH; ++i) {
+    const Span<T, kTiny> sp(i * nt + tid, a.cols);
+    if constexpr (J == Join::kNorm) wo[i] = sp.load(static_cast<const T*>(a.w_out), a.cols);
+    if (J != Join::kNone && gated) g[i] = sp.load(static_cast<const T*>(a.gate) + (int64_t)grp * a.cols, a.cols);
+    if constexpr (kZ) wi[i] = sp.load(static_cast<const T*>(a.w_in), a.cols);
+  }
   float sa[kCH][kN], sb[kCH][kN];
 #pragma unroll
   for (int i = 0; i < kCH; ++i)
 #pragma unroll
     for (int e = 0; e < kN; ++e) sa[i][e] = sb[i][e] = 0.0f;
 
-  int slot = 0;                                  // alternates over the row sums (row_sum)
-  for (int64_t q = p % a.per_group; q < rpg; q += a.per_group) {
-    const int64_t at = (g * rpg + q) * a.cols;
-    u32x4 t4[kCH], dz[kCH], rr[kCH], y[kCH];
+  struct Row { u32x4 t[kCH], dz[kCH], r[kCH], y[kCH]; };
+  auto load = [&](int64_t q, Row& x) {
+    const int64_t at = (grp * rpg + q) * a.cols;
 #pragma unroll
     for (int i = 0; i < kCH; ++i) {
-      const int c = i * kNT + tid;
-      t4[i] = u32x4{0u, 0u, 0u, 0u};
-      if (a.dres_out != nullptr) t4[i] = load_chunk(static_cast<const T*>(a.dres_out) + at, c, a.cols);
+      const Span<T, kTiny> sp(i * nt + tid, a.cols);
+      x.t[i] = u32x4{0u, 0u, 0u, 0u};
+      if (a.dres_out != nullptr) x.t[i] = sp.load(static_cast<const T*>(a.dres_out) + at, a.cols);
       if constexpr (kZ) {
-        dz[i] = load_chunk(static_cast<const T*>(a.dz) + at, c, a.cols);
-        rr[i] = load_chunk(static_cast<const T*>(a.res) + at, c, a.cols);
+        x.dz[i] = sp.load(static_cast<const T*>(a.dz) + at, a.cols);
+        x.r[i] = sp.load(static_cast<const T*>(a.res) + at, a.cols);
       }
-      if (J == Join::kNorm || (J == Join::kPlain && gate != nullptr))
-        y[i] = load_chunk(static_cast<const T*>(a.y) + at, c, a.cols);
+      if (need_y) x.y[i] = sp.load(static_cast<const T*>(a.y) + at, a.cols);
+    }
+  };
+  int slot = 0;                                  // alternates over the row sums (row_sum)
+  auto walk = [&](int64_t q, Row& x) {
+    const int64_t at = (grp * rpg + q) * a.cols;
+#pragma unroll
+    for (int i = 0; i < kCH; ++i) {
+      const Span<T, kTiny> sp(i * nt + tid, a.cols);
+      if (sp.skip != 0) {
+        x.t[i] = sp.own(x.t[i]);
+        if constexpr (kZ) {
+          x.dz[i] = sp.own(x.dz[i]);
+          x.r[i] = sp.own(x.r[i]);
+        }
+        if (need_y) x.y[i] = sp.own(x.y[i]);
+      }
     }
     float t[kCH][kN];
 #pragma unroll
     for (int i = 0; i < kCH; ++i)
 #pragma unroll
-      for (int e = 0; e < kN; ++e) t[i][e] = Ch<T>::get(t4[i], e);
+      for (int e = 0; e < kN; ++e) t[i][e] = Ch<T>::get(x.t[i], e);
     if constexpr (kZ) {
       float s[2] = {0.0f, 0.0f};                 // sum r'^2, sum dz (o + w_in) r'
 #pragma unroll
-      for (int i = 0; i < kCH; ++i) {
-        const u32x4 w = load_chunk(static_cast<const T*>(a.w_in), i * kNT + tid, a.cols);
+      for (int i = 0; i < kCH; ++i)
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-          const float v = Ch<T>::get(rr[i], e);
+          const float v = Ch<T>::get(x.r[i], e);
           s[0] = __builtin_fmaf(v, v, s[0]);
-          s[1] = __builtin_fmaf(Ch<T>::get(dz[i], e) * (a.w_offset + Ch<T>::get(w, e)), v, s[1]);
+          s[1] = __builtin_fmaf(Ch<T>::get(x.dz[i], e) * (a.w_offset + Ch<T>::get(wi[i], e)), v, s[1]);
         }
-      }
-      row_sum<kNT, 2>(s, buf, slot);
+      row_sum<kL, 2>(s, buf, slot);
       slot ^= 1;
       const float k = rstd_of(s[0], a.cols, a.eps);
       const float m = k * (s[1] / (float)a.cols);   // mean of d RMS(r')
 #pragma unroll
-      for (int i = 0; i < kCH; ++i) {
-        const u32x4 w = load_chunk(static_cast<const T*>(a.w_in), i * kNT + tid, a.cols);
+      for (int i = 0; i < kCH; ++i)
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-          const float v = Ch<T>::get(rr[i], e), d = Ch<T>::get(dz[i], e);
-          sb[i][e] = __builtin_fmaf(d, v * k, sb[i][e]);
-          t[i][e] += k * (d * (a.w_offset + Ch<T>::get(w, e)) - v * k * m);
+          const float h = Ch<T>::get(x.r[i], e) * k, d = Ch<T>::get(x.dz[i], e);
+          sb[i][e] = __builtin_fmaf(d, h, sb[i][e]);
+          t[i][e] = __builtin_fmaf(k, d * (a.w_offset + Ch<T>::get(wi[i], e)) - h * m, t[i][e]);
         }
-      }
     }
     const float skip = J == Join::kNone ? 1.0f : a.skip;
 #pragma unroll
     for (int i = 0; i < kCH; ++i) {
+      const Span<T, kTiny> sp(i * nt + tid, a.cols);
       float o[kN];
 #pragma unroll
       for (int e = 0; e < kN; ++e) o[e] = skip * t[i][e];
-      store_chunk(static_cast<T*>(a.dres) + at, i * kNT + tid, a.cols, Ch<T>::pack(o));
+      sp.store(static_cast<T*>(a.dres) + at, a.cols, Ch<T>::pack(o));
     }
+    // The gradient of n, scale t gate: t from here on where there is a gate
+    // (a takes t before it).
     if constexpr (J == Join::kNorm) {
       float s[2] = {0.0f, 0.0f};                 // sum y^2, sum d y with d = scale t gate (o + w_out)
 #pragma unroll
-      for (int i = 0; i < kCH; ++i) {
-        const int c = i * kNT + tid;
-        const u32x4 w = load_chunk(static_cast<const T*>(a.w_out), c, a.cols);
-        u32x4 g4 = {0u, 0u, 0u, 0u};
-        if (gate != nullptr) g4 = load_chunk(gate, c, a.cols);
+      for (int i = 0; i < kCH; ++i)
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-          const float v = Ch<T>::get(y[i], e);
-          float d = a.scale * (a.w_offset + Ch<T>::get(w, e));
-          if (gate != nullptr) d *= Ch<T>::get(g4, e);
+          const float v = Ch<T>::get(x.y[i], e);
+          float d = a.scale * (a.w_offset + Ch<T>::get(wo[i], e));
+          if (gated) d *= Ch<T>::get(g[i], e);
           s[0] = __builtin_fmaf(v, v, s[0]);
           s[1] = __builtin_fmaf(t[i][e] * d, v, s[1]);
         }
-      }
-      row_sum<kNT, 2>(s, buf, slot);
+      row_sum<kL, 2>(s, buf, slot);
       slot ^= 1;
       const float k = rstd_of(s[0], a.cols, a.eps);
       const float m = k * (s[1] / (float)a.cols);   // mean of d RMS(y)
 #pragma unroll
       for (int i = 0; i < kCH; ++i) {
-        const int c = i * kNT + tid;
-        const u32x4 w = load_chunk(static_cast<const T*>(a.w_out), c, a.cols);
-        u32x4 g4 = {0u, 0u, 0u, 0u};
-        if (gate != nullptr) g4 = load_chunk(gate, c, a.cols);
+        const Span<T, kTiny> sp(i * nt + tid, a.cols);
         float o[kN];
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
-          const float v = Ch<T>::get(y[i], e);
-          float d = a.scale * (a.w_offset + Ch<T>::get(w, e));
-          if (gate != nullptr) d *= Ch<T>::get(g4, e);
-          sa[i][e] = __builtin_fmaf(t[i][e], v * k, sa[i][e]);
-          o[e] = k * (t[i][e] * d - v * k * m);
+          const float h = Ch<T>::get(x.y[i], e) * k;
+          float d = a.scale * (a.w_offset + Ch<T>::get(wo[i], e));
+          if (gated) d *= Ch<T>::get(g[i], e);
+          sa[i][e] = __builtin_fmaf(t[i][e], h, sa[i][e]);
+          o[e] = k * (t[i][e] * d - h * m);
         }
-        store_chunk(static_cast<T*>(a.dy) + at, c, a.cols, Ch<T>::pack(o));
+        sp.store(static_cast<T*>(a.dy) + at, a.cols, Ch<T>::pack(o));
       }
     } else if constexpr (J == Join::kPlain) {
 #pragma unroll
       for (int i = 0; i < kCH; ++i) {
-        const int c = i * kNT + tid;
+        const Span<T, kTiny> sp(i * nt + tid, a.cols);
         float o[kN];
-        if (gate != nullptr) {
-          const u32x4 g4 = load_chunk(gate, c, a.cols);
 #pragma unroll
-          for (int e = 0; e < kN; ++e) {
-            sa[i][e] = __builtin_fmaf(t[i][e], Ch<T>::get(y[i], e), sa[i][e]);
-            o[e] = a.scale * t[i][e] * Ch<T>::get(g4, e);
+        for (int e = 0; e < kN; ++e) {
+          o[e] = a.scale * t[i][e];
+          if (gated) {
+            sa[i][e] = __builtin_fmaf(t[i][e], Ch<T>::get(x.y[i], e), sa[i][e]);
+            o[e] *= Ch<T>::get(g[i], e);
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < kN; ++e) o[e] = a.scale * t[i][e];
         }
-        store_chunk(static_cast<T*>(a.dy) + at, c, a.cols, Ch<T>::pack(o));
+        sp.store(static_cast<T*>(a.dy) + at, a.cols, Ch<T>::pack(o));
       }
+    }
+  };
+  const int64_t step = (int64_t)a.per_group * R;
+  int64_t q = (int64_t)turn * R + mine;
+  Row x;
+  if constexpr (kAhead) {
+    if (q < rpg) load(q, x);
+    while (q < rpg) {
+      Row next;
+      if (q + step < rpg) load(q + step, next);
+      walk(q, x);
+      x = next;
+      q += step;
+    }
+  } else {
+    for (; q < rpg; q += step) {
+      load(q, x);
+      walk(q, x);
     }
   }
   // The part's sums.
+  const int64_t parts = (int64_t)groups * a.per_group;
+  auto put = [&](float* out, const float (&v)[kCH][kN]) {
+    if constexpr (kL == kWide) {
 #pragma unroll
-  for (int i = 0; i < kCH; ++i)
+      for (int i = 0; i < kCH; ++i) {
+        const Span<T, kTiny> sp(i * nt + tid, a.cols);
+        if (!kTiny && sp.skip == 0) {
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      const int c = (i * kNT + tid) * kN + e;
-      if (c >= a.cols) continue;
-      if (sum_a) a.part[p * a.cols + c] = sa[i][e];
-      if (kZ) a.part[(parts + p) * a.cols + c] = sb[i][e];
+          for (int e = 0; e < kN; e += 4)
+            *reinterpret_cast<u32x4_any*>(out + sp.start + e) =
+                u32x4{f32_bits(v[i][e]), f32_bits(v[i][e + 1]), f32_bits(v[i][e + 2]), f32_bits(v[i][e + 3])};
+        } else {
+#pragma unroll
+          for (int e = 0; e < kN; ++e)
+            if (e >= sp.skip && (!kTiny || e < a.cols)) out[sp.start + e] = v[i][e];
+        }
+      }
+    } else {
+      __syncthreads();                           // the last sums have been read
+#pragma unroll
+      for (int i = 0; i < kCH; ++i) {
+        const Span<T, kTiny> sp(i * nt + tid, a.cols);
+#pragma unroll
+        for (int e = 0; e < kN; ++e)
+          if (e >= sp.skip && (!kTiny || e < a.cols)) joined[mine * a.cols + sp.start + e] = v[i][e];
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+        float s = joined[c];
+        for (int r = 1; r < R; ++r) s += joined[r * a.cols + c];
+        out[c] = s;
+      }
     }
+  };
+  if (sum_a) put(a.part + (int64_t)p * a.cols, sa);
+  if constexpr (kZ) put(a.part + (parts + p) * a.cols, sb);
 }
 
-// Adds the parts: a workgroup takes 64 columns, its 4 waves every fourth
-// part, joined in wave order.
+// Adds the parts.  A workgroup takes 64 columns of the sums a (blockIdx.y =
+// 0: dgate and dw_out) or b (1: dw_in).  With few groups its 16 waves share
+// each group's parts and are joined in wave order; from 16 groups on a wave
+// takes whole groups.  8 loads are in flight per lane.  At 512 parts of 4096
+// columns (16.8 MB): 4.8 us; one load at a time by 4 waves 63 us; 16 columns
+// per workgroup 9.5 us (two of them, on two L2s, share each 128-byte line).
+constexpr int kSumWaves = 16, kSumThreads = kSumWaves * 64;
+
+__device__ __forceinline__ float sum_parts(const float* __restrict__ p, int64_t n, int64_t first, int64_t step,
+                                           int64_t cols) {
+  constexpr int kU = 8;
+  float s = 0.0f;
+  int64_t i = first;
+  for (; i + (kU - 1) * step < n; i += kU * step) {
+    float v[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) v[u] = p[(i + u * step) * cols];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) s += v[u];
+  }
+  for (; i < n; i += step) s += p[i * cols];
+  return s;
+}
+
 template <typename T>
-__global__ __launch_bounds__(256) void norm_parts_kernel(NormArgs a) {
-  __shared__ float buf[2][4][64];
+__global__ __launch_bounds__(kSumThreads) void norm_parts_kernel(NormArgs a) {
+  constexpr int kGroups = 4;                     // groups joined at a time
+  __shared__ float buf[2][kGroups][kSumWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
   const bool in = c < a.cols;
   const int64_t groups = a.groups > 0 ? a.groups : 1;
   const int64_t per = a.rows > 0 ? a.per_group : 0, parts = groups * a.per_group;
-  const bool with_gate = a.dgate != nullptr, with_out = a.dw_out != nullptr;
-  const float w = with_out && in ? a.w_offset + (float)static_cast<const T*>(a.w_out)[c] : 1.0f;
+  // kS sums of the waves, to every wave, in wave order.
   int slot = 0;
-  auto total = [&](const float* base) {          // sum over `per` parts, to every wave
-    float s = 0.0f;
-    if (in)
-      for (int64_t i = wave; i < per; i += 4) s += base[i * a.cols + c];
-    buf[slot][wave][lane] = s;
+  auto join = [&](auto& v) {
+    constexpr int kS = sizeof(v) / sizeof(float);
+#pragma unroll
+    for (int i = 0; i < kS; ++i) buf[slot][i][wave][lane] = v[i];
     __syncthreads();
-    s = buf[slot][0][lane] + buf[slot][1][lane] + buf[slot][2][lane] + buf[slot][3][lane];
-    slot ^= 1;
-    return s;
-  };
-  if (with_gate || with_out) {
-    float dw = 0.0f;
-    for (int64_t g = 0; g < groups; ++g) {
-      const float s = a.scale * total(a.part + g * per * a.cols);
-      if (with_gate && wave == 0 && in) static_cast<T*>(a.dgate)[g * a.cols + c] = (T)(s * w);
-      const float gv = with_gate && in ? (float)static_cast<const T*>(a.gate)[g * a.cols + c] : 1.0f;
-      dw = __builtin_fmaf(gv, s, dw);
+#pragma unroll
+    for (int i = 0; i < kS; ++i) {
+      v[i] = buf[slot][i][0][lane];
+#pragma unroll
+      for (int w = 1; w < kSumWaves; ++w) v[i] += buf[slot][i][w][lane];
     }
-    if (with_out && wave == 0 && in) static_cast<T*>(a.dw_out)[c] = (T)dw;
+    slot ^= 1;
+  };
+  if (blockIdx.y == 1) {
+    if (a.dw_in == nullptr) return;
+    float s[1] = {in ? sum_parts(a.part + parts * a.cols + c, per * groups, wave, kSumWaves, a.cols) : 0.0f};
+    join(s);
+    if (wave == 0 && in) static_cast<T*>(a.dw_in)[c] = (T)s[0];
+    return;
   }
-  if (a.dw_in != nullptr) {
-    float s = 0.0f;
-    for (int64_t g = 0; g < groups; ++g) s += total(a.part + (parts + g * per) * a.cols);
-    if (wave == 0 && in) static_cast<T*>(a.dw_in)[c] = (T)s;
+  const bool with_gate = a.dgate != nullptr, with_out = a.dw_out != nullptr;
+  if (!with_gate && !with_out) return;
+  const float w = with_out && in ? a.w_offset + (float)static_cast<const T*>(a.w_out)[c] : 1.0f;
+  float dw = 0.0f;
+  auto group = [&](int64_t g, float s, bool store) {
+    s *= a.scale;
+    if (with_gate && store) static_cast<T*>(a.dgate)[g * a.cols + c] = (T)(s * w);
+    const float gv = with_gate ? (float)static_cast<const T*>(a.gate)[g * a.cols + c] : 1.0f;
+    dw = __builtin_fmaf(gv, s, dw);
+  };
+  if (groups < kSumWaves) {
+    for (int64_t g0 = 0; g0 < groups; g0 += kGroups) {
+      float s[kGroups];
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        s[i] = in && g0 + i < groups ? sum_parts(a.part + (g0 + i) * per * a.cols + c, per, wave, kSumWaves, a.cols) : 0.0f;
+      join(s);
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        if (in && g0 + i < groups) group(g0 + i, s[i], wave == 0);
+    }
+  } else {
+    if (in)
+      for (int64_t g = wave; g < groups; g += kSumWaves)
+        group(g, sum_parts(a.part + g * per * a.cols + c, per, 0, 1, a.cols), true);
+    float s[1] = {dw};
+    join(s);
+    dw = s[0];
   }
+  if (with_out && wave == 0 && in) static_cast<T*>(a.dw_out)[c] = (T)dw;
 }
 
-template <typename T, int kNT, int kCH, Join J, bool kZ>
-hipError_t launch_cfg(bool fwd, const NormArgs& a, hipStream_t s) {
-  const int64_t units = fwd ? a.rows : (a.groups > 0 ? a.groups : 1) * a.per_group;
-  const int64_t blocks = kNT == 64 ? (units + 3) / 4 : units;
-  if (fwd)
-    hipLaunchKernelGGL((norm_fwd_kernel<T, kNT, kCH, J, kZ>), dim3((unsigned)blocks), dim3(kBlock<kNT>), 0, s, a);
-  else
-    hipLaunchKernelGGL((norm_bwd_kernel<T, kNT, kCH, J, kZ>), dim3((unsigned)blocks), dim3(kBlock<kNT>), 0, s, a);
+template <typename T>
+hipError_t launch_parts(const NormArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(norm_parts_kernel<T>, dim3((unsigned)((a.cols + 63) / 64), 2), dim3(kSumThreads), 0, s, a);
   return hipGetLastError();
+}
+
+// One launch: rows of kL lanes (kWide: of as many waves as hold the row).
+// Forward workgroups of several rows have 256 threads, backward ones 512.
+template <typename T, int kL, int kCH, Join J, bool kZ, bool kTiny = false>
+hipError_t launch_cfg(bool fwd, NormArgs a, hipStream_t s) {
+  constexpr int kN = Ch<T>::kN;
+  const int nch = (a.cols + kN - 1) / kN;
+  int threads = ((nch + kCH - 1) / kCH + 63) / 64 * 64;
+  if (fwd) {
+    const int R = kL == kWide ? 1 : 256 / (kL == kWide ? 1 : kL);
+    if (kL != kWide) threads = 256;
+    hipLaunchKernelGGL((norm_fwd_kernel<T, kL, kCH, J, kZ, kTiny>), dim3((unsigned)((a.rows + R - 1) / R)),
+                       dim3(threads), 0, s, a);
+    return hipGetLastError();
+  }
+  const int64_t groups = a.groups > 0 ? a.groups : 1, rpg = a.rows / groups;
+  const int R = kL == kWide ? 1 : kThreads / (kL == kWide ? 1 : kL);
+  if (kL != kWide) threads = kThreads;
+  int64_t per = (kL == kWide ? norm_parts(a.cols) : kNormMinParts) / groups;
+  if (per > (rpg + R - 1) / R) per = (rpg + R - 1) / R;
+  a.per_group = (int)(per < 1 ? 1 : per);
+  const size_t lds = kL == kWide ? 0 : (size_t)R * a.cols * 4;
+  // Next-row loads where the registers hold two rows (128 per thread).
+  constexpr bool kAhead = kCH * kN <= 8;
+  hipLaunchKernelGGL((norm_bwd_kernel<T, kL, kCH, J, kZ, kTiny, kAhead>), dim3((unsigned)(groups * a.per_group)),
+                     dim3(threads), lds, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (a.dw_out == nullptr && a.dgate == nullptr && a.dw_in == nullptr) return hipSuccess;
+  return launch_parts<T>(a, s);
 }
 
 template <typename T, Join J, bool kZ>
 hipError_t launch_cols(bool fwd, const NormArgs& a, hipStream_t s) {
-  const int nch = (a.cols + Ch<T>::kN - 1) / Ch<T>::kN;
+  constexpr int kN = Ch<T>::kN;
+  const int nch = (a.cols + kN - 1) / kN;
+  if (a.cols < kN) return launch_cfg<T, 16, 1, J, kZ, true>(fwd, a, s);
+  if (nch <= 16) return launch_cfg<T, 16, 1, J, kZ>(fwd, a, s);
   if (nch <= 64) return launch_cfg<T, 64, 1, J, kZ>(fwd, a, s);
-  if (nch <= 128) return launch_cfg<T, 64, 2, J, kZ>(fwd, a, s);
-  if (nch <= 256) return launch_cfg<T, 256, 1, J, kZ>(fwd, a, s);
-  if (nch <= 512) return launch_cfg<T, 256, 2, J, kZ>(fwd, a, s);
-  if (nch <= 1024) return launch_cfg<T, 512, 2, J, kZ>(fwd, a, s);
-  if (nch <= 2048) return launch_cfg<T, 1024, 2, J, kZ>(fwd, a, s);
+  if (fwd && a.rows > 512 && nch > 256 && nch <= 2048) return launch_cfg<T, kWide, 2, J, kZ>(fwd, a, s);
+  if (nch <= 1024) return launch_cfg<T, kWide, 1, J, kZ>(fwd, a, s);
+  if (nch <= 2048) return launch_cfg<T, kWide, 2, J, kZ>(fwd, a, s);
   if constexpr (sizeof(T) == 4) {
-    if (nch <= 4096) return launch_cfg<T, 1024, 4, J, kZ>(fwd, a, s);
+    if (nch <= 4096) return launch_cfg<T, kWide, 4, J, kZ>(fwd, a, s);
   }
   return hipErrorInvalidValue;                   // past the checked number of columns
 }
@@ -422,15 +599,9 @@ hipError_t launch_norm_fwd(Dt dt, const NormArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_norm_bwd(Dt dt, const NormArgs& a, hipStream_t s) {
-  if (a.rows > 0) {
-    const hipError_t e = dt == Dt::kBF16 ? launch_t<bf16>(false, a, s) : launch_t<float>(false, a, s);
-    if (e != hipSuccess) return e;
-  }
+  if (a.rows > 0) return dt == Dt::kBF16 ? launch_t<bf16>(false, a, s) : launch_t<float>(false, a, s);
   if (a.dw_out == nullptr && a.dgate == nullptr && a.dw_in == nullptr) return hipSuccess;
-  const dim3 grid((unsigned)((a.cols + 63) / 64));
-  if (dt == Dt::kBF16) hipLaunchKernelGGL(norm_parts_kernel<bf16>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(norm_parts_kernel<float>, grid, dim3(256), 0, s, a);
-  return hipGetLastError();
+  return dt == Dt::kBF16 ? launch_parts<bf16>(a, s) : launch_parts<float>(a, s);   // sums over no rows
 }
 
 }  // namespace swg

@@ -336,9 +336,14 @@ inline int validate_moe(int64_t T, int64_t E, int64_t k, int64_t N, int64_t K, c
 }
 
 constexpr int64_t kNormMaxCols = 16384;
-// Parts the backward's row sums are split into, over all groups (each group
-// has at least one).
-constexpr int64_t kNormParts = 512;
+// Parts the backward's row sums are split into over all groups (each group
+// has at least one): a part is the walk of one workgroup, whose threads grow
+// with cols, so narrow rows take more of them to fill the chip.
+constexpr int64_t kNormMinParts = 512, kNormMaxParts = 2048;
+inline int64_t norm_parts(int64_t cols) {
+  const int64_t n = (int64_t(1) << 21) / cols;
+  return n < kNormMinParts ? kNormMinParts : (n > kNormMaxParts ? kNormMaxParts : n);
+}
 
 inline int norm_shape_status(int64_t rows, int64_t cols, int64_t groups) {
   if (rows < 0 || rows > kMaxDim || cols < 1 || groups < 0 || groups > kMaxDim) return SWIGLU_ERR_SHAPE;
@@ -347,19 +352,15 @@ inline int norm_shape_status(int64_t rows, int64_t cols, int64_t groups) {
   return SWIGLU_OK;
 }
 
-// Parts per group: as many as kNormParts allows, at most one per row.
-inline int64_t norm_per_group(int64_t rows, int64_t groups) {
-  const int64_t g = groups > 0 ? groups : 1, rpg = rows / g;
-  int64_t per = (kNormParts + g - 1) / g;
-  if (per > rpg) per = rpg;
-  return per < 1 ? 1 : per;
-}
-
-// Two fp32 sums of [cols] per part.
+// Two fp32 sums of [cols] per part: norm_parts shared out among the groups, at
+// least one and no more than its rows to each.
 inline size_t norm_bwd_workspace_total(int64_t rows, int64_t cols, int64_t groups) {
   if (norm_shape_status(rows, cols, groups) != SWIGLU_OK) return 0;
-  const int64_t g = groups > 0 ? groups : 1;
-  const size_t n = (size_t)2 * g * norm_per_group(rows, groups) * cols * 4;
+  const int64_t g = groups > 0 ? groups : 1, rpg = rows / g;
+  int64_t per = norm_parts(cols) / g;
+  if (per > rpg) per = rpg;
+  if (per < 1) per = rows > 0 ? 1 : 0;
+  const size_t n = (size_t)2 * g * per * cols * 4;
   return (n + 255) / 256 * 256;
 }
 
