@@ -337,8 +337,8 @@ inline int validate_moe(int64_t T, int64_t E, int64_t k, int64_t N, int64_t K, c
 
 constexpr int64_t kNormMaxCols = 16384;
 // Parts the backward's row sums are split into over all groups (each group
-// has at least one): a part is the walk of one workgroup, whose threads grow
-// with cols, so narrow rows take more of them to fill the chip.
+// has at least one): a part is the walk of one workgroup, which has at least
+// one thread for 8 columns, so narrow rows take more of them to fill the chip.
 constexpr int64_t kNormMinParts = 512, kNormMaxParts = 2048;
 inline int64_t norm_parts(int64_t cols) {
   const int64_t n = (int64_t(1) << 21) / cols;
@@ -352,7 +352,7 @@ inline int norm_shape_status(int64_t rows, int64_t cols, int64_t groups) {
   return SWIGLU_OK;
 }
 
-// Two fp32 sums of [cols] per part: norm_parts shared out among the groups, at
+// Two fp32 sums of [cols] per part: at most norm_parts shared out among the groups, at
 // least one and no more than its rows to each.
 inline size_t norm_bwd_workspace_total(int64_t rows, int64_t cols, int64_t groups) {
   if (norm_shape_status(rows, cols, groups) != SWIGLU_OK) return 0;
