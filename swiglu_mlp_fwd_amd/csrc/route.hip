@@ -21,16 +21,28 @@
 //   sigmoid, renorm   q_j (d_j - m) (1 - s_j),          m = sum_j q_j d_j
 // recomputed from the logits, so nothing but ids is kept between the two.
 //
-// One wave per token: lane l holds logits l, l + 64, ...
+// The work is HBM's for many tokens (the logits, and in the backward their
+// gradients) and latency for few.  kL lanes (8 to 64, so that a lane holds 8
+// or 16 logits) share a token, and a wave takes 64 / kL tokens: a choice is a
+// maximum over a lane's logits and over the lanes, which for up to 16 lanes
+// runs on DPP moves.  With one wave per token and shuffles through LDS, 32768
+// x 128 fp32 took 38 us.
+//
+// Chunks of 16 bytes load at any element's address; the one that would pass
+// the row's end loads from E - kN instead and skips what its neighbour has.
+#include <type_traits>
+
 #include "block.hpp"
 #include "common.hpp"
+#include "swiglu.h"
 
 namespace swg {
 
 namespace {
 
-constexpr int kWavesPerBlock = 4;
+constexpr int kThreads = 256;
 constexpr float kInf = __builtin_inff();
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 // e^-a for a >= 0 to about two ulps; 0 from where it underflows, +inf included.
 __device__ __forceinline__ float exp_neg(float a) {
@@ -40,20 +52,107 @@ __device__ __forceinline__ float exp_neg(float a) {
   return ldexpf(p, n);
 }
 
-__device__ __forceinline__ float load_logit(const float* p) { return *p; }
-__device__ __forceinline__ float load_logit(const bf16* p) { return from_bf16(*p); }
-__device__ __forceinline__ void store_grad(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_grad(bf16* p, float v) { *p = to_bf16(v); }
-
-__device__ __forceinline__ float wave_sum(float v) {
+template <typename T> struct Row;                // elements of a 16-byte chunk
+template <> struct Row<float> {
+  static constexpr int kN = 4;
+  __device__ static float get(const u32x4& w, int i) { return bits_f32(w[i]); }
+  __device__ static float one(const float* p) { return *p; }
+  __device__ static u32x4 pack(const float* v) {
+    return u32x4{f32_bits(v[0]), f32_bits(v[1]), f32_bits(v[2]), f32_bits(v[3])};
+  }
+};
+template <> struct Row<bf16> {
+  static constexpr int kN = 8;
+  __device__ static float get(const u32x4& w, int i) {
+    const uint32_t u = w[i >> 1];
+    return bits_f32((i & 1) ? (u & 0xFFFF0000u) : (u << 16));
+  }
+  __device__ static float one(const bf16* p) { return from_bf16(*p); }
+  __device__ static u32x4 pack(const float* v) {
+    u32x4 w;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+    for (int i = 0; i < 4; ++i)
+      w[i] = (uint32_t)__builtin_bit_cast(uint16_t, to_bf16(v[2 * i])) |
+             ((uint32_t)__builtin_bit_cast(uint16_t, to_bf16(v[2 * i + 1])) << 16);
+    return w;
+  }
+};
+
+// A lane's logits of a row: kC chunks, chunk c * kL + sub of the row.  first[c]
+// is the expert of the chunk's first element and skip[c] how many of its
+// elements another lane has (all of them past the row's end); those read as
+// -infinity.  kTiny: rows shorter than a chunk, all on lane 0.
+template <typename T, int kL, int kC, bool kTiny>
+struct Logits {
+  static constexpr int kN = Row<T>::kN, kV = kC * kN;
+  int first[kC], skip[kC];
+  float v[kV];
+  __device__ __forceinline__ void load(const T* row, int E, int sub) {
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      const int c0 = (c * kL + sub) * kN;
+      if constexpr (kTiny) {
+        first[c] = c0;
+        skip[c] = c0 == 0 ? 0 : kN;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[c * kN + i] = c0 + i < E ? Row<T>::one(row + c0 + i) : -kInf;
+      } else {
+        first[c] = c0 + kN <= E ? c0 : E - kN;
+        skip[c] = c0 - first[c] < kN ? c0 - first[c] : kN;
+        const u32x4 w = *reinterpret_cast<const u32x4_any*>(row + first[c]);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[c * kN + i] = Row<T>::get(w, i);
+      }
+    }
+    if constexpr (!kTiny) {
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+        if (skip[c] != 0) {
+#pragma unroll
+          for (int i = 0; i < kN; ++i)
+            if (i < skip[c]) v[c * kN + i] = -kInf;
+        }
+    }
+  }
+  __device__ __forceinline__ int expert(int i) const { return first[i / kN] + i % kN; }
+  __device__ __forceinline__ void store(T* row, int E, const float (&o)[kV]) const {
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      if (!kTiny && skip[c] == 0) {
+        *reinterpret_cast<u32x4_any*>(row + first[c]) = Row<T>::pack(o + c * kN);
+      } else if (skip[c] < kN) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (i >= skip[c] && first[c] + i < E) row[first[c] + i] = (T)o[c * kN + i];
+      }
+    }
+  }
+};
+
+// Over the kL lanes of a token, the result in each of them.
+template <int kL, typename V, typename F>
+__device__ __forceinline__ V over_lanes(V v, F f) {
+  auto dpp = [](V x, auto ctrl) {
+    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(ctrl)::value, 0xF,
+                                                             0xF, true));
+  };
+  static_assert(kL >= 8, "lanes of a token");
+  v = f(v, dpp(v, std::integral_constant<int, 0xB1>{}));    // quad_perm: lane ^ 1
+  v = f(v, dpp(v, std::integral_constant<int, 0x4E>{}));    // quad_perm: lane ^ 2
+  v = f(v, dpp(v, std::integral_constant<int, 0x141>{}));   // row_half_mirror: the other quad of 8
+  if constexpr (kL >= 16) v = f(v, dpp(v, std::integral_constant<int, 0x140>{}));   // row_mirror: the other 8 of 16
+  if constexpr (kL >= 32) v = f(v, __shfl_xor(v, 16));
+  if constexpr (kL >= 64) v = f(v, __shfl_xor(v, 32));
   return v;
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
-  return v;
+template <int kL> __device__ __forceinline__ float lanes_sum(float v) {
+  return over_lanes<kL>(v, [](float a, float b) { return a + b; });
+}
+template <int kL> __device__ __forceinline__ float lanes_max(float v) {
+  return over_lanes<kL>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int kL> __device__ __forceinline__ int lanes_min(int v) {
+  return over_lanes<kL>(v, [](int a, int b) { return a < b ? a : b; });
 }
 
 // The chosen logits' scores before division and scale (see above).
@@ -69,165 +168,197 @@ __device__ __forceinline__ float chosen_score(float l, float top, bool renorm) {
   }
 }
 
-template <typename T, Score S, int V>
-__global__ __launch_bounds__(kWavesPerBlock * 64) void route_fwd_kernel(RouteArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * kWavesPerBlock + (threadIdx.x >> 6);
-  if (t >= a.T) return;
-  const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.E;
-  float l[V], left[V];
-  bool bad = false;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * 64 + lane;
-    l[v] = e < a.E ? load_logit(row + e) : -kInf;
-    if (l[v] != l[v] || (S == Score::kSoftmax && l[v] == kInf)) bad = true;
-    left[v] = l[v] != l[v] ? -kInf : l[v];
-  }
-  bad = __any(bad);
-  float mine = -kInf;                              // lane j: the j-th choice
-  int my_id = -1;
-  for (int j = 0; j < a.k; ++j) {
-    float best = -kInf;
-    int at = 1 << 30;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (left[v] > best) { best = left[v]; at = v * 64 + lane; }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const float ob = __shfl_xor(best, off);
-      const int oa = __shfl_xor(at, off);
-      if (ob > best || (ob == best && oa < at)) { best = ob; at = oa; }
-    }
-    if (best == -kInf) break;                      // none left
-    if (lane == j) { mine = best; my_id = at; }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (at == v * 64 + lane) left[v] = -kInf;
-  }
-  const float top = __shfl(mine, 0);
-  const bool have = my_id >= 0;
-  float w = have ? chosen_score<S>(mine, top, a.renorm) : 0.0f;
-  float z = 1.0f;
-  if (a.renorm) {
-    z = wave_sum(w);
-  } else if constexpr (S == Score::kSoftmax) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) sum += l[v] == -kInf ? 0.0f : exp_neg(top - l[v]);
-    z = wave_sum(sum);
-  }
-  if (lane < a.k) {
-    w = have ? a.scale * (w / z) : 0.0f;
-    if (bad) w = __builtin_nanf("");
-    a.weights[(int64_t)t * a.k + lane] = w;
-    a.ids[(int64_t)t * a.k + lane] = my_id;
-  }
-}
+// Entry j of a token's choice is held by lane j % kL, slot j / kL.
+template <int kL> constexpr int kSlots = (SWIGLU_MAX_TOPK + kL - 1) / kL;
 
-template <typename T, Score S, int V>
-__global__ __launch_bounds__(kWavesPerBlock * 64) void route_bwd_kernel(RouteArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * kWavesPerBlock + (threadIdx.x >> 6);
-  if (t >= a.T) return;
-  const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.E;
-  T* out = static_cast<T*>(a.dlogits) + (int64_t)t * a.E;
-  float l[V];
-  bool bad = false;
+template <typename T, Score S, int kL, int kC, bool kTiny>
+__global__ __launch_bounds__(kThreads) void route_fwd_kernel(RouteArgs a) {
+  constexpr int kV = Logits<T, kL, kC, kTiny>::kV, kS = kSlots<kL>;
+  const int sub = threadIdx.x % kL;
+  const int64_t token = (int64_t)blockIdx.x * (kThreads / kL) + threadIdx.x / kL;
+  const bool live = token < a.T;
+  const int64_t t = live ? token : a.T - 1;        // lanes past the end repeat the last token and store nothing
+  Logits<T, kL, kC, kTiny> l;
+  l.load(static_cast<const T*>(a.logits) + t * a.E, a.E, sub);
+  float left[kV];
+  int bad = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * 64 + lane;
-    l[v] = e < a.E ? load_logit(row + e) : -kInf;
-    if (l[v] != l[v] || (S == Score::kSoftmax && l[v] == kInf)) bad = true;
+  for (int i = 0; i < kV; ++i) {
+    if (l.v[i] != l.v[i] || (S == Score::kSoftmax && l.v[i] == kInf)) bad = -1;
+    left[i] = l.v[i] != l.v[i] ? -kInf : l.v[i];
   }
-  bad = __any(bad);
-  // Lane j < k: entry j of the token's choice.
-  int id = -1;
-  float d = 0.0f, lk = -kInf;
-  if (lane < a.k) {
-    id = a.ids_in[(int64_t)t * a.k + lane];
-    if (id < 0 || id >= a.E) id = -1;
-    if (id >= 0) lk = load_logit(row + id);
-    if (lk == -kInf) id = -1;                      // masked: no gradient
-    if (id >= 0) d = a.scale * a.dweights[(int64_t)t * a.k + lane];
-  }
-  const bool dense = S == Score::kSoftmax && !a.renorm;
-  float top;
-  if (dense) {
-    top = l[0];
+  bad = lanes_min<kL>(bad);
+  float mine[kS], top = -kInf;
+  int my_id[kS];
 #pragma unroll
-    for (int v = 1; v < V; ++v) top = fmaxf(top, l[v]);
-    top = wave_max(top);
-  } else {
-    top = wave_max(id >= 0 ? lk : -kInf);
+  for (int s = 0; s < kS; ++s) {
+    mine[s] = -kInf;
+    my_id[s] = -1;
   }
-  float q = id >= 0 ? chosen_score<S>(lk, top, a.renorm) : 0.0f;
-  float z = 1.0f;
-  float p[V];
-  if (dense) {
-    float sum = 0.0f;
+  for (int j = 0; j < a.k; ++j) {
+    float best = left[0];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      p[v] = l[v] == -kInf ? 0.0f : exp_neg(top - l[v]);
-      sum += p[v];
-    }
-    z = wave_sum(sum);
-  } else if (a.renorm) {
-    z = wave_sum(q);
-  }
-  if (id >= 0) q = q / z;
-  const float m = (dense || a.renorm) ? wave_sum(q * d) : 0.0f;
-  // This lane's entry, to be added at its expert: the whole gradient, or for
-  // the dense form d_e of p_e (d_e - m).
-  float g = 0.0f;
-  if (id >= 0) {
-    if (dense) {
-      g = d;
-    } else {
-      g = q * (d - m);
-      if constexpr (S == Score::kSigmoid) {
-        float s, c;
-        sigmoid_pair_f32(lk, s, c);
-        g *= c;
+    for (int i = 1; i < kV; ++i) best = fmaxf(best, left[i]);
+    best = lanes_max<kL>(best);
+    int at = 1 << 30;                              // the first expert that has it
+#pragma unroll
+    for (int i = kV - 1; i >= 0; --i)
+      if (left[i] == best) at = min(at, l.expert(i));
+    at = lanes_min<kL>(at);
+    if (j == 0) top = best;
+#pragma unroll
+    for (int s = 0; s < kS; ++s)
+      if (j == s * kL + sub && best != -kInf) {
+        mine[s] = best;
+        my_id[s] = at;
       }
-    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+      if (l.expert(i) == at) left[i] = -kInf;
   }
-  float acc[V];
+  float w[kS], z = 0.0f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int ij = __shfl(id, j);
-    const float gj = __shfl(g, j);
+  for (int s = 0; s < kS; ++s) {
+    w[s] = my_id[s] >= 0 ? chosen_score<S>(mine[s], top, a.renorm) : 0.0f;
+    z += w[s];
+  }
+  if (a.renorm) {
+    z = lanes_sum<kL>(z);
+  } else if constexpr (S == Score::kSoftmax) {
+    z = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (ij == v * 64 + lane) acc[v] += gj;
+    for (int i = 0; i < kV; ++i) z += l.v[i] == -kInf ? 0.0f : exp_neg(top - l.v[i]);
+    z = lanes_sum<kL>(z);
+  } else {
+    z = 1.0f;
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * 64 + lane;
-    if (e >= a.E) continue;
-    float r = acc[v];
-    if (dense) r = p[v] == 0.0f ? 0.0f : (p[v] / z) * (r - m);
-    store_grad(out + e, bad ? __builtin_nanf("") : r);
+  for (int s = 0; s < kS; ++s) {
+    const int j = s * kL + sub;
+    if (!live || j >= a.k) continue;
+    float o = my_id[s] >= 0 ? a.scale * (w[s] / z) : 0.0f;
+    if (bad != 0) o = __builtin_nanf("");
+    a.weights[t * a.k + j] = o;
+    a.ids[t * a.k + j] = my_id[s];
   }
 }
 
+template <typename T, Score S, int kL, int kC, bool kTiny>
+__global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteArgs a) {
+  constexpr int kV = Logits<T, kL, kC, kTiny>::kV, kS = kSlots<kL>;
+  const int sub = threadIdx.x % kL;
+  const int64_t token = (int64_t)blockIdx.x * (kThreads / kL) + threadIdx.x / kL;
+  const bool live = token < a.T;
+  const int64_t t = live ? token : a.T - 1;
+  const T* row = static_cast<const T*>(a.logits) + t * a.E;
+  // Entries of the choice; skipped ones have id -1.
+  int id[kS];
+  float d[kS], lk[kS];
+#pragma unroll
+  for (int s = 0; s < kS; ++s) {
+    const int j = s * kL + sub;
+    id[s] = -1;
+    d[s] = 0.0f;
+    lk[s] = -kInf;
+    if (j < a.k) {
+      id[s] = a.ids_in[t * a.k + j];
+      if (id[s] < 0 || id[s] >= a.E) id[s] = -1;
+      if (id[s] >= 0) lk[s] = Row<T>::one(row + id[s]);
+      if (lk[s] == -kInf) id[s] = -1;              // masked: no gradient
+      if (id[s] >= 0) d[s] = a.scale * a.dweights[t * a.k + j];
+    }
+  }
+  Logits<T, kL, kC, kTiny> l;
+  l.load(row, a.E, sub);
+  int bad = 0;
+#pragma unroll
+  for (int i = 0; i < kV; ++i)
+    if (l.v[i] != l.v[i] || (S == Score::kSoftmax && l.v[i] == kInf)) bad = -1;
+  bad = lanes_min<kL>(bad);
+  const bool dense = S == Score::kSoftmax && !a.renorm;
+  float top = -kInf;
+  if (dense) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) top = fmaxf(top, l.v[i]);
+  } else {
+#pragma unroll
+    for (int s = 0; s < kS; ++s) top = fmaxf(top, id[s] >= 0 ? lk[s] : -kInf);
+  }
+  top = lanes_max<kL>(top);
+  float q[kS], p[kV], z = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kS; ++s) {
+    q[s] = id[s] >= 0 ? chosen_score<S>(lk[s], top, a.renorm) : 0.0f;
+    if (!dense) z += q[s];
+  }
+  if (dense) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      p[i] = l.v[i] == -kInf ? 0.0f : exp_neg(top - l.v[i]);
+      z += p[i];
+    }
+  }
+  z = dense || a.renorm ? lanes_sum<kL>(z) : 1.0f;
+  float m = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kS; ++s) {
+    if (id[s] >= 0) q[s] = q[s] / z;
+    m += q[s] * d[s];
+  }
+  m = dense || a.renorm ? lanes_sum<kL>(m) : 0.0f;
+  // The entry's term, to be added at its expert: the whole gradient, or for
+  // the dense form d_e of p_e (d_e - m).
+  float g[kS];
+#pragma unroll
+  for (int s = 0; s < kS; ++s) {
+    g[s] = dense ? d[s] : q[s] * (d[s] - m);
+    if constexpr (S == Score::kSigmoid) {
+      float sg, c;
+      sigmoid_pair_f32(lk[s], sg, c);
+      g[s] *= c;
+    }
+    if (id[s] < 0) g[s] = 0.0f;
+  }
+  float acc[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kS; ++s)
+    for (int j = s * kL; j < a.k && j < (s + 1) * kL; ++j) {
+      const int ij = __shfl(id[s], j - s * kL, kL);
+      const float gj = __shfl(g[s], j - s * kL, kL);
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        if (ij == l.expert(i)) acc[i] += gj;
+    }
+  const float rz = 1.0f / z;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    if (dense) acc[i] = p[i] == 0.0f ? 0.0f : (p[i] * rz) * (acc[i] - m);
+    if (bad != 0) acc[i] = __builtin_nanf("");
+  }
+  if (live) l.store(static_cast<T*>(a.dlogits) + t * a.E, a.E, acc);
+}
+
+template <typename T, Score S, int kL, int kC, bool kTiny = false>
+hipError_t launch_lanes(bool fwd, const RouteArgs& a, hipStream_t s) {
+  constexpr int per = kThreads / kL;
+  const dim3 grid((unsigned)(((int64_t)a.T + per - 1) / per));
+  if (fwd) hipLaunchKernelGGL((route_fwd_kernel<T, S, kL, kC, kTiny>), grid, dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((route_bwd_kernel<T, S, kL, kC, kTiny>), grid, dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+// 8 logits to a lane: 8 to 64 lanes for up to 512 experts, 16 beyond.
 template <typename T, Score S>
 hipError_t launch_v(bool fwd, const RouteArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.T + kWavesPerBlock - 1) / kWavesPerBlock)), block(kWavesPerBlock * 64);
-#define SWG_ROUTE(V)                                                               \
-  if (a.E <= 64 * V) {                                                             \
-    if (fwd) hipLaunchKernelGGL((route_fwd_kernel<T, S, V>), grid, block, 0, s, a); \
-    else hipLaunchKernelGGL((route_bwd_kernel<T, S, V>), grid, block, 0, s, a);    \
-    return hipGetLastError();                                                      \
-  }
-  SWG_ROUTE(1)
-  SWG_ROUTE(2)
-  SWG_ROUTE(4)
-  SWG_ROUTE(8)
-  SWG_ROUTE(16)
-#undef SWG_ROUTE
-  return hipErrorInvalidValue;
+  constexpr int kN = Row<T>::kN, kC = 8 / kN;
+  if (a.E < kN) return launch_lanes<T, S, 8, 1, true>(fwd, a, s);
+  if (a.E <= 64) return launch_lanes<T, S, 8, kC>(fwd, a, s);
+  if (a.E <= 128) return launch_lanes<T, S, 16, kC>(fwd, a, s);
+  if (a.E <= 256) return launch_lanes<T, S, 32, kC>(fwd, a, s);
+  if (a.E <= 512) return launch_lanes<T, S, 64, kC>(fwd, a, s);
+  return launch_lanes<T, S, 64, 2 * kC>(fwd, a, s);
 }
 
 hipError_t launch(bool fwd, Dt dt, Score score, const RouteArgs& a, hipStream_t s) {
