@@ -358,14 +358,12 @@ int swiglu_moe_fwd(int act, int64_t T, int64_t E, int64_t k, int64_t N, int64_t 
                              workspace, workspace_bytes);
   if (st != SWIGLU_OK || T == 0 || K == 0) return st;
   if (N == 0) return hip_status(fill_zero(SWIGLU_BF16, y, T, K, as_stream(stream)));
-  const swg::MoeLayout L = swg::moe_layout(T, N, K, k);
-  char* ws = static_cast<char*>(workspace);
   swg::MoeArgs a{};
   a.x = x; a.ids = ids; a.weights = weights;
   a.wg = wg; a.wu = wu; a.wd = wd;
   a.wg_stride = wg_stride; a.wu_stride = wu_stride; a.wd_stride = wd_stride;
   a.y = y;
-  a.h_hi = ws + L.off_hi; a.h_lo = ws + L.off_lo; a.part = reinterpret_cast<float*>(ws + L.off_part);
+  a.h = workspace;
   a.T = (int)T; a.E = (int)E; a.k = (int)k; a.N = (int)N; a.K = (int)K;
   return hip_status(swg::launch_moe(static_cast<swg::Act>(act), a, as_stream(stream)));
 }

@@ -32,8 +32,7 @@ struct MoeArgs {
   const void *wg, *wu, *wd; // expert e at + e * stride
   int64_t wg_stride, wu_stride, wd_stride;
   void* y;                  // [T, K] bf16
-  void *h_hi, *h_lo;        // workspace: hidden activations of pair t k + j, [T k, N] bf16 each
-  float* part;              // workspace: expert outputs of the pairs, [T k, K]
+  void* h;                  // workspace: hidden activations of pair t k + j in two parts, [T k, 2, N] bf16
   int T, E, k, N, K;
 };
 hipError_t launch_moe(Act act, const MoeArgs& a, hipStream_t s);

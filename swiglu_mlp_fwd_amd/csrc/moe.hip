@@ -1,23 +1,31 @@
 // The routed SwiGLU MLP for a few tokens (bf16, at most 64):
 //   y[t] = sum_j w[t, j] * Wd_e (act(Wg_e x[t]) * (Wu_e x[t])),  e = ids[t, j].
 //
-// The work is bound by reading the touched experts' weights from HBM once,
-// as the dense decode kernel's (gemv.hip), so both products stream weights
-// the same way: a workgroup owns 16 weight rows of one expert, its 8 waves
-// split the reduction into slabs of 128 and load the weights coalesced
-// (256 contiguous bytes of a row per quarter-wave), pass them through a
-// wave-private LDS tile into the operand layout of v_mfma_f32_16x16x32_bf16,
-// and multiply them with up to 16 kG of the expert's tokens at once; the
-// waves' partial sums meet in LDS and are added in wave order.
+// The work is bound by reading the weights of the experts in use from HBM
+// once, so both kernels stream weights as the dense decode kernel does
+// (gemv.hip): a wave loads a slab of 16 weight rows x 128 coalesced (256
+// contiguous bytes of a row per quarter-wave), passes it through a
+// wave-private LDS tile into the operand layout of v_mfma_f32_16x16x32_bf16
+// and multiplies it with the expert's tokens, up to 16 at a time.  A wave
+// requests its next slab's weights before it multiplies the present one, and
+// that slab's token operands (from L2) after it, into the registers it has
+// just used: loads complete in order, so they arrive with the weights.
 //
-// moe_up:    h of each (token, expert) pair, kept as two bf16 (h = hi + lo,
-//            16 significant bits), the second product's operands.
-// moe_down:  Wd_e (hi + lo), two products into one accumulator, to
-//            part[pair] in fp32.
-// moe_sum:   y = sum_j w_j part, in order of j, rounded once.
+// moe_up_kernel: h = act(Wg_e x) * (Wu_e x) of each (token, expert), kept as
+//   two bf16 rows (h = hi + lo, 16 significant bits: rounding h to one bf16
+//   would cost as much as the rounding of y).  A workgroup takes some 16-row tiles of one expert; its waves
+//   split the reduction and meet in LDS at the end of each tile.
+// moe_down_kernel: y.  A workgroup takes 8 or 16 columns of y over all
+//   experts in use, its waves equal shares of the (expert, slab) sequence;
+//   hi and lo are two of the 16 token columns of one product, 8 tokens at a
+//   time, so they cost no second product; at the end of an expert the two
+//   are added, weighted and added to the wave's own fp32 y in LDS.  The
+//   waves' y are added in wave order: no partial sums leave the workgroup,
+//   no atomics, and one rounding.
 //
-// A grid slice (blockIdx.y) is the slot of an expert in use: every workgroup
-// finds its expert and the pairs that name it from ids (at most 1024).
+// Which experts are in use, and by which tokens, every workgroup finds from
+// ids itself: from up to 64 ids without LDS or barriers (kFew), from up to
+// 1024 through a token mask per expert in LDS.
 #include "block.hpp"
 #include "common.hpp"
 
@@ -25,274 +33,513 @@ namespace swg {
 
 namespace {
 
-constexpr int kWaves = 8;
-constexpr int kThreads = kWaves * 64;
-constexpr int kSlabK = 128;                      // reduction elements per slab
+constexpr int kSlabK = 128;                      // reduction elements per slab of 16 rows
 constexpr int kCPR = kSlabK / 8;                 // 16-byte chunks per row per slab
-constexpr int kRowsPerInst = 64 / kCPR;          // rows one load instruction covers
-constexpr int kInst = 16 / kRowsPerInst;         // load instructions per slab of 16 rows
-constexpr int kSteps = kSlabK / 32;              // MFMA steps per slab
-constexpr int kTile = 16 * kCPR;                 // 16-byte chunks of a slab of 16 rows
-constexpr int kMaxPairs = 64 * 16;
-static_assert(kMaxPairs <= 2 * kThreads, "two ids per thread cover every pair");
+constexpr int kInst = 4;                         // load instructions per slab and weight (1 KiB each)
+constexpr int kSteps = kSlabK / 32;              // MFMA steps per slab of 16 rows
+constexpr int kTile = 256;                       // 16-byte chunks of a slab
+constexpr int kMaxTokens = 64, kMaxPairs = 64 * 16, kMaxExperts = 1024;
 
-// The pairs (t k + j, in increasing order) that name the slot-th expert in
-// use, in order of expert.
-struct Found {
-  uint32_t mask[32];
-  int wave_count[2][kWaves];
-  uint16_t list[kMaxPairs];
+// Waits for this wave's LDS operations and joins the workgroup, without
+// waiting for global loads in flight (__syncthreads waits for those too).
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);            // lgkmcnt(0), other counters free
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ int nth_set_bit(uint64_t m, int n) {
+  int at = 0;
+#pragma unroll
+  for (int half = 32; half >= 1; half >>= 1) {
+    const int c = __popcll(m & ((1ull << half) - 1));
+    if (n >= c) {
+      n -= c;
+      m >>= half;
+      at += half;
+    }
+  }
+  return at;
+}
+
+// The experts in use in a fixed order, and who uses them.  All values are the
+// same in every lane unless said otherwise.
+template <bool kFew> struct Route;
+
+// Up to 64 (token, choice) pairs: lane p holds the id of pair p.
+template <> struct Route<true> {
+  struct Shared {};
+  int id, k, T;
+  uint64_t first;                                // pairs that name an expert as the first
+  __device__ __forceinline__ void init(Shared&, const MoeArgs& a, int tid) {
+    const int lane = tid & 63, pairs = a.T * a.k;
+    k = a.k;
+    T = a.T;
+    id = lane < pairs ? a.ids[lane] : -1;
+    if (id < 0 || id >= a.E) id = -1;
+    uint64_t same = ~0ull;                       // lanes with this lane's id
+#pragma unroll
+    for (int b = 0; b < 10; ++b) {
+      const uint64_t m = __ballot((id >> b) & 1);
+      same &= (id >> b) & 1 ? m : ~m;
+    }
+    same &= __ballot(id >= 0);
+    first = __ballot(id >= 0 && (same & ((1ull << lane) - 1)) == 0);
+  }
+  __device__ __forceinline__ int count() const { return __popcll(first); }
+  // Slots run over the set bits of `first`.
+  struct At { uint64_t rest; };
+  __device__ __forceinline__ At at(int slot) const {
+    return At{first & ~((1ull << nth_set_bit(first, slot)) - 1)};
+  }
+  __device__ __forceinline__ int expert(const At& p) const {
+    return __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)p.rest) - 1);
+  }
+  __device__ __forceinline__ void next(At& p) const { p.rest &= p.rest - 1; }
+  // Tokens that name e.
+  __device__ __forceinline__ uint64_t tokens(int e, int lane) const {
+    const uint64_t pairs = __ballot(id == e);
+    bool in = false;
+    if (lane < T) in = (pairs >> (lane * k) & ((k < 64 ? 1ull << k : 0ull) - 1)) != 0;
+    return __ballot(in);
+  }
+  __device__ __forceinline__ int id_of(int pair) const { return __shfl(id, pair); }
 };
 
-// Returns the expert (-1: fewer than slot + 1 are in use) and sets n.
-__device__ __forceinline__ int find_pairs(Found& f, const int32_t* __restrict__ ids, int pairs, int E, int slot,
-                                          int tid, int& n) {
-  const int lane = tid & 63, wave = tid >> 6;
-  if (tid < 32) f.mask[tid] = 0;
-  __syncthreads();
-  int id[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int p = tid + i * kThreads;
-    id[i] = p < pairs ? ids[p] : -1;
-    if (id[i] >= 0 && id[i] < E) atomicOr(&f.mask[id[i] >> 5], 1u << (id[i] & 31));
-  }
-  __syncthreads();
-  // Every wave: lane w < 32 holds mask word w; the word of the slot-th set bit.
-  uint32_t m = lane < 32 ? f.mask[lane] : 0u;
-  const int c = __popc(m);
-  int before = c;                                // inclusive prefix sum
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up(before, off);
-    if (lane >= off) before += o;
-  }
-  before -= c;
-  const uint64_t has = __ballot(lane < 32 && slot >= before && slot < before + c);
-  if (has == 0) return -1;
-  const int word = __ffsll((unsigned long long)has) - 1;
-  m = __shfl(m, word);
-  for (int i = slot - __shfl(before, word); i > 0; --i) m &= m - 1;
-  const int expert = word * 32 + __ffs(m) - 1;
-  uint64_t hit[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    hit[i] = __ballot(id[i] == expert);
-    if (lane == 0) f.wave_count[i][wave] = __popcll(hit[i]);
-  }
-  __syncthreads();
-  n = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    for (int w = 0; w < kWaves; ++w) {
-      if (w == wave && id[i] == expert)
-        f.list[n + __popcll(hit[i] & ((1ull << lane) - 1))] = (uint16_t)(tid + i * kThreads);
-      n += f.wave_count[i][w];
+template <> struct Route<false> {
+  struct Shared {
+    uint32_t mask[kMaxExperts][2];               // tokens of each expert
+    int ids[kMaxPairs];
+  };
+  const Shared* s;
+  int E;
+  __device__ __forceinline__ void init(Shared& sh, const MoeArgs& a, int tid) {
+    s = &sh;
+    E = a.E;
+    for (int e = tid; e < a.E; e += blockDim.x) sh.mask[e][0] = sh.mask[e][1] = 0;
+    __syncthreads();
+    for (int p = tid; p < a.T * a.k; p += blockDim.x) {
+      const int id = a.ids[p], t = p / a.k;
+      sh.ids[p] = id;
+      if (id >= 0 && id < a.E) atomicOr(&sh.mask[id][t >> 5], 1u << (t & 31));
     }
-  __syncthreads();
-  return expert;
+    __syncthreads();
+  }
+  // Experts base .. base + 63 in use.
+  __device__ __forceinline__ uint64_t used(int base) const {
+    const int e = base + (threadIdx.x & 63);
+    return __ballot(e < E && (s->mask[e][0] | s->mask[e][1]) != 0);
+  }
+  __device__ __forceinline__ int count() const {
+    int n = 0;
+    for (int b = 0; b < E; b += 64) n += __popcll(used(b));
+    return n;
+  }
+  struct At { int base; uint64_t rest; };
+  __device__ __forceinline__ At at(int slot) const {   // slot < count()
+    At p{0, used(0)};
+    int n = __popcll(p.rest);
+    while (slot >= n) {
+      slot -= n;
+      p.base += 64;
+      p.rest = used(p.base);
+      n = __popcll(p.rest);
+    }
+    p.rest &= ~((1ull << nth_set_bit(p.rest, slot)) - 1);
+    return p;
+  }
+  __device__ __forceinline__ int expert(const At& p) const { return p.base + __ffsll((unsigned long long)p.rest) - 1; }
+  __device__ __forceinline__ void next(At& p) const {
+    p.rest &= p.rest - 1;
+    while (p.rest == 0 && p.base + 64 < E) {
+      p.base += 64;
+      p.rest = used(p.base);
+    }
+  }
+  __device__ __forceinline__ uint64_t tokens(int e, int) const {
+    return (uint64_t)s->mask[e][1] << 32 | s->mask[e][0];
+  }
+  __device__ __forceinline__ int id_of(int pair) const { return s->ids[pair]; }
+};
+
+// The token of row r of the expert's list (-1 past its end), and the first
+// pair of that token that names e: h of (token, e) lies in that pair's row.
+__device__ __forceinline__ int token_of(uint64_t tokens, int r) {
+  return r < __popcll(tokens) ? nth_set_bit(tokens, r) : -1;
+}
+template <class R>
+__device__ __forceinline__ int pair_of(const R& route, int t, int e, int k) {
+  int p = -1;
+  for (int j = k - 1; j >= 0; --j) {
+    const int id = route.id_of(t < 0 ? 0 : t * k + j);
+    if (t >= 0 && id == e) p = t * k + j;
+  }
+  return p;
 }
 
-// One pass of 16 rows (n0 ..) of kW weights over the tokens of one group of
-// 16 kG pairs: acc[w][g] in the MFMA's layout, summed over the workgroup's
-// waves, in the registers of wave g (of the waves g < kG).
-//   w4[i]    weight i, row r at w4[i] + r * nch chunks; rows past `rows` read as zero
-//   b4[i]    kB token operands (their products add up), token row r16 of group g
-//            at b4[i] + brow[g] * nch, absent (zero) where brow[g] < 0
-template <int kW, int kB, int kG>
-__device__ __forceinline__ void stream_rows(u32x4* lds, const u32x4* const (&w4)[kW], const u32x4* const (&b4)[kB],
-                                            const int (&brow)[kG], int n0, int rows, int nch, int tid,
-                                            f32x4 (&acc)[kW][kG]) {
-  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nslab = (nch + kCPR - 1) / kCPR;
-  const int s0 = (int)((int64_t)wave * nslab / kWaves), s1 = (int)((int64_t)(wave + 1) * nslab / kWaves);
-  u32x4* tile = lds + wave * kW * kTile;
-  const int lc = lane % kCPR, lr = lane / kCPR;
-  const int r16 = lane & 15, q4 = lane >> 4;
+// kRows weight rows (8 or 16); a slab is 128 * kQ of the reduction,
+// kQ = 16 / kRows.  Load instruction i covers rows 4 i + lane / 16 of the
+// slab's piece i / (kRows / 4).
+template <int kRows> constexpr int kPieces = 16 / kRows;
+
+// Groups of 16 token columns whose operands are held in registers; further
+// ones load as they are used.
+template <int kG> constexpr int kHeld = kG < 2 ? kG : 2;
+
+// The token operands of slab s: this lane's row of b4, zero where brow < 0.
+template <int kQ, int kH, int kG>
+__device__ __forceinline__ void load_tokens(u32x4 (&v)[kH][kSteps * kQ], const u32x4* b4, const int (&brow)[kG],
+                                            int groups, int s, int nch, int lane) {
+#pragma unroll
+  for (int g = 0; g < kH; ++g) {
+    if (g > 0 && g >= groups) break;
+#pragma unroll
+    for (int j = 0; j < kSteps * kQ; ++j) {
+      const int c = s * kQ * kCPR + 4 * j + (lane >> 4);
+      v[g][j] = brow[g] >= 0 && c < nch ? b4[(int64_t)brow[g] * nch + c] : u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+}
+
+// A wave's slab in flight: 4 KiB of each of kW weights.
+template <int kRows, int kW>
+__device__ __forceinline__ void load_slab(u32x4 (&v)[kW][kInst], const u32x4* const (&w4)[kW], int n0, int rows, int s,
+                                          int nch, int lane) {
+  constexpr int kQ = kPieces<kRows>;
   const u32x4 zero = {0u, 0u, 0u, 0u};
+  const int lc = lane % kCPR, lr = lane / kCPR;
 #pragma unroll
-  for (int w = 0; w < kW; ++w)
+  for (int i = 0; i < kInst; ++i) {
+    const int n = n0 + (i % (kRows / 4)) * 4 + lr, c = (s * kQ + i / (kRows / 4)) * kCPR + lc;
+    const bool in = n < rows && c < nch;
+    const int64_t off = in ? (int64_t)n * nch + c : 0;
 #pragma unroll
-    for (int g = 0; g < kG; ++g) acc[w][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = s0; s < s1; ++s) {
-    const int c = s * kCPR + lc;
-    u32x4 v[kW][kInst];
+    for (int w = 0; w < kW; ++w) v[w][i] = in ? __builtin_nontemporal_load(w4[w] + off) : zero;
+  }
+}
+
+// Row r, chunk c of a 16-chunk piece sits at chunk c ^ (r & 15): the 16 lanes
+// that write one row and the 16 that read one chunk of 16 rows each hit 16
+// distinct 16-byte bank groups.
+template <int kRows, int kW>
+__device__ __forceinline__ void to_tile(const u32x4 (&v)[kW][kInst], u32x4* tile, int lane) {
+  const int lc = lane % kCPR, lr = lane / kCPR;
 #pragma unroll
-    for (int i = 0; i < kInst; ++i) {
-      const int n = n0 + i * kRowsPerInst + lr;
-      const bool in = n < rows && c < nch;
-      const int64_t off = in ? (int64_t)n * nch + c : 0;
+  for (int i = 0; i < kInst; ++i) {
+    const int r = (i % (kRows / 4)) * 4 + lr, piece = i / (kRows / 4);
 #pragma unroll
-      for (int w = 0; w < kW; ++w) v[w][i] = in ? __builtin_nontemporal_load(w4[w] + off) : zero;
-    }
-    // Row r, chunk c of a tile sits at chunk c ^ (r & 15): see gemv.hip.
+    for (int w = 0; w < kW; ++w) tile[w * kTile + (piece * kRows + r) * kCPR + (lc ^ r)] = v[w][i];
+  }
+}
+
+// The slab in the tile times the token columns.
+template <int kRows, int kW, int kG, int kH>
+__device__ __forceinline__ void multiply(const u32x4* tile, const u32x4 (&b)[kH][kSteps * kPieces<kRows>],
+                                         const u32x4* b4, const int (&brow)[kG], int groups, int s, int nch, int lane,
+                                         f32x4 (&acc)[kW][kG]) {
+  constexpr int kQ = kPieces<kRows>;
+  const int r16 = lane & 15, q4 = lane >> 4, r = r16 % kRows;
+  // Groups g0, g0 + 1, .. with the operands t, each tile chunk read once.
+  auto product = [&](auto& t, int g0) {
+    constexpr int kT = sizeof(t) / sizeof(t[0]);
 #pragma unroll
-    for (int i = 0; i < kInst; ++i) {
-      const int r = i * kRowsPerInst + lr;
+    for (int j = 0; j < kSteps * kQ; ++j) {
+      const int pc = (4 * (j % kSteps) + q4) ^ r;
+      u32x4 w[kW];
 #pragma unroll
-      for (int w = 0; w < kW; ++w) tile[w * kTile + r * kCPR + (lc ^ r)] = v[w][i];
-    }
+      for (int i = 0; i < kW; ++i) w[i] = tile[i * kTile + ((j / kSteps) * kRows + r) * kCPR + pc];
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      const int pc = (4 * j + q4) ^ r16;
-      const int cb = s * kCPR + 4 * j + q4;
+      for (int g = 0; g < kT; ++g) {
+        if (g > 0 && g0 + g >= groups) break;
 #pragma unroll
-      for (int g = 0; g < kG; ++g) {
-#pragma unroll
-        for (int b = 0; b < kB; ++b) {
-          const bool in = brow[g] >= 0 && cb < nch;
-          const u32x4 xv = in ? b4[b][(int64_t)brow[g] * nch + cb] : zero;
-#pragma unroll
-          for (int w = 0; w < kW; ++w)
-            acc[w][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, tile[w * kTile + r16 * kCPR + pc]), __builtin_bit_cast(bf16x8, xv),
-                acc[w][g], 0, 0, 0);
-        }
+        for (int i = 0; i < kW; ++i)
+          acc[i][g0 + g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, w[i]), __builtin_bit_cast(bf16x8, t[g][j]), acc[i][g0 + g], 0, 0, 0);
       }
     }
+  };
+  product(b, 0);
+#pragma unroll
+  for (int g = kH; g < kG; ++g) {
+    if (g >= groups) break;
+    // One group at a time: several groups' operands, or the tile kept for
+    // them, would spill.
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    u32x4 t[1][kSteps * kQ];
+    const int one[1] = {brow[g]};
+    load_tokens<kQ>(t, b4, one, 1, s, nch, lane);
+    product(t, g);
   }
-  __syncthreads();                               // every wave is done with its tiles
-  f32x4* red = reinterpret_cast<f32x4*>(lds);    // [kW][kG][wave][lane]
-#pragma unroll
-  for (int w = 0; w < kW; ++w)
-#pragma unroll
-    for (int g = 0; g < kG; ++g) red[((w * kG + g) * kWaves + wave) * 64 + lane] = acc[w][g];
-  __syncthreads();
-  if (wave < kG) {
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      f32x4 sum = red[((w * kG + wave) * kWaves) * 64 + lane];
-      for (int o = 1; o < kWaves; ++o) sum += red[((w * kG + wave) * kWaves + o) * 64 + lane];
-      acc[w][0] = sum;
-    }
-  }
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-constexpr size_t lds_bytes(int kW, int kG) {
-  const size_t tiles = (size_t)kWaves * kW * kTile * 16, red = (size_t)kW * kG * kWaves * 64 * 16;
-  return tiles > red ? tiles : red;
-}
+// ---------------------------------------------------------------- first product
 
-// This lane's token rows: token row r16 of group g is entry p0 + 16 g + r16
-// of the list; -1 past its end.
-template <int kG>
-__device__ __forceinline__ void pair_rows(const Found& f, int p0, int n, int r16, int (&pair)[kG]) {
-#pragma unroll
-  for (int g = 0; g < kG; ++g) {
-    const int i = p0 + 16 * g + r16;
-    pair[g] = i < n ? (int)f.list[i] : -1;
-  }
-}
+constexpr int kUpWaves = 8;
 
-template <Act A, int kG>
-__global__ __launch_bounds__(kThreads) void moe_up_kernel(MoeArgs a) {
+template <Act A, bool kFew, int kG>
+__global__ __launch_bounds__(kUpWaves * 64, kG > 2 ? 2 : 4) void moe_up_kernel(MoeArgs a, int tiles) {
   extern __shared__ u32x4 lds[];
-  __shared__ Found found;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int n;
-  const int e = find_pairs(found, a.ids, a.T * a.k, a.E, blockIdx.y, tid, n);
-  if (e < 0) return;
-  const int n0 = blockIdx.x * 16, nch = a.K >> 3;
+  __shared__ typename Route<kFew>::Shared shared;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nw = blockDim.x >> 6, r16 = lane & 15, q4 = lane >> 4;
+  Route<kFew> route;
+  route.init(shared, a, tid);
+  if ((int)blockIdx.y >= route.count()) return;
+  const int e = route.expert(route.at(blockIdx.y));
+  const uint64_t tokens = route.tokens(e, lane);
+  const int groups = (__popcll(tokens) + 15) / 16;
+  int row[kG];
+#pragma unroll
+  for (int g = 0; g < kG; ++g) row[g] = token_of(tokens, 16 * g + r16);
+
+  const int nch = a.K >> 3, nslab = (nch + kCPR - 1) / kCPR;
   const u32x4* const w4[2] = {
       reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wg) + e * a.wg_stride),
       reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wu) + e * a.wu_stride)};
-  const u32x4* const b4[1] = {static_cast<const u32x4*>(a.x)};
-  for (int p0 = 0; p0 < n; p0 += 16 * kG) {
-    int pair[kG], row[kG];
-    pair_rows(found, p0, n, lane & 15, pair);
+  const u32x4* b4 = static_cast<const u32x4*>(a.x);
+  u32x4* tile = lds + wave * 2 * kTile;
+  // Tiles t0, t0 + 1, ... of this workgroup; slabs s0 .. s1 of each for this wave.
+  const int t0 = blockIdx.x * tiles, t1 = min(t0 + tiles, (a.N + 15) / 16);
+  const int s0 = wave * nslab / nw, s1 = (wave + 1) * nslab / nw;
+  f32x4 acc[2][kG];
+  auto clear = [&] {
 #pragma unroll
-    for (int g = 0; g < kG; ++g) row[g] = pair[g] < 0 ? -1 : pair[g] / a.k;
-    f32x4 acc[2][kG];
-    stream_rows<2, 1, kG>(lds, w4, b4, row, n0, a.N, nch, tid, acc);
-    // Lane l element i: weight row n0 + 4 (l / 16) + i of token row l % 16.
-    const int i = p0 + 16 * wave + (lane & 15), nb = n0 + 4 * (lane >> 4);
-    if (wave < kG && i < n && nb < a.N) {        // N % 8 == 0: four columns lie inside or outside together
-      uint16_t hi[4], lo[4];
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float g = acc[0][0][q];
-        const float h = (A == Act::kGeluTanh ? gelu_tanh_f32(g) : silu_f32(g)) * acc[1][0][q];
-        const bf16 b = to_bf16(h);
-        const float f = from_bf16(b);
-        hi[q] = __builtin_bit_cast(uint16_t, b);
-        lo[q] = __builtin_bit_cast(uint16_t, to_bf16(fabsf(f) < __builtin_inff() ? h - f : 0.0f));
-      }
-      const int64_t at = (int64_t)found.list[i] * a.N + nb;
-      *reinterpret_cast<u32x2*>(static_cast<bf16*>(a.h_hi) + at) = __builtin_bit_cast(u32x2, hi);
-      *reinterpret_cast<u32x2*>(static_cast<bf16*>(a.h_lo) + at) = __builtin_bit_cast(u32x2, lo);
+      for (int g = 0; g < kG; ++g) acc[w][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  clear();
+  u32x4 v[2][kInst], b[kHeld<kG>][kSteps];
+  if (t0 < t1 && s0 < s1) {
+    load_slab<16, 2>(v, w4, t0 * 16, a.N, s0, nch, lane);
+    load_tokens<1>(b, b4, row, groups, s0, nch, lane);
+  }
+  for (int t = t0; t < t1; ++t) {
+    for (int s = s0; s < s1; ++s) {
+      to_tile<16, 2>(v, tile, lane);
+      const bool more = s + 1 < s1, any = more || t + 1 < t1;
+      if (any) load_slab<16, 2>(v, w4, (more ? t : t + 1) * 16, a.N, more ? s + 1 : s0, nch, lane);
+      multiply<16, 2, kG>(tile, b, b4, row, groups, s, nch, lane, acc);
+      if (any) load_tokens<1>(b, b4, row, groups, more ? s + 1 : s0, nch, lane);
     }
-    __syncthreads();                             // the sums are read before the next tiles are written
+    // The waves' sums in wave order: group g and weight w by wave 2 g + w % nw.
+    lds_barrier();                               // every wave is done with its tile
+    f32x4* red = reinterpret_cast<f32x4*>(lds);  // [kG][2][wave][lane]
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      if (g >= groups) break;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) red[((g * 2 + w) * nw + wave) * 64 + lane] = acc[w][g];
+    }
+    clear();
+    lds_barrier();
+    for (int g = wave; g < groups; g += nw) {
+      f32x4 sum[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        sum[w] = red[((g * 2 + w) * nw) * 64 + lane];
+        for (int o = 1; o < nw; ++o) sum[w] += red[((g * 2 + w) * nw + o) * 64 + lane];
+      }
+      // Lane l element i: weight row 16 t + 4 (l / 16) + i of token row l % 16.
+      const int tok = token_of(tokens, 16 * g + r16), nb = t * 16 + 4 * q4;
+      const int pair = pair_of(route, tok, e, a.k);
+      if (pair >= 0 && nb < a.N) {               // N % 8 == 0: four columns lie inside or outside together
+        uint16_t hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float z = sum[0][q];
+          const float h = (A == Act::kGeluTanh ? gelu_tanh_f32(z) : silu_f32(z)) * sum[1][q];
+          const bf16 b = to_bf16(h);
+          const float f = from_bf16(b);
+          hi[q] = __builtin_bit_cast(uint16_t, b);
+          lo[q] = __builtin_bit_cast(uint16_t, to_bf16(fabsf(f) < __builtin_inff() ? h - f : 0.0f));
+        }
+        bf16* h = static_cast<bf16*>(a.h) + (int64_t)pair * 2 * a.N + nb;
+        *reinterpret_cast<u32x2*>(h) = __builtin_bit_cast(u32x2, hi);
+        *reinterpret_cast<u32x2*>(h + a.N) = __builtin_bit_cast(u32x2, lo);
+      }
+    }
+    lds_barrier();                               // the sums are read before the next tile is written
   }
 }
 
-template <int kG>
-__global__ __launch_bounds__(kThreads) void moe_down_kernel(MoeArgs a) {
+// --------------------------------------------------------------- second product
+
+// Many token groups need up to 256 registers, and so half the waves.
+template <int kG> constexpr int kDownWaves = kG > 2 ? 8 : 16;
+
+template <bool kFew, int kG, int kRows>
+__global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a) {
+  constexpr int kQ = kPieces<kRows>;
   extern __shared__ u32x4 lds[];
-  __shared__ Found found;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  int n;
-  const int e = find_pairs(found, a.ids, a.T * a.k, a.E, blockIdx.y, tid, n);
-  if (e < 0) return;
-  const int n0 = blockIdx.x * 16, nch = a.N >> 3;
-  const u32x4* const w4[1] = {reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wd) + e * a.wd_stride)};
-  const u32x4* const b4[2] = {static_cast<const u32x4*>(a.h_hi), static_cast<const u32x4*>(a.h_lo)};
-  for (int p0 = 0; p0 < n; p0 += 16 * kG) {
-    int pair[kG];
-    pair_rows(found, p0, n, lane & 15, pair);
+  __shared__ typename Route<kFew>::Shared shared;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nw = blockDim.x >> 6, r16 = lane & 15, q4 = lane >> 4;
+  u32x4* tile = lds + wave * kTile;
+  float* ys = reinterpret_cast<float*>(lds + nw * kTile);   // [wave][T][kRows]
+  for (int i = tid; i < nw * a.T * kRows; i += blockDim.x) ys[i] = 0.0f;
+  Route<kFew> route;
+  route.init(shared, a, tid);
+  __syncthreads();
+  float* mine = ys + wave * a.T * kRows;
+
+  const int n0 = blockIdx.x * kRows, nch = a.N >> 3, nslab = (nch + kQ * kCPR - 1) / (kQ * kCPR);
+  const u32x4* b4 = static_cast<const u32x4*>(a.h);
+  const int r8 = lane & 7, half = r16 >> 3;      // token column r16: token r8 of a group of 8, its hi or lo row
+  // This wave's share of the (expert in use, slab) sequence.
+  const int total = route.count() * nslab;
+  int u = (int)((int64_t)wave * total / nw);
+  const int u1 = (int)((int64_t)(wave + 1) * total / nw);
+  if (u < u1) {
+    auto at = route.at(u / nslab);
+    int s = u % nslab;
+    // The expert being multiplied: its tokens, and this lane's rows of h.
+    int e, groups, row[kG];
+    uint64_t tokens;
+    const u32x4* w4[1];
+    auto enter = [&] {
+      tokens = route.tokens(e, lane);
+      groups = (__popcll(tokens) + 7) / 8;
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        row[g] = -1;
+        if (g < groups) row[g] = pair_of(route, token_of(tokens, 8 * g + r8), e, a.k);
+        if (row[g] >= 0) row[g] = row[g] * 2 + half;
+      }
+    };
+    auto weights_of = [&](int expert) {
+      return reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wd) + expert * a.wd_stride);
+    };
+    e = __builtin_amdgcn_readfirstlane(route.expert(at));
+    w4[0] = weights_of(e);
+    u32x4 v[1][kInst], b[kHeld<kG>][kSteps * kQ];
+    load_slab<kRows, 1>(v, w4, n0, a.K, s, nch, lane);
+    enter();
+    load_tokens<kQ>(b, b4, row, groups, s, nch, lane);
     f32x4 acc[1][kG];
-    stream_rows<1, 2, kG>(lds, w4, b4, pair, n0, a.K, nch, tid, acc);
-    const int i = p0 + 16 * wave + (lane & 15), nb = n0 + 4 * (lane >> 4);
-    if (wave < kG && i < n && nb < a.K)
-      *reinterpret_cast<f32x4*>(a.part + (int64_t)found.list[i] * a.K + nb) = acc[0][0];
-    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < kG; ++g) acc[0][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (; u < u1; ++u) {
+      to_tile<kRows, 1>(v, tile, lane);
+      const bool last = s + 1 == nslab, more = u + 1 < u1;   // of this expert; of this wave
+      int e2 = e;
+      if (more) {
+        if (last) {
+          route.next(at);
+          e2 = __builtin_amdgcn_readfirstlane(route.expert(at));
+          w4[0] = weights_of(e2);
+        }
+        load_slab<kRows, 1>(v, w4, n0, a.K, last ? 0 : s + 1, nch, lane);
+      }
+      multiply<kRows, 1, kG>(tile, b, b4, row, groups, s, nch, lane, acc);
+      ++s;
+      if (last || !more) {                       // weighted, into this wave's y
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          if (g >= groups) break;
+          const int t = token_of(tokens, 8 * g + r8);
+          float w = 0.0f;
+          for (int j = 0; j < a.k; ++j) {
+            const int p = t < 0 ? 0 : t * a.k + j, id = route.id_of(p);
+            if (t >= 0 && id == e) w += a.weights[p];
+          }
+          f32x4 o = acc[0][g];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) o[q] += __shfl_xor(o[q], 8);   // hi + lo
+          // Rows 4 q4 .. + 3 of the tile; with 8 rows the upper half repeats the lower.
+          if (t >= 0 && half == 0 && 4 * q4 < kRows) {
+            f32x4* y = reinterpret_cast<f32x4*>(mine + t * kRows + 4 * q4);
+            f32x4 sum = *y;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum[q] = __builtin_fmaf(w, o[q], sum[q]);
+            *y = sum;
+          }
+          acc[0][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        if (more) {
+          e = e2;
+          s = 0;
+          enter();
+        }
+      }
+      if (more) load_tokens<kQ>(b, b4, row, groups, s, nch, lane);
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < a.T * kRows; i += blockDim.x) {
+    float y = ys[i];
+    for (int w = 1; w < nw; ++w) y += ys[w * a.T * kRows + i];
+    const int t = i / kRows, c = n0 + i % kRows;
+    if (c < a.K) static_cast<bf16*>(a.y)[(int64_t)t * a.K + c] = to_bf16(y);
   }
 }
 
-// Thread: four columns of a token.
-__global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a) {
-  const int c = (blockIdx.x * 256 + threadIdx.x) * 4, t = blockIdx.y;
-  if (c >= a.K) return;
-  f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int j = 0; j < a.k; ++j) {
-    const int p = t * a.k + j, id = a.ids[p];
-    if (id < 0 || id >= a.E) continue;
-    const float w = a.weights[p];
-    const f32x4 v = *reinterpret_cast<const f32x4*>(a.part + (int64_t)p * a.K + c);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) y[q] = __builtin_fmaf(w, v[q], y[q]);
-  }
-  uint16_t o[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) o[q] = __builtin_bit_cast(uint16_t, to_bf16(y[q]));
-  *reinterpret_cast<u32x2*>(static_cast<bf16*>(a.y) + (int64_t)t * a.K + c) = __builtin_bit_cast(u32x2, o);
-}
+// ---------------------------------------------------------------------- launch
 
-template <Act A, int kG>
-hipError_t launch_g(const MoeArgs& a, hipStream_t s) {
-  const unsigned slots = (unsigned)(a.E < a.T * a.k ? a.E : a.T * a.k);
-  constexpr size_t up_lds = lds_bytes(2, kG), down_lds = lds_bytes(1, kG);
-  hipError_t e;
-  if ((e = allow_lds<&moe_up_kernel<A, kG>>(up_lds)) != hipSuccess) return e;
-  if ((e = allow_lds<&moe_down_kernel<kG>>(down_lds)) != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_up_kernel<A, kG>), dim3((a.N + 15) / 16, slots), dim3(kThreads), up_lds, s, a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<kG>), dim3((a.K + 15) / 16, slots), dim3(kThreads), down_lds, s, a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  hipLaunchKernelGGL(moe_sum_kernel, dim3((a.K + 1023) / 1024, a.T), dim3(256), 0, s, a);
+template <Act A, bool kFew, int kG>
+hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
+  const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
+  const int nslab = (a.K / 8 + kCPR - 1) / kCPR, ntiles = (a.N + 15) / 16;
+  int nw = kUpWaves;
+  if (nslab < 4 * kUpWaves) {                    // equal shares where a count from 4 to 8 gives them (see gemv.hip)
+    while (nw > 4 && nslab % nw != 0) --nw;
+    if (nslab % nw != 0) nw = nslab < kUpWaves ? nslab : kUpWaves;
+  }
+  int tiles = (int)(((int64_t)ntiles * slots + 1023) / 1024);
+  if (tiles > 8) tiles = 8;
+  if (tiles < 1) tiles = 1;
+  constexpr size_t most = (size_t)kUpWaves * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);
+  const size_t lds = (size_t)nw * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);   // tiles (8 KiB a wave) or sums (2 kG KiB)
+  const hipError_t e = allow_lds<&moe_up_kernel<A, kFew, kG>>(most);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((moe_up_kernel<A, kFew, kG>), dim3((ntiles + tiles - 1) / tiles, slots), dim3(nw * 64), lds, s, a,
+                     tiles);
   return hipGetLastError();
 }
 
-template <Act A>
-hipError_t launch_a(const MoeArgs& a, hipStream_t s) {
-  if (a.T <= 16) return launch_g<A, 1>(a, s);
-  if (a.T <= 32) return launch_g<A, 2>(a, s);
-  return launch_g<A, 4>(a, s);
+template <bool kFew, int kG, int kRows>
+hipError_t launch_down(const MoeArgs& a, int nw, hipStream_t s) {
+  if (nw > kDownWaves<kG>) nw = kDownWaves<kG>;
+  constexpr size_t most = (size_t)kDownWaves<kG> * (kTile * 16 + 8 * kG * kRows * 4);
+  const size_t lds = (size_t)nw * (kTile * 16 + a.T * kRows * 4);
+  const hipError_t e = allow_lds<&moe_down_kernel<kFew, kG, kRows>>(most);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((moe_down_kernel<kFew, kG, kRows>), dim3((a.K + kRows - 1) / kRows), dim3(nw * 64), lds, s, a);
+  return hipGetLastError();
+}
+
+template <bool kFew, int kG>
+hipError_t launch_up_act(Act act, const MoeArgs& a, hipStream_t s) {
+  return act == Act::kGeluTanh ? launch_up<Act::kGeluTanh, kFew, kG>(a, s) : launch_up<Act::kSilu, kFew, kG>(a, s);
+}
+
+template <bool kFew, int kG>
+hipError_t launch_down_rows(const MoeArgs& a, hipStream_t s) {
+  if (a.K <= 2048) return launch_down<kFew, kG, 8>(a, 16, s);
+  return launch_down<kFew, kG, 16>(a, a.K <= 4096 ? 16 : 8, s);
+}
+
+// Token groups of 16 (first product) and 8 (second) as many as one expert can
+// have.
+template <bool kFew>
+hipError_t launch_few(Act act, const MoeArgs& a, hipStream_t s) {
+  const hipError_t e = a.T <= 16   ? launch_up_act<kFew, 1>(act, a, s)
+                       : a.T <= 32 ? launch_up_act<kFew, 2>(act, a, s)
+                                   : launch_up_act<kFew, 4>(act, a, s);
+  if (e != hipSuccess) return e;
+  if (a.T <= 8) return launch_down_rows<kFew, 1>(a, s);
+  if (a.T <= 16) return launch_down_rows<kFew, 2>(a, s);
+  if (a.T <= 32) return launch_down_rows<kFew, 4>(a, s);
+  return launch_down_rows<kFew, 8>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_moe(Act act, const MoeArgs& a, hipStream_t s) {
-  return act == Act::kGeluTanh ? launch_a<Act::kGeluTanh>(a, s) : launch_a<Act::kSilu>(a, s);
+  return a.T * a.k <= 64 ? launch_few<true>(act, a, s) : launch_few<false>(act, a, s);
 }
 
 }  // namespace swg

@@ -278,13 +278,6 @@ inline int validate_route(int score, int dtype, int64_t T, int64_t E, int64_t k,
   return SWIGLU_OK;
 }
 
-// Workspace of the few-token experts, regions on 256-byte boundaries: the
-// hidden activations' high and low halves [T k, N] bf16 and the expert
-// outputs [T k, K] fp32.
-struct MoeLayout {
-  size_t off_hi, off_lo, off_part, total;
-};
-
 constexpr int64_t kMoeMaxDim = int64_t(1) << 20;
 
 inline int moe_shape_status(int64_t T, int64_t N, int64_t K, int64_t k) {
@@ -295,19 +288,11 @@ inline int moe_shape_status(int64_t T, int64_t N, int64_t K, int64_t k) {
   return SWIGLU_OK;
 }
 
-inline MoeLayout moe_layout(int64_t T, int64_t N, int64_t K, int64_t k) {
-  auto a256 = [](size_t v) { return (v + 255) / 256 * 256; };
-  MoeLayout L;
-  size_t off = 0;
-  L.off_hi = off;   off += a256((size_t)T * k * N * 2);
-  L.off_lo = off;   off += a256((size_t)T * k * N * 2);
-  L.off_part = off; off += a256((size_t)T * k * K * 4);
-  L.total = off;
-  return L;
-}
-
+// Workspace of the few-token experts: the hidden activations in two parts,
+// [T k, 2, N] bf16.
 inline size_t moe_workspace_total(int64_t T, int64_t N, int64_t K, int64_t k) {
-  return moe_shape_status(T, N, K, k) == SWIGLU_OK ? moe_layout(T, N, K, k).total : 0;
+  if (moe_shape_status(T, N, K, k) != SWIGLU_OK) return 0;
+  return ((size_t)T * k * N * 4 + 255) / 256 * 256;
 }
 
 inline int validate_moe(int64_t T, int64_t E, int64_t k, int64_t N, int64_t K, const void* x, const void* ids,
@@ -331,7 +316,7 @@ inline int validate_moe(int64_t T, int64_t E, int64_t k, int64_t N, int64_t K, c
   if ((st = check_ptr(wd))) return st;
   if (ws == nullptr) return SWIGLU_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return SWIGLU_ERR_ALIGN;
-  if (ws_bytes < moe_layout(T, N, K, k).total) return SWIGLU_ERR_WORKSPACE;
+  if (ws_bytes < moe_workspace_total(T, N, K, k)) return SWIGLU_ERR_WORKSPACE;
   return SWIGLU_OK;
 }
 
