@@ -13,8 +13,9 @@
 //
 // moe_up_kernel: h = act(Wg_e x) * (Wu_e x) of each (token, expert), kept as
 //   two bf16 rows (h = hi + lo, 16 significant bits: rounding h to one bf16
-//   would cost as much as the rounding of y).  A workgroup takes some 16-row tiles of one expert; its waves
-//   split the reduction and meet in LDS at the end of each tile.
+//   would cost as much as the rounding of y).  A workgroup takes an equal share of the (expert in
+//   use, 16-row tile) sequence; its waves split the reduction and meet in
+//   LDS at the end of each tile, with the next tile's slab already requested.
 // moe_down_kernel: y.  A workgroup takes 8 or 16 columns of y over all
 //   experts in use, its waves equal shares of the (expert, slab) sequence;
 //   hi and lo are two of the 16 token columns of one product, 8 tokens at a
@@ -278,32 +279,44 @@ __device__ __forceinline__ void multiply(const u32x4* tile, const u32x4 (&b)[kH]
 // ---------------------------------------------------------------- first product
 
 constexpr int kUpWaves = 8;
+// Waves per SIMD: many token groups need up to 256 registers.
+template <int kG> constexpr int kUpOcc = kG > 2 ? 2 : 4;
 
 template <Act A, bool kFew, int kG>
-__global__ __launch_bounds__(kUpWaves * 64, kG > 2 ? 2 : 4) void moe_up_kernel(MoeArgs a, int tiles) {
+__global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeArgs a) {
   extern __shared__ u32x4 lds[];
   __shared__ typename Route<kFew>::Shared shared;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nw = blockDim.x >> 6, r16 = lane & 15, q4 = lane >> 4;
   Route<kFew> route;
   route.init(shared, a, tid);
-  if ((int)blockIdx.y >= route.count()) return;
-  const int e = route.expert(route.at(blockIdx.y));
-  const uint64_t tokens = route.tokens(e, lane);
-  const int groups = (__popcll(tokens) + 15) / 16;
-  int row[kG];
-#pragma unroll
-  for (int g = 0; g < kG; ++g) row[g] = token_of(tokens, 16 * g + r16);
+  // This workgroup's share of the (expert in use, tile) sequence.
+  const int ntiles = (a.N + 15) / 16;
+  const int64_t total = (int64_t)route.count() * ntiles;
+  int64_t u = (int64_t)blockIdx.x * total / gridDim.x;
+  const int64_t u1 = (int64_t)(blockIdx.x + 1) * total / gridDim.x;
+  if (u >= u1) return;
+  auto at = route.at((int)(u / ntiles));
+  int t = (int)(u % ntiles);
 
   const int nch = a.K >> 3, nslab = (nch + kCPR - 1) / kCPR;
-  const u32x4* const w4[2] = {
-      reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wg) + e * a.wg_stride),
-      reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wu) + e * a.wu_stride)};
+  // The expert being multiplied: its tokens, and this lane's rows of x.
+  int e = __builtin_amdgcn_readfirstlane(route.expert(at)), groups, row[kG];
+  uint64_t tokens;
+  auto enter = [&] {
+    tokens = route.tokens(e, lane);
+    groups = (__popcll(tokens) + 15) / 16;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) row[g] = token_of(tokens, 16 * g + r16);
+  };
+  const u32x4* w4[2];                            // of the expert whose slab is in flight
+  auto weights_of = [&](int expert) {
+    w4[0] = reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wg) + expert * a.wg_stride);
+    w4[1] = reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wu) + expert * a.wu_stride);
+  };
   const u32x4* b4 = static_cast<const u32x4*>(a.x);
   u32x4* tile = lds + wave * 2 * kTile;
-  // Tiles t0, t0 + 1, ... of this workgroup; slabs s0 .. s1 of each for this wave.
-  const int t0 = blockIdx.x * tiles, t1 = min(t0 + tiles, (a.N + 15) / 16);
-  const int s0 = wave * nslab / nw, s1 = (wave + 1) * nslab / nw;
+  const int s0 = wave * nslab / nw, s1 = (wave + 1) * nslab / nw;   // slabs of each tile for this wave
   f32x4 acc[2][kG];
   auto clear = [&] {
 #pragma unroll
@@ -312,18 +325,29 @@ __global__ __launch_bounds__(kUpWaves * 64, kG > 2 ? 2 : 4) void moe_up_kernel(M
       for (int g = 0; g < kG; ++g) acc[w][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   };
   clear();
+  weights_of(e);
   u32x4 v[2][kInst], b[kHeld<kG>][kSteps];
-  if (t0 < t1 && s0 < s1) {
-    load_slab<16, 2>(v, w4, t0 * 16, a.N, s0, nch, lane);
-    load_tokens<1>(b, b4, row, groups, s0, nch, lane);
-  }
-  for (int t = t0; t < t1; ++t) {
+  if (s0 < s1) load_slab<16, 2>(v, w4, t * 16, a.N, s0, nch, lane);
+  enter();
+  if (s0 < s1) load_tokens<1>(b, b4, row, groups, s0, nch, lane);
+  for (; u < u1; ++u) {
+    const bool more = u + 1 < u1, other = t + 1 == ntiles;   // another tile; of another expert
+    const int t2 = other ? 0 : t + 1;
+    int e2 = e;
+    if (more && other) {
+      route.next(at);
+      e2 = __builtin_amdgcn_readfirstlane(route.expert(at));
+    }
     for (int s = s0; s < s1; ++s) {
       to_tile<16, 2>(v, tile, lane);
-      const bool more = s + 1 < s1, any = more || t + 1 < t1;
-      if (any) load_slab<16, 2>(v, w4, (more ? t : t + 1) * 16, a.N, more ? s + 1 : s0, nch, lane);
+      if (s + 1 < s1) {
+        load_slab<16, 2>(v, w4, t * 16, a.N, s + 1, nch, lane);
+      } else if (more) {
+        if (other) weights_of(e2);
+        load_slab<16, 2>(v, w4, t2 * 16, a.N, s0, nch, lane);
+      }
       multiply<16, 2, kG>(tile, b, b4, row, groups, s, nch, lane, acc);
-      if (any) load_tokens<1>(b, b4, row, groups, more ? s + 1 : s0, nch, lane);
+      if (s + 1 < s1 || (more && !other)) load_tokens<1>(b, b4, row, groups, s + 1 < s1 ? s + 1 : s0, nch, lane);
     }
     // The waves' sums in wave order: group g and weight w by wave 2 g + w % nw.
     lds_barrier();                               // every wave is done with its tile
@@ -363,6 +387,12 @@ __global__ __launch_bounds__(kUpWaves * 64, kG > 2 ? 2 : 4) void moe_up_kernel(M
       }
     }
     lds_barrier();                               // the sums are read before the next tile is written
+    t = t2;
+    if (more && other) {
+      e = e2;
+      enter();
+      if (s0 < s1) load_tokens<1>(b, b4, row, groups, s0, nch, lane);
+    }
   }
 }
 
@@ -488,15 +518,14 @@ hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
     while (nw > 4 && nslab % nw != 0) --nw;
     if (nslab % nw != 0) nw = nslab < kUpWaves ? nslab : kUpWaves;
   }
-  int tiles = (int)(((int64_t)ntiles * slots + 1023) / 1024);
-  if (tiles > 8) tiles = 8;
-  if (tiles < 1) tiles = 1;
+  // As many workgroups as are resident at once (256 CUs), or as there can be tiles.
+  const int64_t resident = 256 * (4 * kUpOcc<kG> / nw), most_tiles = (int64_t)ntiles * slots;
   constexpr size_t most = (size_t)kUpWaves * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);
   const size_t lds = (size_t)nw * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);   // tiles (8 KiB a wave) or sums (2 kG KiB)
   const hipError_t e = allow_lds<&moe_up_kernel<A, kFew, kG>>(most);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_up_kernel<A, kFew, kG>), dim3((ntiles + tiles - 1) / tiles, slots), dim3(nw * 64), lds, s, a,
-                     tiles);
+  hipLaunchKernelGGL((moe_up_kernel<A, kFew, kG>), dim3((unsigned)(most_tiles < resident ? most_tiles : resident)),
+                     dim3(nw * 64), lds, s, a);
   return hipGetLastError();
 }
 
