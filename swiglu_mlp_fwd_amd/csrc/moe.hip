@@ -64,20 +64,48 @@ __device__ __forceinline__ int nth_set_bit(uint64_t m, int n) {
   return at;
 }
 
-// The experts in use in a fixed order, and who uses them.  All values are the
-// same in every lane unless said otherwise.
-template <bool kFew> struct Route;
+// The sequence of (expert in use, pass) and who uses the expert.  A pass
+// takes at most kCap of an expert's tokens; an expert with more has several,
+// each of which reads its weights again.  All values are the same in every
+// lane unless said otherwise.
+template <bool kFew, int kCap> struct Route;
 
-// Up to 64 (token, choice) pairs: lane p holds the id of pair p.
-template <> struct Route<true> {
+// Passes of n tokens.
+template <int kCap> __device__ __forceinline__ int passes_of(int n) { return (n + kCap - 1) / kCap; }
+
+// A lane's index and what lies before it: of the lanes' counts, the lane
+// where the running sum passes n, and n less the sum before that lane (-1:
+// the counts sum to n or less).  `sum` is their total.
+__device__ __forceinline__ int lane_of(int count, int lane, int& n, int& sum) {
+  int incl = count;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(incl, off);
+    if (lane >= off) incl += o;
+  }
+  sum = __builtin_amdgcn_readlane(incl, 63);
+  const uint64_t past = __ballot(incl > n);
+  if (past == 0) return -1;
+  const int at = __ffsll((unsigned long long)past) - 1;
+  n -= __builtin_amdgcn_readlane(incl - count, at);
+  return at;
+}
+
+// Up to 64 (token, choice) pairs: lane p holds the id of pair p, and, where p
+// is the first pair that names its expert, the expert's passes.
+template <int kCap> struct Route<true, kCap> {
   struct Shared {};
-  int id, k, T;
-  uint64_t first;                                // pairs that name an expert as the first
-  __device__ __forceinline__ void init(Shared&, const MoeArgs& a, int tid) {
-    const int lane = tid & 63, pairs = a.T * a.k;
+  int id, k, T, lane;
+  int passes;                                    // per lane
+  float weight;                                  // per lane: of pair `lane`
+  uint64_t first;                                // lanes with passes
+  __device__ __forceinline__ void init(Shared&, const MoeArgs& a, int tid, bool weights) {
+    const int pairs = a.T * a.k;
+    lane = tid & 63;
     k = a.k;
     T = a.T;
     id = lane < pairs ? a.ids[lane] : -1;
+    weight = weights && lane < pairs ? a.weights[lane] : 0.0f;
     if (id < 0 || id >= a.E) id = -1;
     uint64_t same = ~0ull;                       // lanes with this lane's id
 #pragma unroll
@@ -86,82 +114,106 @@ template <> struct Route<true> {
       same &= (id >> b) & 1 ? m : ~m;
     }
     same &= __ballot(id >= 0);
-    first = __ballot(id >= 0 && (same & ((1ull << lane) - 1)) == 0);
+    const bool is_first = id >= 0 && (same & ((1ull << lane) - 1)) == 0;
+    // Of pairs, not tokens: a token that names an expert twice may add a pass without tokens.
+    passes = is_first ? passes_of<kCap>(__popcll(same)) : 0;
+    first = __ballot(is_first);
   }
-  __device__ __forceinline__ int count() const { return __popcll(first); }
-  // Slots run over the set bits of `first`.
-  struct At { uint64_t rest; };
-  __device__ __forceinline__ At at(int slot) const {
-    return At{first & ~((1ull << nth_set_bit(first, slot)) - 1)};
+  __device__ __forceinline__ int count() const {
+    if (kCap >= kMaxTokens) return __popcll(first);
+    int n = 64 * kMaxTokens, sum;
+    lane_of(passes, lane, n, sum);
+    return sum;
   }
-  __device__ __forceinline__ int expert(const At& p) const {
-    return __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)p.rest) - 1);
+  struct At { int pair, pass; };
+  __device__ __forceinline__ At at(int slot) const {   // slot < count()
+    if (kCap >= kMaxTokens) return At{nth_set_bit(first, slot), 0};
+    int sum;
+    const int p = lane_of(passes, lane, slot, sum);
+    return At{p, slot};
   }
-  __device__ __forceinline__ void next(At& p) const { p.rest &= p.rest - 1; }
+  __device__ __forceinline__ int expert(const At& p) const { return __builtin_amdgcn_readlane(id, p.pair); }
+  __device__ __forceinline__ void next(At& p) const {
+    if (kCap < kMaxTokens && ++p.pass < __builtin_amdgcn_readlane(passes, p.pair)) return;
+    const uint64_t rest = p.pair < 63 ? first >> (p.pair + 1) : 0;
+    p.pair = rest == 0 ? 0 : p.pair + __ffsll((unsigned long long)rest);
+    p.pass = 0;
+  }
   // Tokens that name e.
-  __device__ __forceinline__ uint64_t tokens(int e, int lane) const {
+  __device__ __forceinline__ uint64_t tokens(int e) const {
     const uint64_t pairs = __ballot(id == e);
     bool in = false;
     if (lane < T) in = (pairs >> (lane * k) & ((k < 64 ? 1ull << k : 0ull) - 1)) != 0;
     return __ballot(in);
   }
   __device__ __forceinline__ int id_of(int pair) const { return __shfl(id, pair); }
+  __device__ __forceinline__ float weight_of(int pair) const { return __shfl(weight, pair); }
 };
 
-template <> struct Route<false> {
+template <int kCap> struct Route<false, kCap> {
   struct Shared {
     uint32_t mask[kMaxExperts][2];               // tokens of each expert
     int ids[kMaxPairs];
+    float weights[kMaxPairs];
   };
   const Shared* s;
-  int E;
-  __device__ __forceinline__ void init(Shared& sh, const MoeArgs& a, int tid) {
+  int E, lane;
+  __device__ __forceinline__ void init(Shared& sh, const MoeArgs& a, int tid, bool weights) {
     s = &sh;
     E = a.E;
+    lane = tid & 63;
     for (int e = tid; e < a.E; e += blockDim.x) sh.mask[e][0] = sh.mask[e][1] = 0;
     __syncthreads();
     for (int p = tid; p < a.T * a.k; p += blockDim.x) {
       const int id = a.ids[p], t = p / a.k;
       sh.ids[p] = id;
+      if (weights) sh.weights[p] = a.weights[p];
       if (id >= 0 && id < a.E) atomicOr(&sh.mask[id][t >> 5], 1u << (t & 31));
     }
     __syncthreads();
   }
-  // Experts base .. base + 63 in use.
-  __device__ __forceinline__ uint64_t used(int base) const {
-    const int e = base + (threadIdx.x & 63);
-    return __ballot(e < E && (s->mask[e][0] | s->mask[e][1]) != 0);
+  // Passes of expert base + lane (per lane).
+  __device__ __forceinline__ int passes(int base) const {
+    const int e = base + lane;
+    return e < E ? passes_of<kCap>(__popc(s->mask[e][0]) + __popc(s->mask[e][1])) : 0;
   }
   __device__ __forceinline__ int count() const {
     int n = 0;
-    for (int b = 0; b < E; b += 64) n += __popcll(used(b));
+    for (int b = 0; b < E; b += 64) {
+      int huge = 64 * kMaxTokens, sum;
+      lane_of(passes(b), lane, huge, sum);
+      n += sum;
+    }
     return n;
   }
-  struct At { int base; uint64_t rest; };
+  struct At { int e, pass; };
   __device__ __forceinline__ At at(int slot) const {   // slot < count()
-    At p{0, used(0)};
-    int n = __popcll(p.rest);
-    while (slot >= n) {
-      slot -= n;
-      p.base += 64;
-      p.rest = used(p.base);
-      n = __popcll(p.rest);
+    for (int b = 0;; b += 64) {
+      int sum;
+      const int l = lane_of(passes(b), lane, slot, sum);
+      if (l >= 0) return At{b + l, slot};
+      slot -= sum;
     }
-    p.rest &= ~((1ull << nth_set_bit(p.rest, slot)) - 1);
-    return p;
   }
-  __device__ __forceinline__ int expert(const At& p) const { return p.base + __ffsll((unsigned long long)p.rest) - 1; }
+  __device__ __forceinline__ int expert(const At& p) const { return p.e; }
   __device__ __forceinline__ void next(At& p) const {
-    p.rest &= p.rest - 1;
-    while (p.rest == 0 && p.base + 64 < E) {
-      p.base += 64;
-      p.rest = used(p.base);
+    if (kCap < kMaxTokens && ++p.pass < passes_of<kCap>(__popcll(tokens(p.e)))) return;
+    p.pass = 0;
+    // The next expert with tokens: in the rest of its 64, then 64 at a time.
+    for (int from = p.e + 1; from < E; from = (from & ~63) + 64) {
+      const int base = from & ~63;
+      const uint64_t used = __ballot(passes(base) != 0) >> (from - base);
+      if (used != 0) {
+        p.e = from + __ffsll((unsigned long long)used) - 1;
+        return;
+      }
     }
   }
-  __device__ __forceinline__ uint64_t tokens(int e, int) const {
+  __device__ __forceinline__ uint64_t tokens(int e) const {
     return (uint64_t)s->mask[e][1] << 32 | s->mask[e][0];
   }
   __device__ __forceinline__ int id_of(int pair) const { return s->ids[pair]; }
+  __device__ __forceinline__ float weight_of(int pair) const { return s->weights[pair]; }
 };
 
 // The token of row r of the expert's list (-1 past its end), and the first
@@ -281,16 +333,18 @@ __device__ __forceinline__ void multiply(const u32x4* tile, const u32x4 (&b)[kH]
 constexpr int kUpWaves = 8;
 // Waves per SIMD: many token groups need up to 256 registers.
 template <int kG> constexpr int kUpOcc = kG > 2 ? 2 : 4;
+template <bool kFew, int kG> using UpRoute = Route<kFew, 16 * kG>;
 
 template <Act A, bool kFew, int kG>
 __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeArgs a) {
   extern __shared__ u32x4 lds[];
-  __shared__ typename Route<kFew>::Shared shared;
+  using R = UpRoute<kFew, kG>;
+  __shared__ typename R::Shared shared;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nw = blockDim.x >> 6, r16 = lane & 15, q4 = lane >> 4;
-  Route<kFew> route;
-  route.init(shared, a, tid);
-  // This workgroup's share of the (expert in use, tile) sequence.
+  R route;
+  route.init(shared, a, tid, false);
+  // This workgroup's share of the (pass, tile) sequence.
   const int ntiles = (a.N + 15) / 16;
   const int64_t total = (int64_t)route.count() * ntiles;
   int64_t u = (int64_t)blockIdx.x * total / gridDim.x;
@@ -301,13 +355,14 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
 
   const int nch = a.K >> 3, nslab = (nch + kCPR - 1) / kCPR;
   // The expert being multiplied: its tokens, and this lane's rows of x.
-  int e = __builtin_amdgcn_readfirstlane(route.expert(at)), groups, row[kG];
+  int e = __builtin_amdgcn_readfirstlane(route.expert(at)), first, groups, row[kG];
   uint64_t tokens;
-  auto enter = [&] {
-    tokens = route.tokens(e, lane);
-    groups = (__popcll(tokens) + 15) / 16;
+  auto enter = [&](int pass) {
+    tokens = route.tokens(e);
+    first = pass * 16 * kG;
+    groups = min(kG, (__popcll(tokens) - first + 15) / 16);
 #pragma unroll
-    for (int g = 0; g < kG; ++g) row[g] = token_of(tokens, 16 * g + r16);
+    for (int g = 0; g < kG; ++g) row[g] = token_of(tokens, first + 16 * g + r16);
   };
   const u32x4* w4[2];                            // of the expert whose slab is in flight
   auto weights_of = [&](int expert) {
@@ -328,10 +383,10 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
   weights_of(e);
   u32x4 v[2][kInst], b[kHeld<kG>][kSteps];
   if (s0 < s1) load_slab<16, 2>(v, w4, t * 16, a.N, s0, nch, lane);
-  enter();
+  enter(at.pass);
   if (s0 < s1) load_tokens<1>(b, b4, row, groups, s0, nch, lane);
   for (; u < u1; ++u) {
-    const bool more = u + 1 < u1, other = t + 1 == ntiles;   // another tile; of another expert
+    const bool more = u + 1 < u1, other = t + 1 == ntiles;   // another tile; of another pass
     const int t2 = other ? 0 : t + 1;
     int e2 = e;
     if (more && other) {
@@ -368,7 +423,7 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
         for (int o = 1; o < nw; ++o) sum[w] += red[((g * 2 + w) * nw + o) * 64 + lane];
       }
       // Lane l element i: weight row 16 t + 4 (l / 16) + i of token row l % 16.
-      const int tok = token_of(tokens, 16 * g + r16), nb = t * 16 + 4 * q4;
+      const int tok = token_of(tokens, first + 16 * g + r16), nb = t * 16 + 4 * q4;
       const int pair = pair_of(route, tok, e, a.k);
       if (pair >= 0 && nb < a.N) {               // N % 8 == 0: four columns lie inside or outside together
         uint16_t hi[4], lo[4];
@@ -390,7 +445,7 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
     t = t2;
     if (more && other) {
       e = e2;
-      enter();
+      enter(at.pass);
       if (s0 < s1) load_tokens<1>(b, b4, row, groups, s0, nch, lane);
     }
   }
@@ -399,27 +454,29 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
 // --------------------------------------------------------------- second product
 
 // Many token groups need up to 256 registers, and so half the waves.
-template <int kG> constexpr int kDownWaves = kG > 2 ? 8 : 16;
+template <int kG, int kRows> constexpr int kDownWaves = kG <= 2 || (kG == 4 && kRows == 16) ? 16 : 8;
+template <bool kFew, int kG> using DownRoute = Route<kFew, 8 * kG>;
 
 template <bool kFew, int kG, int kRows>
-__global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(MoeArgs a) {
   constexpr int kQ = kPieces<kRows>;
   extern __shared__ u32x4 lds[];
-  __shared__ typename Route<kFew>::Shared shared;
+  using R = DownRoute<kFew, kG>;
+  __shared__ typename R::Shared shared;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nw = blockDim.x >> 6, r16 = lane & 15, q4 = lane >> 4;
   u32x4* tile = lds + wave * kTile;
   float* ys = reinterpret_cast<float*>(lds + nw * kTile);   // [wave][T][kRows]
   for (int i = tid; i < nw * a.T * kRows; i += blockDim.x) ys[i] = 0.0f;
-  Route<kFew> route;
-  route.init(shared, a, tid);
+  R route;
+  route.init(shared, a, tid, true);
   __syncthreads();
   float* mine = ys + wave * a.T * kRows;
 
   const int n0 = blockIdx.x * kRows, nch = a.N >> 3, nslab = (nch + kQ * kCPR - 1) / (kQ * kCPR);
   const u32x4* b4 = static_cast<const u32x4*>(a.h);
   const int r8 = lane & 7, half = r16 >> 3;      // token column r16: token r8 of a group of 8, its hi or lo row
-  // This wave's share of the (expert in use, slab) sequence.
+  // This wave's share of the (pass, slab) sequence.
   const int total = route.count() * nslab;
   int u = (int)((int64_t)wave * total / nw);
   const int u1 = (int)((int64_t)(wave + 1) * total / nw);
@@ -427,16 +484,17 @@ __global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a
     auto at = route.at(u / nslab);
     int s = u % nslab;
     // The expert being multiplied: its tokens, and this lane's rows of h.
-    int e, groups, row[kG];
+    int e, first, groups, row[kG];
     uint64_t tokens;
     const u32x4* w4[1];
-    auto enter = [&] {
-      tokens = route.tokens(e, lane);
-      groups = (__popcll(tokens) + 7) / 8;
+    auto enter = [&](int pass) {
+      tokens = route.tokens(e);
+      first = pass * 8 * kG;
+      groups = min(kG, (__popcll(tokens) - first + 7) / 8);
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
         row[g] = -1;
-        if (g < groups) row[g] = pair_of(route, token_of(tokens, 8 * g + r8), e, a.k);
+        if (g < groups) row[g] = pair_of(route, token_of(tokens, first + 8 * g + r8), e, a.k);
         if (row[g] >= 0) row[g] = row[g] * 2 + half;
       }
     };
@@ -447,14 +505,14 @@ __global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a
     w4[0] = weights_of(e);
     u32x4 v[1][kInst], b[kHeld<kG>][kSteps * kQ];
     load_slab<kRows, 1>(v, w4, n0, a.K, s, nch, lane);
-    enter();
+    enter(at.pass);
     load_tokens<kQ>(b, b4, row, groups, s, nch, lane);
     f32x4 acc[1][kG];
 #pragma unroll
     for (int g = 0; g < kG; ++g) acc[0][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (; u < u1; ++u) {
       to_tile<kRows, 1>(v, tile, lane);
-      const bool last = s + 1 == nslab, more = u + 1 < u1;   // of this expert; of this wave
+      const bool last = s + 1 == nslab, more = u + 1 < u1;   // of this pass; of this wave
       int e2 = e;
       if (more) {
         if (last) {
@@ -470,11 +528,12 @@ __global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
           if (g >= groups) break;
-          const int t = token_of(tokens, 8 * g + r8);
+          const int t = token_of(tokens, first + 8 * g + r8);
           float w = 0.0f;
           for (int j = 0; j < a.k; ++j) {
-            const int p = t < 0 ? 0 : t * a.k + j, id = route.id_of(p);
-            if (t >= 0 && id == e) w += a.weights[p];
+            const int p = t < 0 ? 0 : t * a.k + j;
+            const float wj = route.weight_of(p);
+            w += route.id_of(p) == e ? wj : 0.0f;
           }
           f32x4 o = acc[0][g];
 #pragma unroll
@@ -492,7 +551,7 @@ __global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a
         if (more) {
           e = e2;
           s = 0;
-          enter();
+          enter(at.pass);
         }
       }
       if (more) load_tokens<kQ>(b, b4, row, groups, s, nch, lane);
@@ -519,6 +578,7 @@ hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
     if (nslab % nw != 0) nw = nslab < kUpWaves ? nslab : kUpWaves;
   }
   // As many workgroups as are resident at once (256 CUs), or as there can be tiles.
+  // (a second pass of an expert lengthens the shares, it adds no workgroups).
   const int64_t resident = 256 * (4 * kUpOcc<kG> / nw), most_tiles = (int64_t)ntiles * slots;
   constexpr size_t most = (size_t)kUpWaves * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);
   const size_t lds = (size_t)nw * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);   // tiles (8 KiB a wave) or sums (2 kG KiB)
@@ -531,8 +591,8 @@ hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
 
 template <bool kFew, int kG, int kRows>
 hipError_t launch_down(const MoeArgs& a, int nw, hipStream_t s) {
-  if (nw > kDownWaves<kG>) nw = kDownWaves<kG>;
-  constexpr size_t most = (size_t)kDownWaves<kG> * (kTile * 16 + 8 * kG * kRows * 4);
+  if (nw > kDownWaves<kG, kRows>) nw = kDownWaves<kG, kRows>;
+  constexpr size_t most = (size_t)kDownWaves<kG, kRows> * (kTile * 16 + 8 * kG * kRows * 4);
   const size_t lds = (size_t)nw * (kTile * 16 + a.T * kRows * 4);
   const hipError_t e = allow_lds<&moe_down_kernel<kFew, kG, kRows>>(most);
   if (e != hipSuccess) return e;
@@ -551,17 +611,19 @@ hipError_t launch_down_rows(const MoeArgs& a, hipStream_t s) {
   return launch_down<kFew, kG, 16>(a, a.K <= 4096 ? 16 : 8, s);
 }
 
-// Token groups of 16 (first product) and 8 (second) as many as one expert can
-// have.
+// Tokens of one expert that a pass takes: all that there can be where T is
+// small, otherwise at least about twice as many as an expert has on average
+// (T k / E), so that few experts need a second pass.
 template <bool kFew>
 hipError_t launch_few(Act act, const MoeArgs& a, hipStream_t s) {
-  const hipError_t e = a.T <= 16   ? launch_up_act<kFew, 1>(act, a, s)
-                       : a.T <= 32 ? launch_up_act<kFew, 2>(act, a, s)
-                                   : launch_up_act<kFew, 4>(act, a, s);
+  const int avg = a.T * a.k / a.E;
+  const hipError_t e = a.T <= 16 || avg <= 8   ? launch_up_act<kFew, 1>(act, a, s)
+                       : a.T <= 32 || avg <= 16 ? launch_up_act<kFew, 2>(act, a, s)
+                                                : launch_up_act<kFew, 4>(act, a, s);
   if (e != hipSuccess) return e;
-  if (a.T <= 8) return launch_down_rows<kFew, 1>(a, s);
-  if (a.T <= 16) return launch_down_rows<kFew, 2>(a, s);
-  if (a.T <= 32) return launch_down_rows<kFew, 4>(a, s);
+  if (a.T <= 8 || avg <= 3) return launch_down_rows<kFew, 1>(a, s);
+  if (a.T <= 16 || avg <= 8) return launch_down_rows<kFew, 2>(a, s);
+  if (a.T <= 32 || avg <= 16) return launch_down_rows<kFew, 4>(a, s);
   return launch_down_rows<kFew, 8>(a, s);
 }
 
