@@ -32,7 +32,7 @@ struct MoeArgs {
   const void *wg, *wu, *wd; // expert e at + e * stride
   int64_t wg_stride, wu_stride, wd_stride;
   void* y;                  // [T, K] bf16
-  void* h;                  // workspace: hidden activations of pair t k + j in two parts, [T k, 2, N] bf16
+  void* h;                  // workspace: hidden activations, 2 T k N bf16 (see moe.hip)
   int T, E, k, N, K;
 };
 hipError_t launch_moe(Act act, const MoeArgs& a, hipStream_t s);

@@ -73,16 +73,21 @@ template <bool kFew, int kCap> struct Route;
 // Passes of n tokens.
 template <int kCap> __device__ __forceinline__ int passes_of(int n) { return (n + kCap - 1) / kCap; }
 
-// A lane's index and what lies before it: of the lanes' counts, the lane
-// where the running sum passes n, and n less the sum before that lane (-1:
-// the counts sum to n or less).  `sum` is their total.
-__device__ __forceinline__ int lane_of(int count, int lane, int& n, int& sum) {
-  int incl = count;
+// Per lane: the sum of v over this lane and those before it.
+__device__ __forceinline__ int running_sum(int v, int lane) {
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(incl, off);
-    if (lane >= off) incl += o;
+    const int o = __shfl_up(v, off);
+    if (lane >= off) v += o;
   }
+  return v;
+}
+
+// Of the lanes' counts, the lane where the running sum passes n, and n less
+// the sum before that lane (-1: the counts sum to n or less).  `sum` is their
+// total.
+__device__ __forceinline__ int lane_of(int count, int lane, int& n, int& sum) {
+  const int incl = running_sum(count, lane);
   sum = __builtin_amdgcn_readlane(incl, 63);
   const uint64_t past = __ballot(incl > n);
   if (past == 0) return -1;
@@ -96,7 +101,7 @@ __device__ __forceinline__ int lane_of(int count, int lane, int& n, int& sum) {
 template <int kCap> struct Route<true, kCap> {
   struct Shared {};
   int id, k, T, lane;
-  int passes;                                    // per lane
+  int passes, before;                            // per lane: of its expert; pairs of the experts before it
   float weight;                                  // per lane: of pair `lane`
   uint64_t first;                                // lanes with passes
   __device__ __forceinline__ void init(Shared&, const MoeArgs& a, int tid, bool weights) {
@@ -118,6 +123,8 @@ template <int kCap> struct Route<true, kCap> {
     // Of pairs, not tokens: a token that names an expert twice may add a pass without tokens.
     passes = is_first ? passes_of<kCap>(__popcll(same)) : 0;
     first = __ballot(is_first);
+    const int n = is_first ? __popcll(same) : 0;
+    before = running_sum(n, lane) - n;
   }
   __device__ __forceinline__ int count() const {
     if (kCap >= kMaxTokens) return __popcll(first);
@@ -133,6 +140,7 @@ template <int kCap> struct Route<true, kCap> {
     return At{p, slot};
   }
   __device__ __forceinline__ int expert(const At& p) const { return __builtin_amdgcn_readlane(id, p.pair); }
+  __device__ __forceinline__ int base(const At& p) const { return __builtin_amdgcn_readlane(before, p.pair); }
   __device__ __forceinline__ void next(At& p) const {
     if (kCap < kMaxTokens && ++p.pass < __builtin_amdgcn_readlane(passes, p.pair)) return;
     const uint64_t rest = p.pair < 63 ? first >> (p.pair + 1) : 0;
@@ -186,19 +194,26 @@ template <int kCap> struct Route<false, kCap> {
     }
     return n;
   }
-  struct At { int e, pass; };
+  struct At { int e, pass, before; };
   __device__ __forceinline__ At at(int slot) const {   // slot < count()
+    int before = 0;                              // tokens of the experts before, expert by expert
     for (int b = 0;; b += 64) {
+      const int e = b + lane, n = e < E ? __popc(s->mask[e][0]) + __popc(s->mask[e][1]) : 0;
+      const int incl = running_sum(n, lane);
       int sum;
       const int l = lane_of(passes(b), lane, slot, sum);
-      if (l >= 0) return At{b + l, slot};
+      if (l >= 0) return At{b + l, slot, before + __builtin_amdgcn_readlane(incl - n, l)};
       slot -= sum;
+      before += __builtin_amdgcn_readlane(incl, 63);
     }
   }
   __device__ __forceinline__ int expert(const At& p) const { return p.e; }
+  __device__ __forceinline__ int base(const At& p) const { return p.before; }
   __device__ __forceinline__ void next(At& p) const {
-    if (kCap < kMaxTokens && ++p.pass < passes_of<kCap>(__popcll(tokens(p.e)))) return;
+    const int n = __popcll(tokens(p.e));
+    if (kCap < kMaxTokens && ++p.pass < passes_of<kCap>(n)) return;
     p.pass = 0;
+    p.before += n;
     // The next expert with tokens: in the rest of its 64, then 64 at a time.
     for (int from = p.e + 1; from < E; from = (from & ~63) + 64) {
       const int base = from & ~63;
@@ -216,19 +231,19 @@ template <int kCap> struct Route<false, kCap> {
   __device__ __forceinline__ float weight_of(int pair) const { return s->weights[pair]; }
 };
 
-// The token of row r of the expert's list (-1 past its end), and the first
-// pair of that token that names e: h of (token, e) lies in that pair's row.
+// The token of row r of the expert's list (-1 past its end).
 __device__ __forceinline__ int token_of(uint64_t tokens, int r) {
   return r < __popcll(tokens) ? nth_set_bit(tokens, r) : -1;
 }
-template <class R>
-__device__ __forceinline__ int pair_of(const R& route, int t, int e, int k) {
-  int p = -1;
-  for (int j = k - 1; j >= 0; --j) {
-    const int id = route.id_of(t < 0 ? 0 : t * k + j);
-    if (t >= 0 && id == e) p = t * k + j;
-  }
-  return p;
+
+// h of row r of an expert's list lies in entry base + r (base: the entries of
+// the experts before it), chunk by chunk with the entries of a chunk side by
+// side, hi then lo: [N / 8][entries][2] chunks of 8.  The 16 token columns of
+// one chunk are then 256 contiguous bytes.  (Entry by entry, [entries][2][N],
+// the 16 columns of N = 1024 lie 2 KiB apart, on two of an L2's 16 channels:
+// 64 tokens of 64 x (1024, 2048) took 37 us longer.)
+__device__ __forceinline__ int64_t h_chunk(int c, int entries, int entry, int half) {
+  return ((int64_t)c * entries + entry) * 2 + half;
 }
 
 // kRows weight rows (8 or 16); a slab is 128 * kQ of the reduction,
@@ -240,9 +255,14 @@ template <int kRows> constexpr int kPieces = 16 / kRows;
 // ones load as they are used.
 template <int kG> constexpr int kHeld = kG < 2 ? kG : 2;
 
-// The token operands of slab s: this lane's row of b4, zero where brow < 0.
+// The token operands of slab s: chunk c of this lane's column g lies at
+// b4[brow[g] * row_step + c * step]; zero where brow[g] < 0.
+struct Tokens {
+  const u32x4* b4;
+  int row_step, step;
+};
 template <int kQ, int kH, int kG>
-__device__ __forceinline__ void load_tokens(u32x4 (&v)[kH][kSteps * kQ], const u32x4* b4, const int (&brow)[kG],
+__device__ __forceinline__ void load_tokens(u32x4 (&v)[kH][kSteps * kQ], const Tokens& x, const int (&brow)[kG],
                                             int groups, int s, int nch, int lane) {
 #pragma unroll
   for (int g = 0; g < kH; ++g) {
@@ -250,7 +270,8 @@ __device__ __forceinline__ void load_tokens(u32x4 (&v)[kH][kSteps * kQ], const u
 #pragma unroll
     for (int j = 0; j < kSteps * kQ; ++j) {
       const int c = s * kQ * kCPR + 4 * j + (lane >> 4);
-      v[g][j] = brow[g] >= 0 && c < nch ? b4[(int64_t)brow[g] * nch + c] : u32x4{0u, 0u, 0u, 0u};
+      v[g][j] = brow[g] >= 0 && c < nch ? x.b4[(int64_t)brow[g] * x.row_step + (int64_t)c * x.step]
+                                        : u32x4{0u, 0u, 0u, 0u};
     }
   }
 }
@@ -289,7 +310,7 @@ __device__ __forceinline__ void to_tile(const u32x4 (&v)[kW][kInst], u32x4* tile
 // The slab in the tile times the token columns.
 template <int kRows, int kW, int kG, int kH>
 __device__ __forceinline__ void multiply(const u32x4* tile, const u32x4 (&b)[kH][kSteps * kPieces<kRows>],
-                                         const u32x4* b4, const int (&brow)[kG], int groups, int s, int nch, int lane,
+                                         const Tokens& x, const int (&brow)[kG], int groups, int s, int nch, int lane,
                                          f32x4 (&acc)[kW][kG]) {
   constexpr int kQ = kPieces<kRows>;
   const int r16 = lane & 15, q4 = lane >> 4, r = r16 % kRows;
@@ -322,7 +343,7 @@ __device__ __forceinline__ void multiply(const u32x4* tile, const u32x4 (&b)[kH]
     __builtin_amdgcn_sched_barrier(0);
     u32x4 t[1][kSteps * kQ];
     const int one[1] = {brow[g]};
-    load_tokens<kQ>(t, b4, one, 1, s, nch, lane);
+    load_tokens<kQ>(t, x, one, 1, s, nch, lane);
     product(t, g);
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -355,11 +376,12 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
 
   const int nch = a.K >> 3, nslab = (nch + kCPR - 1) / kCPR;
   // The expert being multiplied: its tokens, and this lane's rows of x.
-  int e = __builtin_amdgcn_readfirstlane(route.expert(at)), first, groups, row[kG];
+  int e = __builtin_amdgcn_readfirstlane(route.expert(at)), first, base, groups, row[kG];
   uint64_t tokens;
-  auto enter = [&](int pass) {
+  auto enter = [&] {
     tokens = route.tokens(e);
-    first = pass * 16 * kG;
+    first = at.pass * 16 * kG;
+    base = route.base(at);
     groups = min(kG, (__popcll(tokens) - first + 15) / 16);
 #pragma unroll
     for (int g = 0; g < kG; ++g) row[g] = token_of(tokens, first + 16 * g + r16);
@@ -369,7 +391,7 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
     w4[0] = reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wg) + expert * a.wg_stride);
     w4[1] = reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wu) + expert * a.wu_stride);
   };
-  const u32x4* b4 = static_cast<const u32x4*>(a.x);
+  const Tokens x{static_cast<const u32x4*>(a.x), nch, 1};
   u32x4* tile = lds + wave * 2 * kTile;
   const int s0 = wave * nslab / nw, s1 = (wave + 1) * nslab / nw;   // slabs of each tile for this wave
   f32x4 acc[2][kG];
@@ -383,8 +405,8 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
   weights_of(e);
   u32x4 v[2][kInst], b[kHeld<kG>][kSteps];
   if (s0 < s1) load_slab<16, 2>(v, w4, t * 16, a.N, s0, nch, lane);
-  enter(at.pass);
-  if (s0 < s1) load_tokens<1>(b, b4, row, groups, s0, nch, lane);
+  enter();
+  if (s0 < s1) load_tokens<1>(b, x, row, groups, s0, nch, lane);
   for (; u < u1; ++u) {
     const bool more = u + 1 < u1, other = t + 1 == ntiles;   // another tile; of another pass
     const int t2 = other ? 0 : t + 1;
@@ -401,8 +423,8 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
         if (other) weights_of(e2);
         load_slab<16, 2>(v, w4, t2 * 16, a.N, s0, nch, lane);
       }
-      multiply<16, 2, kG>(tile, b, b4, row, groups, s, nch, lane, acc);
-      if (s + 1 < s1 || (more && !other)) load_tokens<1>(b, b4, row, groups, s + 1 < s1 ? s + 1 : s0, nch, lane);
+      multiply<16, 2, kG>(tile, b, x, row, groups, s, nch, lane, acc);
+      if (s + 1 < s1 || (more && !other)) load_tokens<1>(b, x, row, groups, s + 1 < s1 ? s + 1 : s0, nch, lane);
     }
     // The waves' sums in wave order: group g and weight w by wave 2 g + w % nw.
     lds_barrier();                               // every wave is done with its tile
@@ -423,9 +445,8 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
         for (int o = 1; o < nw; ++o) sum[w] += red[((g * 2 + w) * nw + o) * 64 + lane];
       }
       // Lane l element i: weight row 16 t + 4 (l / 16) + i of token row l % 16.
-      const int tok = token_of(tokens, first + 16 * g + r16), nb = t * 16 + 4 * q4;
-      const int pair = pair_of(route, tok, e, a.k);
-      if (pair >= 0 && nb < a.N) {               // N % 8 == 0: four columns lie inside or outside together
+      const int at_row = first + 16 * g + r16, nb = t * 16 + 4 * q4;
+      if (at_row < __popcll(tokens) && nb < a.N) {               // N % 8 == 0: four columns lie inside or outside together
         uint16_t hi[4], lo[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -436,17 +457,17 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
           hi[q] = __builtin_bit_cast(uint16_t, b);
           lo[q] = __builtin_bit_cast(uint16_t, to_bf16(fabsf(f) < __builtin_inff() ? h - f : 0.0f));
         }
-        bf16* h = static_cast<bf16*>(a.h) + (int64_t)pair * 2 * a.N + nb;
+        bf16* h = static_cast<bf16*>(a.h) + h_chunk(nb >> 3, a.T * a.k, base + at_row, 0) * 8 + (nb & 7);
         *reinterpret_cast<u32x2*>(h) = __builtin_bit_cast(u32x2, hi);
-        *reinterpret_cast<u32x2*>(h + a.N) = __builtin_bit_cast(u32x2, lo);
+        *reinterpret_cast<u32x2*>(h + 8) = __builtin_bit_cast(u32x2, lo);
       }
     }
     lds_barrier();                               // the sums are read before the next tile is written
     t = t2;
     if (more && other) {
       e = e2;
-      enter(at.pass);
-      if (s0 < s1) load_tokens<1>(b, b4, row, groups, s0, nch, lane);
+      enter();
+      if (s0 < s1) load_tokens<1>(b, x, row, groups, s0, nch, lane);
     }
   }
 }
@@ -474,7 +495,7 @@ __global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(
   float* mine = ys + wave * a.T * kRows;
 
   const int n0 = blockIdx.x * kRows, nch = a.N >> 3, nslab = (nch + kQ * kCPR - 1) / (kQ * kCPR);
-  const u32x4* b4 = static_cast<const u32x4*>(a.h);
+  const Tokens x{static_cast<const u32x4*>(a.h), 1, 2 * a.T * a.k};
   const int r8 = lane & 7, half = r16 >> 3;      // token column r16: token r8 of a group of 8, its hi or lo row
   // This wave's share of the (pass, slab) sequence.
   const int total = route.count() * nslab;
@@ -483,19 +504,18 @@ __global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(
   if (u < u1) {
     auto at = route.at(u / nslab);
     int s = u % nslab;
-    // The expert being multiplied: its tokens, and this lane's rows of h.
+    // The expert being multiplied: its tokens, and this lane's entries of h.
     int e, first, groups, row[kG];
     uint64_t tokens;
     const u32x4* w4[1];
-    auto enter = [&](int pass) {
+    auto enter = [&] {
       tokens = route.tokens(e);
-      first = pass * 8 * kG;
+      first = at.pass * 8 * kG;
       groups = min(kG, (__popcll(tokens) - first + 7) / 8);
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
-        row[g] = -1;
-        if (g < groups) row[g] = pair_of(route, token_of(tokens, first + 8 * g + r8), e, a.k);
-        if (row[g] >= 0) row[g] = row[g] * 2 + half;
+        const int r = first + 8 * g + r8;
+        row[g] = r < __popcll(tokens) ? (route.base(at) + r) * 2 + half : -1;
       }
     };
     auto weights_of = [&](int expert) {
@@ -505,8 +525,8 @@ __global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(
     w4[0] = weights_of(e);
     u32x4 v[1][kInst], b[kHeld<kG>][kSteps * kQ];
     load_slab<kRows, 1>(v, w4, n0, a.K, s, nch, lane);
-    enter(at.pass);
-    load_tokens<kQ>(b, b4, row, groups, s, nch, lane);
+    enter();
+    load_tokens<kQ>(b, x, row, groups, s, nch, lane);
     f32x4 acc[1][kG];
 #pragma unroll
     for (int g = 0; g < kG; ++g) acc[0][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -522,7 +542,7 @@ __global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(
         }
         load_slab<kRows, 1>(v, w4, n0, a.K, last ? 0 : s + 1, nch, lane);
       }
-      multiply<kRows, 1, kG>(tile, b, b4, row, groups, s, nch, lane, acc);
+      multiply<kRows, 1, kG>(tile, b, x, row, groups, s, nch, lane, acc);
       ++s;
       if (last || !more) {                       // weighted, into this wave's y
 #pragma unroll
@@ -551,10 +571,10 @@ __global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(
         if (more) {
           e = e2;
           s = 0;
-          enter(at.pass);
+          enter();
         }
       }
-      if (more) load_tokens<kQ>(b, b4, row, groups, s, nch, lane);
+      if (more) load_tokens<kQ>(b, x, row, groups, s, nch, lane);
     }
   }
   __syncthreads();

@@ -288,8 +288,8 @@ inline int moe_shape_status(int64_t T, int64_t N, int64_t K, int64_t k) {
   return SWIGLU_OK;
 }
 
-// Workspace of the few-token experts: the hidden activations in two parts,
-// [T k, 2, N] bf16.
+// Workspace of the few-token experts: the hidden activations of T k (token,
+// expert) entries, two bf16 each.
 inline size_t moe_workspace_total(int64_t T, int64_t N, int64_t K, int64_t k) {
   if (moe_shape_status(T, N, K, k) != SWIGLU_OK) return 0;
   return ((size_t)T * k * N * 4 + 255) / 256 * 256;
