@@ -14,9 +14,31 @@ import math
 import torch
 
 from ._lib import MAX_EXPERTS, MAX_TOPK, MOE_MAX_TOKENS, SWIGLU_SCORE_SIGMOID, SWIGLU_SCORE_SOFTMAX, check, lib
-from .ops import _act_code, _check_out, _dtype_code, _on_gpu, _p, _same, _stream
+from .ops import _act_code, _check_out, _dtype_code, _on_gpu, _p, _same
+
+# The current stream's handle: these calls take a few microseconds on the GPU,
+# and torch.cuda.current_stream alone takes two on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 _SCORE = {"softmax": SWIGLU_SCORE_SOFTMAX, "sigmoid": SWIGLU_SCORE_SIGMOID}
+
+
+def _stream(t: torch.Tensor) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _rows(t: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
+    """t as a contiguous [rows, cols]."""
+    if t.dim() == 2 and t.is_contiguous():
+        return t
+    return t.reshape(rows, cols).contiguous()
+
+
+def _lead(t: torch.Tensor, lead, cols: int) -> torch.Tensor:
+    """[rows, cols] back to [*lead, cols]."""
+    return t if len(lead) == 1 else t.reshape(*lead, cols)
 
 
 def _score_code(score: str) -> int:
@@ -52,13 +74,13 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", renorm: bool = T
         _check_out(w, "weights", (T, k), torch.float32, logits.device)
         _check_out(ids, "ids", (T, k), torch.int32, logits.device)
     _on_gpu(logits)
-    l2 = logits.reshape(T, E).contiguous()
+    l2 = _rows(logits, T, E)
     if out is None:
         w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
     check("swiglu_route_fwd", lib().swiglu_route_fwd(sc, int(renorm), dt, T, E, k, _p(l2), float(scale), _p(w),
                                                      _p(ids), _stream(logits)))
-    return w.reshape(*lead, k), ids.reshape(*lead, k)
+    return _lead(w, lead, k), _lead(ids, lead, k)
 
 
 def route_bwd(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
@@ -79,13 +101,11 @@ def route_bwd(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, s
     if out is not None:
         _check_out(out, "out", (T, E), logits.dtype, logits.device)
     _on_gpu(logits)
-    l2 = logits.reshape(T, E).contiguous()
-    i2 = ids.reshape(T, k).contiguous()
-    d2 = dweights.reshape(T, k).contiguous()
+    l2, i2, d2 = _rows(logits, T, E), _rows(ids, T, k), _rows(dweights, T, k)
     d = out if out is not None else torch.empty((T, E), dtype=logits.dtype, device=logits.device)
     check("swiglu_route_bwd", lib().swiglu_route_bwd(sc, int(renorm), dt, T, E, k, _p(l2), float(scale), _p(i2),
                                                      _p(d2), _p(d), _stream(logits)))
-    return d.reshape(*lead, E)
+    return _lead(d, lead, E)
 
 
 def moe_workspace_bytes(T: int, N: int, K: int, k: int) -> int:
@@ -96,10 +116,13 @@ def _expert_weights(t: torch.Tensor, rows: int, cols: int) -> tuple[torch.Tensor
     """Stacked [E, rows, cols] weights and the elements between experts; each
     expert dense, experts apart as the tensor has them (a slice of a stacked
     pair needs no copy)."""
-    if t.shape[0] > 0 and not t[0].is_contiguous() or (t.shape[0] > 1 and t.stride(0) < rows * cols) \
-            or t.stride(0) % 8 != 0:
+    e, r, c = t.stride()
+    one = t.shape[0] <= 1                        # its stride means nothing
+    dense = (c == 1 or cols <= 1) and (r == cols or rows <= 1) and (one or (e >= rows * cols and e % 8 == 0))
+    if not dense:
         t = t.contiguous()
-    return t, (t.stride(0) if t.shape[0] > 1 else rows * cols)
+        e = rows * cols
+    return t, (rows * cols if one else e)
 
 
 def moe_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, wd: torch.Tensor, ids: torch.Tensor,
@@ -121,10 +144,10 @@ def moe_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, wd: torch.Tenso
     if wg.dim() != 3:
         raise ValueError(f"wg must be [E, N, K], got {tuple(wg.shape)}")
     E, N = wg.shape[0], wg.shape[1]
-    if tuple(wg.shape) != (E, N, K) or tuple(wu.shape) != (E, N, K) or tuple(wd.shape) != (E, K, N):
+    if wg.shape != (E, N, K) or wu.shape != (E, N, K) or wd.shape != (E, K, N):
         raise ValueError(f"weights must be [E, N, K], [E, N, K], [E, K, N] with K = {K}, got {tuple(wg.shape)}, "
                          f"{tuple(wu.shape)}, {tuple(wd.shape)}")
-    if ids.dim() < 1 or tuple(ids.shape) != (*lead, ids.shape[-1]) or ids.shape != weights.shape:
+    if ids.dim() < 1 or ids.shape[:-1] != lead or ids.shape != weights.shape:
         raise ValueError(f"ids and weights must be {(*lead, 'k')}, got {tuple(ids.shape)}, {tuple(weights.shape)}")
     k = ids.shape[-1]
     if ids.dtype != torch.int32 or weights.dtype != torch.float32:
@@ -138,9 +161,7 @@ def moe_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, wd: torch.Tenso
     if workspace is not None and (workspace.device != x.device or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the device of x")
     _on_gpu(x)
-    x2 = x.reshape(T, K).contiguous()
-    i2 = ids.reshape(T, k).contiguous()
-    w2 = weights.reshape(T, k).contiguous()
+    x2, i2, w2 = _rows(x, T, K), _rows(ids, T, k), _rows(weights, T, k)
     wg, sg = _expert_weights(wg, N, K)
     wu, su = _expert_weights(wu, N, K)
     wd, sd = _expert_weights(wd, K, N)
@@ -151,7 +172,7 @@ def moe_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, wd: torch.Tenso
     check("swiglu_moe_fwd", lib().swiglu_moe_fwd(_act_code(act), T, E, k, N, K, _p(x2), _p(i2), _p(w2), _p(wg),
                                                  sg, _p(wu), su, _p(wd), sd, _p(y), _p(workspace),
                                                  workspace.numel() * workspace.element_size(), _stream(x)))
-    return y.reshape(*lead, K)
+    return _lead(y, lead, K)
 
 
 def _norm_sizes(like: torch.Tensor, w_out, gate, w_in) -> tuple[int, int, int]:

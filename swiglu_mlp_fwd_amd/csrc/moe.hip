@@ -592,19 +592,27 @@ template <Act A, bool kFew, int kG>
 hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
   const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
   const int nslab = (a.K / 8 + kCPR - 1) / kCPR, ntiles = (a.N + 15) / 16;
-  int nw = kUpWaves;
-  if (nslab < 4 * kUpWaves) {                    // equal shares where a count from 4 to 8 gives them (see gemv.hip)
-    while (nw > 4 && nslab % nw != 0) --nw;
-    if (nslab % nw != 0) nw = nslab < kUpWaves ? nslab : kUpWaves;
+  // As many workgroups as are resident at once (256 CUs), or as there can be
+  // tiles (a second pass of an expert lengthens the shares, it adds no
+  // workgroups).  4 to 8 waves (a slab each at most): those with the shortest
+  // chain of slabs, tiles per workgroup times slabs per wave.  At 2 x 432
+  // tiles of 12 slabs 4 waves (1 x 3) take 19.6 us, 6 (2 x 2) 20.6.
+  const int64_t tiles = (int64_t)ntiles * slots;
+  int nw = 0;
+  int64_t resident = 0, best = 0;
+  for (int n = nslab < kUpWaves ? nslab : kUpWaves; n >= 4 || nw == 0; --n) {
+    const int64_t res = 256 * (4 * kUpOcc<kG> / n), chain = (tiles + res - 1) / res * ((nslab + n - 1) / n);
+    if (nw == 0 || chain < best) {
+      nw = n;
+      resident = res;
+      best = chain;
+    }
   }
-  // As many workgroups as are resident at once (256 CUs), or as there can be tiles.
-  // (a second pass of an expert lengthens the shares, it adds no workgroups).
-  const int64_t resident = 256 * (4 * kUpOcc<kG> / nw), most_tiles = (int64_t)ntiles * slots;
   constexpr size_t most = (size_t)kUpWaves * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);
   const size_t lds = (size_t)nw * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);   // tiles (8 KiB a wave) or sums (2 kG KiB)
   const hipError_t e = allow_lds<&moe_up_kernel<A, kFew, kG>>(most);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_up_kernel<A, kFew, kG>), dim3((unsigned)(most_tiles < resident ? most_tiles : resident)),
+  hipLaunchKernelGGL((moe_up_kernel<A, kFew, kG>), dim3((unsigned)(tiles < resident ? tiles : resident)),
                      dim3(nw * 64), lds, s, a);
   return hipGetLastError();
 }
