@@ -364,6 +364,7 @@ int swiglu_moe_fwd(int act, int64_t T, int64_t E, int64_t k, int64_t N, int64_t 
   a.wg_stride = wg_stride; a.wu_stride = wu_stride; a.wd_stride = wd_stride;
   a.y = y;
   a.h = workspace;
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + swg::moe_layout(T, N, K, k).off_part);
   a.T = (int)T; a.E = (int)E; a.k = (int)k; a.N = (int)N; a.K = (int)K;
   return hip_status(swg::launch_moe(static_cast<swg::Act>(act), a, as_stream(stream)));
 }

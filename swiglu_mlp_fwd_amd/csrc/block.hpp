@@ -33,6 +33,7 @@ struct MoeArgs {
   int64_t wg_stride, wu_stride, wd_stride;
   void* y;                  // [T, K] bf16
   void* h;                  // workspace: hidden activations, 2 T k N bf16 (see moe.hip)
+  float* part;              // workspace: parts of y, [parts, T, K]
   int T, E, k, N, K;
 };
 hipError_t launch_moe(Act act, const MoeArgs& a, hipStream_t s);

@@ -17,18 +17,21 @@
 //   use, 16-row tile) sequence; its waves split the reduction and meet in
 //   LDS at the end of each tile, with the next tile's slab already requested.
 // moe_down_kernel: y.  A workgroup takes 8 or 16 columns of y over all
-//   experts in use, its waves equal shares of the (expert, slab) sequence;
+//   experts in use (or, where that leaves CUs without work, over one of S
+//   equal parts), its waves equal shares of the (expert, slab) sequence;
 //   hi and lo are two of the 16 token columns of one product, 8 tokens at a
 //   time, so they cost no second product; at the end of an expert the two
 //   are added, weighted and added to the wave's own fp32 y in LDS.  The
-//   waves' y are added in wave order: no partial sums leave the workgroup,
-//   no atomics, and one rounding.
+//   waves' y are added in wave order.  Only with S > 1 do partial sums leave
+//   the workgroup, for moe_sum_kernel to add in order.  No atomics, and one
+//   rounding.
 //
 // Which experts are in use, and by which tokens, every workgroup finds from
 // ids itself: from up to 64 ids without LDS or barriers (kFew), from up to
 // 1024 through a token mask per expert in LDS.
 #include "block.hpp"
 #include "common.hpp"
+#include "validate.hpp"
 
 namespace swg {
 
@@ -276,21 +279,28 @@ __device__ __forceinline__ void load_tokens(u32x4 (&v)[kH][kSteps * kQ], const T
   }
 }
 
-// A wave's slab in flight: 4 KiB of each of kW weights.
+// A wave's slab in flight: 4 KiB of each of kW weights.  Rows of whole
+// 128-byte lines are read once and bypass the caches; in others neighbouring
+// slabs share a line, which the bypass would read from HBM twice (1.4 times
+// the bytes at K = 1160).
 template <int kRows, int kW>
 __device__ __forceinline__ void load_slab(u32x4 (&v)[kW][kInst], const u32x4* const (&w4)[kW], int n0, int rows, int s,
                                           int nch, int lane) {
   constexpr int kQ = kPieces<kRows>;
   const u32x4 zero = {0u, 0u, 0u, 0u};
   const int lc = lane % kCPR, lr = lane / kCPR;
+  auto load = [&](auto get) {
 #pragma unroll
-  for (int i = 0; i < kInst; ++i) {
-    const int n = n0 + (i % (kRows / 4)) * 4 + lr, c = (s * kQ + i / (kRows / 4)) * kCPR + lc;
-    const bool in = n < rows && c < nch;
-    const int64_t off = in ? (int64_t)n * nch + c : 0;
+    for (int i = 0; i < kInst; ++i) {
+      const int n = n0 + (i % (kRows / 4)) * 4 + lr, c = (s * kQ + i / (kRows / 4)) * kCPR + lc;
+      const bool in = n < rows && c < nch;
+      const int64_t off = in ? (int64_t)n * nch + c : 0;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) v[w][i] = in ? __builtin_nontemporal_load(w4[w] + off) : zero;
-  }
+      for (int w = 0; w < kW; ++w) v[w][i] = in ? get(w4[w] + off) : zero;
+    }
+  };
+  if (nch % 8 == 0) load([](const u32x4* p) { return __builtin_nontemporal_load(p); });
+  else load([](const u32x4* p) { return *p; });
 }
 
 // Row r, chunk c of a 16-chunk piece sits at chunk c ^ (r & 15): the 16 lanes
@@ -497,10 +507,12 @@ __global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(
   const int n0 = blockIdx.x * kRows, nch = a.N >> 3, nslab = (nch + kQ * kCPR - 1) / (kQ * kCPR);
   const Tokens x{static_cast<const u32x4*>(a.h), 1, 2 * a.T * a.k};
   const int r8 = lane & 7, half = r16 >> 3;      // token column r16: token r8 of a group of 8, its hi or lo row
-  // This wave's share of the (pass, slab) sequence.
+  // This wave's share of this workgroup's part of the (pass, slab) sequence.
   const int total = route.count() * nslab;
-  int u = (int)((int64_t)wave * total / nw);
-  const int u1 = (int)((int64_t)(wave + 1) * total / nw);
+  const int p0 = (int)((int64_t)blockIdx.y * total / gridDim.y);
+  const int p1 = (int)((int64_t)(blockIdx.y + 1) * total / gridDim.y);
+  int u = p0 + (int)((int64_t)wave * (p1 - p0) / nw);
+  const int u1 = p0 + (int)((int64_t)(wave + 1) * (p1 - p0) / nw);
   if (u < u1) {
     auto at = route.at(u / nslab);
     int s = u % nslab;
@@ -582,8 +594,22 @@ __global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(
     float y = ys[i];
     for (int w = 1; w < nw; ++w) y += ys[w * a.T * kRows + i];
     const int t = i / kRows, c = n0 + i % kRows;
-    if (c < a.K) static_cast<bf16*>(a.y)[(int64_t)t * a.K + c] = to_bf16(y);
+    if (c >= a.K) continue;
+    if (gridDim.y == 1) static_cast<bf16*>(a.y)[(int64_t)t * a.K + c] = to_bf16(y);
+    else a.part[((int64_t)blockIdx.y * a.T + t) * a.K + c] = y;
   }
+}
+
+// y from the S parts, four columns to a thread (K % 8 == 0).
+__global__ __launch_bounds__(256) void moe_sum_kernel(MoeArgs a, int parts) {
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4, n = a.T * a.K;
+  if (i >= n) return;
+  f32x4 y = *reinterpret_cast<const f32x4*>(a.part + i);
+  for (int p = 1; p < parts; ++p) y += *reinterpret_cast<const f32x4*>(a.part + (int64_t)p * n + i);
+  uint16_t o[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) o[q] = __builtin_bit_cast(uint16_t, to_bf16(y[q]));
+  *reinterpret_cast<u32x2*>(static_cast<bf16*>(a.y) + i) = __builtin_bit_cast(u32x2, o);
 }
 
 // ---------------------------------------------------------------------- launch
@@ -618,13 +644,27 @@ hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
 }
 
 template <bool kFew, int kG, int kRows>
-hipError_t launch_down(const MoeArgs& a, int nw, hipStream_t s) {
-  if (nw > kDownWaves<kG, kRows>) nw = kDownWaves<kG, kRows>;
-  constexpr size_t most = (size_t)kDownWaves<kG, kRows> * (kTile * 16 + 8 * kG * kRows * 4);
+hipError_t launch_down(const MoeArgs& a, hipStream_t s) {
+  constexpr int kMost = kDownWaves<kG, kRows>;
+  const int blocks = (a.K + kRows - 1) / kRows;
+  // 16 waves (8 where the registers allow no more); 8 and two workgroups per
+  // CU where there are enough of them.
+  const int nw = blocks > 256 ? 8 : kMost;
+  // Parts: at most as many as give every wave a slab.
+  int parts = 1;
+  if (kRows == 16) {
+    const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
+    const int64_t units = (int64_t)slots * ((a.N / 8 + kCPR - 1) / kCPR), most_parts = units / nw;
+    parts = (int)moe_parts(a.K);
+    if (parts > most_parts) parts = most_parts > 1 ? (int)most_parts : 1;
+  }
+  constexpr size_t most = (size_t)kMost * (kTile * 16 + kMaxTokens * kRows * 4);
   const size_t lds = (size_t)nw * (kTile * 16 + a.T * kRows * 4);
-  const hipError_t e = allow_lds<&moe_down_kernel<kFew, kG, kRows>>(most);
+  hipError_t e = allow_lds<&moe_down_kernel<kFew, kG, kRows>>(most);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<kFew, kG, kRows>), dim3((a.K + kRows - 1) / kRows), dim3(nw * 64), lds, s, a);
+  hipLaunchKernelGGL((moe_down_kernel<kFew, kG, kRows>), dim3(blocks, parts), dim3(nw * 64), lds, s, a);
+  if ((e = hipGetLastError()) != hipSuccess || parts == 1) return e;
+  hipLaunchKernelGGL(moe_sum_kernel, dim3((a.T * a.K / 4 + 255) / 256), dim3(256), 0, s, a, parts);
   return hipGetLastError();
 }
 
@@ -633,10 +673,14 @@ hipError_t launch_up_act(Act act, const MoeArgs& a, hipStream_t s) {
   return act == Act::kGeluTanh ? launch_up<Act::kGeluTanh, kFew, kG>(a, s) : launch_up<Act::kSilu, kFew, kG>(a, s);
 }
 
+// 16 columns of y to a workgroup; 8 where 16 would need a split and 8 do not,
+// if the tokens are few: a slab of 8 rows takes the token operands of twice
+// the reduction.  At K = 2048 with 2 tokens per expert 46 us (8 columns)
+// against 49 (16, with the sum of the parts), with 8 tokens 77 against 66.
 template <bool kFew, int kG>
 hipError_t launch_down_rows(const MoeArgs& a, hipStream_t s) {
-  if (a.K <= 2048) return launch_down<kFew, kG, 8>(a, 16, s);
-  return launch_down<kFew, kG, 16>(a, a.K <= 4096 ? 16 : 8, s);
+  if (moe_parts(a.K) > 1 && a.K > 8 * kMoeFullBlocks && a.T * a.k < 4 * a.E) return launch_down<kFew, kG, 8>(a, s);
+  return launch_down<kFew, kG, 16>(a, s);
 }
 
 // Tokens of one expert that a pass takes: all that there can be where T is

@@ -288,11 +288,30 @@ inline int moe_shape_status(int64_t T, int64_t N, int64_t K, int64_t k) {
   return SWIGLU_OK;
 }
 
-// Workspace of the few-token experts: the hidden activations of T k (token,
-// expert) entries, two bf16 each.
+// Parts that the second product's reduction is split into where its 16-column
+// tiles leave many of the 256 CUs without a workgroup.
+constexpr int64_t kMoeFullBlocks = 160;
+inline int64_t moe_parts(int64_t K) {
+  const int64_t blocks = (K + 15) / 16;
+  return blocks == 0 || blocks > kMoeFullBlocks ? 1 : (256 + blocks - 1) / blocks;
+}
+
+// Workspace of the few-token experts, regions on 256-byte boundaries: the
+// hidden activations of T k (token, expert) entries, two bf16 each, and the
+// parts of y in fp32.
+struct MoeLayout {
+  size_t off_part, total;
+};
+inline MoeLayout moe_layout(int64_t T, int64_t N, int64_t K, int64_t k) {
+  auto a256 = [](size_t v) { return (v + 255) / 256 * 256; };
+  const int64_t parts = moe_parts(K);
+  MoeLayout L;
+  L.off_part = a256((size_t)T * k * N * 4);
+  L.total = L.off_part + (parts > 1 ? a256((size_t)parts * T * K * 4) : 0);
+  return L;
+}
 inline size_t moe_workspace_total(int64_t T, int64_t N, int64_t K, int64_t k) {
-  if (moe_shape_status(T, N, K, k) != SWIGLU_OK) return 0;
-  return ((size_t)T * k * N * 4 + 255) / 256 * 256;
+  return moe_shape_status(T, N, K, k) == SWIGLU_OK ? moe_layout(T, N, K, k).total : 0;
 }
 
 inline int validate_moe(int64_t T, int64_t E, int64_t k, int64_t N, int64_t K, const void* x, const void* ids,
