@@ -254,21 +254,17 @@ __device__ __forceinline__ int64_t h_chunk(int c, int entries, int entry, int ha
 // slab's piece i / (kRows / 4).
 template <int kRows> constexpr int kPieces = 16 / kRows;
 
-// Groups of 16 token columns whose operands are held in registers; further
-// ones load as they are used.
-template <int kG> constexpr int kHeld = kG < 2 ? kG : 2;
-
 // The token operands of slab s: chunk c of this lane's column g lies at
 // b4[brow[g] * row_step + c * step]; zero where brow[g] < 0.
 struct Tokens {
   const u32x4* b4;
   int row_step, step;
 };
-template <int kQ, int kH, int kG>
-__device__ __forceinline__ void load_tokens(u32x4 (&v)[kH][kSteps * kQ], const Tokens& x, const int (&brow)[kG],
+template <int kQ, int kG>
+__device__ __forceinline__ void load_tokens(u32x4 (&v)[kG][kSteps * kQ], const Tokens& x, const int (&brow)[kG],
                                             int groups, int s, int nch, int lane) {
 #pragma unroll
-  for (int g = 0; g < kH; ++g) {
+  for (int g = 0; g < kG; ++g) {
     if (g > 0 && g >= groups) break;
 #pragma unroll
     for (int j = 0; j < kSteps * kQ; ++j) {
@@ -318,52 +314,32 @@ __device__ __forceinline__ void to_tile(const u32x4 (&v)[kW][kInst], u32x4* tile
 }
 
 // The slab in the tile times the token columns.
-template <int kRows, int kW, int kG, int kH>
-__device__ __forceinline__ void multiply(const u32x4* tile, const u32x4 (&b)[kH][kSteps * kPieces<kRows>],
-                                         const Tokens& x, const int (&brow)[kG], int groups, int s, int nch, int lane,
-                                         f32x4 (&acc)[kW][kG]) {
-  constexpr int kQ = kPieces<kRows>;
-  const int r16 = lane & 15, q4 = lane >> 4, r = r16 % kRows;
-  // Groups g0, g0 + 1, .. with the operands t, each tile chunk read once.
-  auto product = [&](auto& t, int g0) {
-    constexpr int kT = sizeof(t) / sizeof(t[0]);
+template <int kRows, int kW, int kG>
+__device__ __forceinline__ void multiply(const u32x4* tile, const u32x4 (&b)[kG][kSteps * kPieces<kRows>], int groups,
+                                         int lane, f32x4 (&acc)[kW][kG]) {
+  const int r = (lane & 15) % kRows, q4 = lane >> 4;
 #pragma unroll
-    for (int j = 0; j < kSteps * kQ; ++j) {
-      const int pc = (4 * (j % kSteps) + q4) ^ r;
-      u32x4 w[kW];
+  for (int j = 0; j < kSteps * kPieces<kRows>; ++j) {
+    const int pc = (4 * (j % kSteps) + q4) ^ r;
+    u32x4 w[kW];
 #pragma unroll
-      for (int i = 0; i < kW; ++i) w[i] = tile[i * kTile + ((j / kSteps) * kRows + r) * kCPR + pc];
+    for (int i = 0; i < kW; ++i) w[i] = tile[i * kTile + ((j / kSteps) * kRows + r) * kCPR + pc];
 #pragma unroll
-      for (int g = 0; g < kT; ++g) {
-        if (g > 0 && g0 + g >= groups) break;
+    for (int g = 0; g < kG; ++g) {
+      if (g > 0 && g >= groups) break;
 #pragma unroll
-        for (int i = 0; i < kW; ++i)
-          acc[i][g0 + g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, w[i]), __builtin_bit_cast(bf16x8, t[g][j]), acc[i][g0 + g], 0, 0, 0);
-      }
+      for (int i = 0; i < kW; ++i)
+        acc[i][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i]),
+                                                            __builtin_bit_cast(bf16x8, b[g][j]), acc[i][g], 0, 0, 0);
     }
-  };
-  product(b, 0);
-#pragma unroll
-  for (int g = kH; g < kG; ++g) {
-    if (g >= groups) break;
-    // One group at a time: several groups' operands, or the tile kept for
-    // them, would spill.
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    u32x4 t[1][kSteps * kQ];
-    const int one[1] = {brow[g]};
-    load_tokens<kQ>(t, x, one, 1, s, nch, lane);
-    product(t, g);
   }
-  __builtin_amdgcn_sched_barrier(0);
 }
 
 // ---------------------------------------------------------------- first product
 
 constexpr int kUpWaves = 8;
-// Waves per SIMD: many token groups need up to 256 registers.
-template <int kG> constexpr int kUpOcc = kG > 2 ? 2 : 4;
+// Waves per SIMD: the operands of more token groups take more registers.
+template <int kG> constexpr int kUpOcc = kG == 1 ? 4 : kG == 2 ? 3 : 2;
 template <bool kFew, int kG> using UpRoute = Route<kFew, 16 * kG>;
 
 template <Act A, bool kFew, int kG>
@@ -413,7 +389,7 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
   };
   clear();
   weights_of(e);
-  u32x4 v[2][kInst], b[kHeld<kG>][kSteps];
+  u32x4 v[2][kInst], b[kG][kSteps];
   if (s0 < s1) load_slab<16, 2>(v, w4, t * 16, a.N, s0, nch, lane);
   enter();
   if (s0 < s1) load_tokens<1>(b, x, row, groups, s0, nch, lane);
@@ -433,7 +409,7 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
         if (other) weights_of(e2);
         load_slab<16, 2>(v, w4, t2 * 16, a.N, s0, nch, lane);
       }
-      multiply<16, 2, kG>(tile, b, x, row, groups, s, nch, lane, acc);
+      multiply<16, 2, kG>(tile, b, groups, lane, acc);
       if (s + 1 < s1 || (more && !other)) load_tokens<1>(b, x, row, groups, s + 1 < s1 ? s + 1 : s0, nch, lane);
     }
     // The waves' sums in wave order: group g and weight w by wave 2 g + w % nw.
@@ -484,12 +460,12 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
 
 // --------------------------------------------------------------- second product
 
-// Many token groups need up to 256 registers, and so half the waves.
-template <int kG, int kRows> constexpr int kDownWaves = kG <= 2 || (kG == 4 && kRows == 16) ? 16 : 8;
+// Waves: the operands of more token groups take more registers.
+template <int kG> constexpr int kDownWaves = kG <= 2 ? 16 : kG == 4 ? 12 : 8;
 template <bool kFew, int kG> using DownRoute = Route<kFew, 8 * kG>;
 
 template <bool kFew, int kG, int kRows>
-__global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a) {
   constexpr int kQ = kPieces<kRows>;
   extern __shared__ u32x4 lds[];
   using R = DownRoute<kFew, kG>;
@@ -535,7 +511,7 @@ __global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(
     };
     e = __builtin_amdgcn_readfirstlane(route.expert(at));
     w4[0] = weights_of(e);
-    u32x4 v[1][kInst], b[kHeld<kG>][kSteps * kQ];
+    u32x4 v[1][kInst], b[kG][kSteps * kQ];
     load_slab<kRows, 1>(v, w4, n0, a.K, s, nch, lane);
     enter();
     load_tokens<kQ>(b, x, row, groups, s, nch, lane);
@@ -554,7 +530,7 @@ __global__ __launch_bounds__((kDownWaves<kG, kRows> * 64)) void moe_down_kernel(
         }
         load_slab<kRows, 1>(v, w4, n0, a.K, last ? 0 : s + 1, nch, lane);
       }
-      multiply<kRows, 1, kG>(tile, b, x, row, groups, s, nch, lane, acc);
+      multiply<kRows, 1, kG>(tile, b, groups, lane, acc);
       ++s;
       if (last || !more) {                       // weighted, into this wave's y
 #pragma unroll
@@ -645,10 +621,10 @@ hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
 
 template <bool kFew, int kG, int kRows>
 hipError_t launch_down(const MoeArgs& a, hipStream_t s) {
-  constexpr int kMost = kDownWaves<kG, kRows>;
+  constexpr int kMost = kDownWaves<kG>;
   const int blocks = (a.K + kRows - 1) / kRows;
-  // 16 waves (8 where the registers allow no more); 8 and two workgroups per
-  // CU where there are enough of them.
+  // As many waves as the registers allow, or two workgroups of 8 per CU where
+  // there are enough of them.
   const int nw = blocks > 256 ? 8 : kMost;
   // Parts: at most as many as give every wave a slab.
   int parts = 1;
@@ -679,7 +655,8 @@ hipError_t launch_up_act(Act act, const MoeArgs& a, hipStream_t s) {
 // against 49 (16, with the sum of the parts), with 8 tokens 77 against 66.
 template <bool kFew, int kG>
 hipError_t launch_down_rows(const MoeArgs& a, hipStream_t s) {
-  if (moe_parts(a.K) > 1 && a.K > 8 * kMoeFullBlocks && a.T * a.k < 4 * a.E) return launch_down<kFew, kG, 8>(a, s);
+  if constexpr (kG == 1)
+    if (moe_parts(a.K) > 1 && a.K > 8 * kMoeFullBlocks && a.T * a.k < 4 * a.E) return launch_down<kFew, 1, 8>(a, s);
   return launch_down<kFew, kG, 16>(a, s);
 }
 
