@@ -23,6 +23,8 @@
 // (`skip` of them) set to zero on use and left to that neighbour, so every
 // load is full and none is behind a branch.  Threads past the last chunk skip all
 // of theirs.
+#include <type_traits>
+
 #include "block.hpp"
 #include "common.hpp"
 #include "validate.hpp"
@@ -117,27 +119,42 @@ constexpr int kWide = 0;
 constexpr int kThreads = 512;                    // workgroups of several rows
 constexpr int kMaxThreads = 1024;
 
+// The sum over the 16 lanes of a DPP row, in each of them.
+__device__ __forceinline__ float sum16(float v) {
+  auto add = [&](auto ctrl) {
+    v += bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  add(std::integral_constant<int, 0xB1>{});      // quad_perm: lane ^ 1
+  add(std::integral_constant<int, 0x4E>{});      // quad_perm: lane ^ 2
+  add(std::integral_constant<int, 0x141>{});     // row_half_mirror: the other quad of 8
+  add(std::integral_constant<int, 0x140>{});     // row_mirror: the other 8 of 16
+  return v;
+}
+__device__ __forceinline__ float sum64(float v) {
+  v = sum16(v);
+  auto at = [&](int lane) { return bits_f32((uint32_t)__builtin_amdgcn_readlane((int)f32_bits(v), lane)); };
+  return (at(0) + at(16)) + (at(32) + at(48));
+}
+
 // Sums of kS values over a row's threads, in a fixed order.  The caller
 // alternates `slot` between 0 and 1, so one barrier per sum suffices: a
-// buffer is rewritten only after every thread passed the other one's.
+// buffer is rewritten only after every thread passed the other one's.  The
+// sums are the critical path of a row where there are few rows, so lanes are
+// added by DPP and the (at most 16) waves by the lanes of one DPP row.
 template <int kL, int kS>
 __device__ __forceinline__ void row_sum(float (&v)[kS], float (*buf)[kS][kMaxThreads / 64], int slot) {
-  constexpr int kLanes = kL == kWide ? 64 : kL;
 #pragma unroll
-  for (int off = kLanes / 2; off >= 1; off >>= 1)
-#pragma unroll
-    for (int s = 0; s < kS; ++s) v[s] += __shfl_xor(v[s], off);
+  for (int s = 0; s < kS; ++s) v[s] = kL == 16 ? sum16(v[s]) : sum64(v[s]);
   if constexpr (kL == kWide) {
-    const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    if ((threadIdx.x & 63) == 0)
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, other = lane & 15;
+    if (lane == 0)
 #pragma unroll
       for (int s = 0; s < kS; ++s) buf[slot][s][wave] = v[s];
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < kS; ++s) {
-      float sum = buf[slot][s][0];
-      for (int w = 1; w < waves; ++w) sum += buf[slot][s][w];
-      v[s] = sum;
+      const float part = buf[slot][s][other];
+      v[s] = sum16(other < (int)(blockDim.x >> 6) ? part : 0.0f);
     }
   }
 }
