@@ -397,7 +397,8 @@ enum swiglu_score {
  *   logits   [T, E] fp32 or bf16 (dtype), 16-byte aligned
  *   weights  [T, k] fp32,  ids [T, k] int32 (outputs, 4-byte aligned)
  * 1 <= E <= SWIGLU_MAX_EXPERTS, 1 <= k <= min(E, SWIGLU_MAX_TOPK), else
- * SWIGLU_ERR_SHAPE; unknown score, or scale not finite: SWIGLU_ERR_ARG. */
+ * SWIGLU_ERR_SHAPE; T * max(E, 64) <= 2^33, else SWIGLU_ERR_UNSUPPORTED;
+ * unknown score, or scale not finite: SWIGLU_ERR_ARG. */
 int swiglu_route_fwd(int score, int renorm, int dtype, int64_t T, int64_t E, int64_t k,
                      const void* logits, float scale, float* weights, int32_t* ids, void* stream);
 
@@ -427,9 +428,11 @@ size_t swiglu_moe_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t k);
 /* The routed MLP for a few tokens, bf16: with e = ids[t, j],
  *   y[t] = sum_j weights[t, j] * Wd_e (act(Wg_e x[t]) * (Wu_e x[t]))
  * The weights of each expert that some token names are read once for all its
- * tokens; other experts are not read.  Products accumulate in fp32 in a fixed
+ * tokens (again for every 8 to 32 of them where one has far more than T k / E);
+ * other experts are not read.  Products accumulate in fp32 in a fixed
  * order (results are deterministic), the hidden activations are kept to 16
- * significant bits, and y is rounded once.  Entries with an id outside [0, E)
+ * significant bits (as a sum of two bf16, so that an infinite weight in wd
+ * gives NaN where one of them is 0), and y is rounded once.  Entries with an id outside [0, E)
  * are skipped (no expert had room; a token without experts gets 0); an expert
  * named twice by a token counts twice.
  *
@@ -471,8 +474,8 @@ int swiglu_moe_fwd(int act, int64_t T, int64_t E, int64_t k, int64_t N, int64_t 
  *               so groups = 1 is a gate per channel and groups = batch one per
  *               sample; groups is 0 where gate is NULL
  *   res_out, z  [rows, cols] (outputs, dtype)
- * Any cols from 1 to 16384 (else SWIGLU_ERR_UNSUPPORTED) and pointers aligned
- * to an element; rows % groups == 0, else SWIGLU_ERR_SHAPE; eps > 0 and
+ * Any cols from 1 to 16384, rows * max(cols, 128) <= 2^33, groups <= 2^20
+ * (else SWIGLU_ERR_UNSUPPORTED), and pointers aligned to an element; rows % groups == 0, else SWIGLU_ERR_SHAPE; eps > 0 and
  * finite skip, scale, w_offset, eps, else SWIGLU_ERR_ARG; y and w_in not both
  * NULL. */
 int swiglu_block_norm_fwd(int dtype, int64_t rows, int64_t cols, int64_t groups,

@@ -182,7 +182,7 @@ def _norm_sizes(like: torch.Tensor, w_out, gate, w_in) -> tuple[int, int, int]:
     cols = like.shape[-1]
     rows = math.prod(like.shape[:-1])
     for t, name in ((w_out, "w_out"), (w_in, "w_in")):
-        if t is not None and tuple(t.shape) != (cols,):
+        if t is not None and t.shape != (cols,):
             raise ValueError(f"{name} must have shape {(cols,)}, got {tuple(t.shape)}")
     groups = 0
     if gate is not None:
@@ -195,7 +195,12 @@ def _norm_sizes(like: torch.Tensor, w_out, gate, w_in) -> tuple[int, int, int]:
 
 
 def _contig(t):
-    return None if t is None else t.contiguous()
+    return t if t is None or t.is_contiguous() else t.contiguous()
+
+
+def _like(t):
+    """An output shaped as t (contiguous or None)."""
+    return None if t is None else torch.empty_like(t)
 
 
 def block_norm(res: torch.Tensor, y: torch.Tensor | None = None, w_out: torch.Tensor | None = None,
@@ -229,10 +234,10 @@ def block_norm(res: torch.Tensor, y: torch.Tensor | None = None, w_out: torch.Te
         if (y is None and ro is not None) or (w_in is None and z is not None):
             raise ValueError("out has an output that this call does not compute")
     _on_gpu(res)
-    res, y, w_out, gate, w_in = (_contig(t) for t in (res, y, w_out, gate, w_in))
+    res, y, w_out, gate, w_in = _contig(res), _contig(y), _contig(w_out), _contig(gate), _contig(w_in)
     if out is None:
-        ro = torch.empty_like(res) if y is not None else None
-        z = torch.empty_like(res) if w_in is not None else None
+        ro = _like(y)
+        z = None if w_in is None else torch.empty_like(res)
     check("swiglu_block_norm_fwd", lib().swiglu_block_norm_fwd(
         dt, rows, cols, groups, _p(res), _p(y), _p(w_out), _p(gate), _p(w_in), float(skip), float(scale),
         float(w_offset), float(eps), _p(ro), _p(z), _stream(res)))
@@ -272,24 +277,22 @@ def block_norm_bwd(res_out: torch.Tensor | None, y: torch.Tensor | None = None, 
         if t is not None and t.shape != like.shape:
             raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
     rows, cols, groups = _norm_sizes(like, w_out, gate, w_in)
-    shapes = (like.shape, None if y is None else y.shape, None if w_out is None else w_out.shape,
-              None if gate is None else gate.shape, None if w_in is None else w_in.shape)
     if out is not None:
         if len(out) != 5:
             raise ValueError("out must be (dres, dy, dw_out, dgate, dw_in)")
-        for t, shape, name in zip(out, shapes, ("dres", "dy", "dw_out", "dgate", "dw_in")):
-            if shape is not None:
-                _check_out(t, name, shape, like.dtype, like.device)
+        for t, of, name in zip(out, (like, y, w_out, gate, w_in), ("dres", "dy", "dw_out", "dgate", "dw_in")):
+            if of is not None:
+                _check_out(t, name, of.shape, like.dtype, like.device)
             elif t is not None:
                 raise ValueError("out has an output that this call does not compute")
     if workspace is not None and (workspace.device != like.device or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on the device of the inputs")
     _on_gpu(like)
+    res_out, y, w_out, gate, w_in = _contig(res_out), _contig(y), _contig(w_out), _contig(gate), _contig(w_in)
+    dres_out, dz = _contig(dres_out), _contig(dz)
     if out is None:
-        out = tuple(None if s is None else torch.empty(s, dtype=like.dtype, device=like.device) for s in shapes)
+        out = (_like(dz if dz is not None else dres_out), _like(y), _like(w_out), _like(gate), _like(w_in))
     dres, dy, dw_out, dgate, dw_in = out
-    res_out, y, w_out, gate, w_in, dres_out, dz = (
-        _contig(t) for t in (res_out, y, w_out, gate, w_in, dres_out, dz))
     need = int(lib().swiglu_block_norm_bwd_workspace_bytes(rows, cols, groups))
     if workspace is None or workspace.numel() * workspace.element_size() < need:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)

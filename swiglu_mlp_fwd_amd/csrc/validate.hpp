@@ -259,6 +259,11 @@ inline int check_route(int64_t T, int64_t E, int64_t k) {
   return SWIGLU_OK;
 }
 
+// Elements of a tensor that one launch walks: a launch has at most 2^32 - 1
+// threads, and the kernels take one for 4 to 16 elements (and at least 8 for
+// a token, 16 for a row).
+constexpr int64_t kBlockMaxElems = int64_t(1) << 33;
+
 inline bool finite_f(float v) { return v - v == 0.0f; }
 
 // weights / dweights: `f`; ids: `i`; dlogits: `d` (nullptr in the forward's
@@ -270,6 +275,7 @@ inline int validate_route(int score, int dtype, int64_t T, int64_t E, int64_t k,
   if (st) return st;
   if ((st = check_route(T, E, k))) return st;
   if (!finite_f(scale)) return SWIGLU_ERR_ARG;
+  if (T * (E > 64 ? E : 64) > kBlockMaxElems) return SWIGLU_ERR_UNSUPPORTED;
   if (T == 0) return SWIGLU_OK;
   if ((st = check_ptr(logits))) return st;
   if (f == nullptr || i == nullptr) return SWIGLU_ERR_NULL;
@@ -340,6 +346,7 @@ inline int validate_moe(int64_t T, int64_t E, int64_t k, int64_t N, int64_t K, c
 }
 
 constexpr int64_t kNormMaxCols = 16384;
+constexpr int64_t kNormMaxGroups = int64_t(1) << 20;   // a workgroup of the backward each
 // Parts the backward's row sums are split into over all groups (each group
 // has at least one): a part is the walk of one workgroup, which has at least
 // one thread for 8 columns, so narrow rows take more of them to fill the chip.
@@ -352,7 +359,8 @@ inline int64_t norm_parts(int64_t cols) {
 inline int norm_shape_status(int64_t rows, int64_t cols, int64_t groups) {
   if (rows < 0 || rows > kMaxDim || cols < 1 || groups < 0 || groups > kMaxDim) return SWIGLU_ERR_SHAPE;
   if (groups > 0 && rows % groups != 0) return SWIGLU_ERR_SHAPE;
-  if (cols > kNormMaxCols) return SWIGLU_ERR_UNSUPPORTED;
+  if (cols > kNormMaxCols || groups > kNormMaxGroups) return SWIGLU_ERR_UNSUPPORTED;
+  if (rows * (cols > 128 ? cols : 128) > kBlockMaxElems) return SWIGLU_ERR_UNSUPPORTED;
   return SWIGLU_OK;
 }
 

@@ -17,6 +17,7 @@ def test_route_validation(L):  # noqa: F811
     assert f(0, 0, 0, 1 << 31, 8, 2, A, 1.0, A, A, None) == ESHAPE
     for E, k in ((0, 1), (1025, 1), (8, 0), (8, 9), (64, 17)):
         assert f(0, 0, 0, 4, E, k, A, 1.0, A, A, None) == ESHAPE
+    assert f(0, 0, 0, (1 << 27) + 1, 8, 2, A, 1.0, A, A, None) == EUNSUP
     for s in (math.nan, math.inf, -math.inf):
         assert f(0, 0, 0, 4, 8, 2, A, s, A, A, None) == EARG
     assert f(0, 0, 0, 4, 8, 2, None, 1.0, A, A, None) == ENULL
@@ -69,7 +70,7 @@ def test_norm_validation(L):  # noqa: F811
     assert fwd(dt=2) == EDTYPE
     for bad in (dict(rows=-1), dict(cols=0), dict(groups=-1), dict(groups=4), dict(rows=1 << 31)):
         assert fwd(**bad) == ESHAPE, bad
-    assert fwd(cols=16385) == EUNSUP
+    assert fwd(cols=16385) == EUNSUP and fwd(rows=1 << 27) == EUNSUP and fwd(rows=1 << 21, groups=1 << 21) == EUNSUP
     for bad in (dict(skip=math.nan), dict(scale=math.inf), dict(off=math.nan), dict(eps=0.0), dict(eps=-1.0),
                 dict(eps=math.inf), dict(groups=0), dict(gate=None), dict(y=None), dict(wi=None), dict(ro=A, y=None, wo=None,
                                                                                                    gate=None, groups=0)):

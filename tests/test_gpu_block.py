@@ -195,6 +195,9 @@ def moe_case(T, E, k, N, K, seed, act="silu", spread="even", check=True, what=No
     g = np.random.default_rng(seed + 4)
     if spread == "even":
         ids = np.stack([g.permutation(E)[:k] for _ in range(T)])
+    elif spread == "skewed":                     # one expert for every token, the others spread
+        ids = np.stack([np.concatenate([[E // 2], g.permutation([e for e in range(E) if e != E // 2])[:k - 1]])
+                        for _ in range(T)])
     elif spread == "one":                        # every token on one expert, however often it can be named
         ids = np.full((T, k), E - 1)
     else:                                        # holes, and ids outside the experts
@@ -223,6 +226,19 @@ def test_moe(act, T, E, k, N, K):
 def test_moe_repeated_missing_and_foreign_ids(T, E, k, N, K):
     moe_case(T, E, k, N, K, 200 + T, spread="one")
     moe_case(T, E, k, N, K, 300 + T, spread="holes")
+
+
+@pytest.mark.parametrize("T,E,k,N,K", [(64, 64, 1, 136, 72), (64, 128, 2, 72, 136), (64, 16, 2, 264, 64), (64, 8, 2, 136, 200),
+                                       (48, 32, 3, 72, 72), (33, 40, 1, 24, 264), (20, 60, 2, 40, 2608), (64, 70, 1, 40, 1400)])
+def test_moe_an_expert_with_far_more_tokens_than_the_others(T, E, k, N, K):
+    moe_case(T, E, k, N, K, 250 + T, spread="skewed")
+
+
+@pytest.mark.parametrize("T,E,k,N,K", [(3, 4, 2, 1000, 2048), (2, 3, 2, 264, 1304), (9, 4, 1, 136, 4104), (5, 7, 3, 5000, 64),
+                                       (20, 3, 2, 2056, 520), (40, 2, 2, 136, 3000)])
+def test_moe_column_tiles_and_parts(T, E, k, N, K):
+    """8 or 16 columns to a workgroup, one part or several, 4 to 16 waves."""
+    moe_case(T, E, k, N, K, 270 + T)
 
 
 def test_moe_no_expert_at_all_and_empty():
