@@ -626,13 +626,20 @@ hipError_t launch_down(const MoeArgs& a, hipStream_t s) {
   // As many waves as the registers allow, or two workgroups of 8 per CU where
   // there are enough of them.
   const int nw = blocks > 256 ? 8 : kMost;
-  // Parts: at most as many as give every wave a slab.
+  // Parts: as many as shorten the waves' chain of slabs by more than the sum
+  // of the parts takes, about three slabs' time (4.5 us).
   int parts = 1;
   if (kRows == 16) {
     const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
-    const int64_t units = (int64_t)slots * ((a.N / 8 + kCPR - 1) / kCPR), most_parts = units / nw;
-    parts = (int)moe_parts(a.K);
-    if (parts > most_parts) parts = most_parts > 1 ? (int)most_parts : 1;
+    const int64_t units = (int64_t)slots * ((a.N / 8 + kCPR - 1) / kCPR);
+    int64_t best = (units + nw - 1) / nw;
+    for (int p = 2; p <= moe_parts(a.K); ++p) {
+      const int64_t chain = (units + (int64_t)p * nw - 1) / ((int64_t)p * nw) + 3;
+      if (chain < best) {
+        best = chain;
+        parts = p;
+      }
+    }
   }
   constexpr size_t most = (size_t)kMost * (kTile * 16 + kMaxTokens * kRows * 4);
   const size_t lds = (size_t)nw * (kTile * 16 + a.T * kRows * 4);
