@@ -16,7 +16,7 @@
 //   would cost as much as the rounding of y).  A workgroup takes an equal share of the (expert in
 //   use, 16-row tile) sequence; its waves split the reduction and meet in
 //   LDS at the end of each tile, with the next tile's slab already requested.
-// moe_down_kernel: y.  A workgroup takes 8 or 16 columns of y over all
+// moe_down_kernel: y.  A workgroup takes 8, 16 or 32 columns of y over all
 //   experts in use (or, where that leaves CUs without work, over one of S
 //   equal parts), its waves equal shares of the (expert, slab) sequence;
 //   hi and lo are two of the 16 token columns of one product, 8 tokens at a
@@ -279,7 +279,8 @@ __device__ __forceinline__ void load_tokens(u32x4 (&v)[kG][kSteps * kQ], const T
 // 128-byte lines are read once and bypass the caches; in others neighbouring
 // slabs share a line, which the bypass would read from HBM twice (1.4 times
 // the bytes at K = 1160).
-template <int kRows, int kW>
+// The tiles are of kW weights, or of one weight, kRows rows after each other (kDown).
+template <int kRows, int kW, bool kDown>
 __device__ __forceinline__ void load_slab(u32x4 (&v)[kW][kInst], const u32x4* const (&w4)[kW], int n0, int rows, int s,
                                           int nch, int lane) {
   constexpr int kQ = kPieces<kRows>;
@@ -289,10 +290,18 @@ __device__ __forceinline__ void load_slab(u32x4 (&v)[kW][kInst], const u32x4* co
 #pragma unroll
     for (int i = 0; i < kInst; ++i) {
       const int n = n0 + (i % (kRows / 4)) * 4 + lr, c = (s * kQ + i / (kRows / 4)) * kCPR + lc;
-      const bool in = n < rows && c < nch;
-      const int64_t off = in ? (int64_t)n * nch + c : 0;
+      if constexpr (kDown) {
 #pragma unroll
-      for (int w = 0; w < kW; ++w) v[w][i] = in ? get(w4[w] + off) : zero;
+        for (int w = 0; w < kW; ++w) {
+          const bool in = n + w * kRows < rows && c < nch;
+          v[w][i] = in ? get(w4[w] + (in ? (int64_t)n * nch + c : 0)) : zero;
+        }
+      } else {
+        const bool in = n < rows && c < nch;
+        const int64_t off = in ? (int64_t)n * nch + c : 0;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) v[w][i] = in ? get(w4[w] + off) : zero;
+      }
     }
   };
   if (nch % 8 == 0) load([](const u32x4* p) { return __builtin_nontemporal_load(p); });
@@ -390,7 +399,7 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
   clear();
   weights_of(e);
   u32x4 v[2][kInst], b[kG][kSteps];
-  if (s0 < s1) load_slab<16, 2>(v, w4, t * 16, a.N, s0, nch, lane);
+  if (s0 < s1) load_slab<16, 2, false>(v, w4, t * 16, a.N, s0, nch, lane);
   enter();
   if (s0 < s1) load_tokens<1>(b, x, row, groups, s0, nch, lane);
   for (; u < u1; ++u) {
@@ -404,10 +413,10 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
     for (int s = s0; s < s1; ++s) {
       to_tile<16, 2>(v, tile, lane);
       if (s + 1 < s1) {
-        load_slab<16, 2>(v, w4, t * 16, a.N, s + 1, nch, lane);
+        load_slab<16, 2, false>(v, w4, t * 16, a.N, s + 1, nch, lane);
       } else if (more) {
         if (other) weights_of(e2);
-        load_slab<16, 2>(v, w4, t2 * 16, a.N, s0, nch, lane);
+        load_slab<16, 2, false>(v, w4, t2 * 16, a.N, s0, nch, lane);
       }
       multiply<16, 2, kG>(tile, b, groups, lane, acc);
       if (s + 1 < s1 || (more && !other)) load_tokens<1>(b, x, row, groups, s + 1 < s1 ? s + 1 : s0, nch, lane);
@@ -460,27 +469,30 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
 
 // --------------------------------------------------------------- second product
 
-// Waves: the operands of more token groups take more registers.
-template <int kG> constexpr int kDownWaves = kG <= 2 ? 16 : kG == 4 ? 12 : 8;
+// kCols columns of y: tiles of 8 or 16 weight rows, two of 16 for 32.
+template <int kCols> constexpr int kTileRows = kCols < 16 ? kCols : 16;
+// Waves: the operands of more token groups take more registers, and the
+// waves' y of 32 columns more LDS.
+template <int kG, int kCols> constexpr int kDownWaves = kCols == 32 ? 8 : kG <= 2 ? 16 : kG == 4 ? 12 : 8;
 template <bool kFew, int kG> using DownRoute = Route<kFew, 8 * kG>;
 
-template <bool kFew, int kG, int kRows>
-__global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a) {
-  constexpr int kQ = kPieces<kRows>;
+template <bool kFew, int kG, int kCols>
+__global__ __launch_bounds__((kDownWaves<kG, kCols> * 64)) void moe_down_kernel(MoeArgs a) {
+  constexpr int kRows = kTileRows<kCols>, kT = kCols / kRows, kQ = kPieces<kRows>;
   extern __shared__ u32x4 lds[];
   using R = DownRoute<kFew, kG>;
   __shared__ typename R::Shared shared;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nw = blockDim.x >> 6, r16 = lane & 15, q4 = lane >> 4;
-  u32x4* tile = lds + wave * kTile;
-  float* ys = reinterpret_cast<float*>(lds + nw * kTile);   // [wave][T][kRows]
-  for (int i = tid; i < nw * a.T * kRows; i += blockDim.x) ys[i] = 0.0f;
+  u32x4* tile = lds + wave * kT * kTile;
+  float* ys = reinterpret_cast<float*>(lds + nw * kT * kTile);   // [wave][T][kCols]
+  for (int i = tid; i < nw * a.T * kCols; i += blockDim.x) ys[i] = 0.0f;
   R route;
   route.init(shared, a, tid, true);
   __syncthreads();
-  float* mine = ys + wave * a.T * kRows;
+  float* mine = ys + wave * a.T * kCols;
 
-  const int n0 = blockIdx.x * kRows, nch = a.N >> 3, nslab = (nch + kQ * kCPR - 1) / (kQ * kCPR);
+  const int n0 = blockIdx.x * kCols, nch = a.N >> 3, nslab = (nch + kQ * kCPR - 1) / (kQ * kCPR);
   const Tokens x{static_cast<const u32x4*>(a.h), 1, 2 * a.T * a.k};
   const int r8 = lane & 7, half = r16 >> 3;      // token column r16: token r8 of a group of 8, its hi or lo row
   // This wave's share of this workgroup's part of the (pass, slab) sequence.
@@ -495,7 +507,7 @@ __global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a
     // The expert being multiplied: its tokens, and this lane's entries of h.
     int e, first, groups, row[kG];
     uint64_t tokens;
-    const u32x4* w4[1];
+    const u32x4* w4[kT];
     auto enter = [&] {
       tokens = route.tokens(e);
       first = at.pass * 8 * kG;
@@ -507,30 +519,34 @@ __global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a
       }
     };
     auto weights_of = [&](int expert) {
-      return reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wd) + expert * a.wd_stride);
+      w4[0] = reinterpret_cast<const u32x4*>(static_cast<const bf16*>(a.wd) + expert * a.wd_stride);
+#pragma unroll
+      for (int i = 1; i < kT; ++i) w4[i] = w4[0] + (int64_t)kRows * i * nch;
     };
     e = __builtin_amdgcn_readfirstlane(route.expert(at));
-    w4[0] = weights_of(e);
-    u32x4 v[1][kInst], b[kG][kSteps * kQ];
-    load_slab<kRows, 1>(v, w4, n0, a.K, s, nch, lane);
+    weights_of(e);
+    u32x4 v[kT][kInst], b[kG][kSteps * kQ];
+    load_slab<kRows, kT, true>(v, w4, n0, a.K, s, nch, lane);
     enter();
     load_tokens<kQ>(b, x, row, groups, s, nch, lane);
-    f32x4 acc[1][kG];
+    f32x4 acc[kT][kG];
 #pragma unroll
-    for (int g = 0; g < kG; ++g) acc[0][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < kT; ++i)
+#pragma unroll
+      for (int g = 0; g < kG; ++g) acc[i][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (; u < u1; ++u) {
-      to_tile<kRows, 1>(v, tile, lane);
+      to_tile<kRows, kT>(v, tile, lane);
       const bool last = s + 1 == nslab, more = u + 1 < u1;   // of this pass; of this wave
       int e2 = e;
       if (more) {
         if (last) {
           route.next(at);
           e2 = __builtin_amdgcn_readfirstlane(route.expert(at));
-          w4[0] = weights_of(e2);
+          weights_of(e2);
         }
-        load_slab<kRows, 1>(v, w4, n0, a.K, last ? 0 : s + 1, nch, lane);
+        load_slab<kRows, kT, true>(v, w4, n0, a.K, last ? 0 : s + 1, nch, lane);
       }
-      multiply<kRows, 1, kG>(tile, b, groups, lane, acc);
+      multiply<kRows, kT, kG>(tile, b, groups, lane, acc);
       ++s;
       if (last || !more) {                       // weighted, into this wave's y
 #pragma unroll
@@ -543,18 +559,21 @@ __global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a
             const float wj = route.weight_of(p);
             w += route.id_of(p) == e ? wj : 0.0f;
           }
-          f32x4 o = acc[0][g];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) o[q] += __shfl_xor(o[q], 8);   // hi + lo
-          // Rows 4 q4 .. + 3 of the tile; with 8 rows the upper half repeats the lower.
-          if (t >= 0 && half == 0 && 4 * q4 < kRows) {
-            f32x4* y = reinterpret_cast<f32x4*>(mine + t * kRows + 4 * q4);
-            f32x4 sum = *y;
+          for (int i = 0; i < kT; ++i) {
+            f32x4 o = acc[i][g];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) sum[q] = __builtin_fmaf(w, o[q], sum[q]);
-            *y = sum;
+            for (int q = 0; q < 4; ++q) o[q] += __shfl_xor(o[q], 8);   // hi + lo
+            // Rows 4 q4 .. + 3 of the tile; with 8 rows the upper half repeats the lower.
+            if (t >= 0 && half == 0 && 4 * q4 < kRows) {
+              f32x4* y = reinterpret_cast<f32x4*>(mine + t * kCols + 16 * i + 4 * q4);
+              f32x4 sum = *y;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) sum[q] = __builtin_fmaf(w, o[q], sum[q]);
+              *y = sum;
+            }
+            acc[i][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
           }
-          acc[0][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
         if (more) {
           e = e2;
@@ -566,10 +585,10 @@ __global__ __launch_bounds__(kDownWaves<kG> * 64) void moe_down_kernel(MoeArgs a
     }
   }
   __syncthreads();
-  for (int i = tid; i < a.T * kRows; i += blockDim.x) {
+  for (int i = tid; i < a.T * kCols; i += blockDim.x) {
     float y = ys[i];
-    for (int w = 1; w < nw; ++w) y += ys[w * a.T * kRows + i];
-    const int t = i / kRows, c = n0 + i % kRows;
+    for (int w = 1; w < nw; ++w) y += ys[w * a.T * kCols + i];
+    const int t = i / kCols, c = n0 + i % kCols;
     if (c >= a.K) continue;
     if (gridDim.y == 1) static_cast<bf16*>(a.y)[(int64_t)t * a.K + c] = to_bf16(y);
     else a.part[((int64_t)blockIdx.y * a.T + t) * a.K + c] = y;
@@ -619,21 +638,21 @@ hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool kFew, int kG, int kRows>
+template <bool kFew, int kG, int kCols>
 hipError_t launch_down(const MoeArgs& a, hipStream_t s) {
-  constexpr int kMost = kDownWaves<kG>;
-  const int blocks = (a.K + kRows - 1) / kRows;
+  constexpr int kMost = kDownWaves<kG, kCols>, kT = kCols / kTileRows<kCols>;
+  const int blocks = (a.K + kCols - 1) / kCols;
   // As many waves as the registers allow, or two workgroups of 8 per CU where
   // there are enough of them.
   const int nw = blocks > 256 ? 8 : kMost;
   // Parts: as many as shorten the waves' chain of slabs by more than the sum
   // of the parts takes, about three slabs' time (4.5 us).
   int parts = 1;
-  if (kRows == 16) {
+  if (kCols >= 16) {
     const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
     const int64_t units = (int64_t)slots * ((a.N / 8 + kCPR - 1) / kCPR);
     int64_t best = (units + nw - 1) / nw;
-    for (int p = 2; p <= moe_parts(a.K); ++p) {
+    for (int p = 2; p <= moe_parts(a.K, kCols); ++p) {
       const int64_t chain = (units + (int64_t)p * nw - 1) / ((int64_t)p * nw) + 3;
       if (chain < best) {
         best = chain;
@@ -641,11 +660,11 @@ hipError_t launch_down(const MoeArgs& a, hipStream_t s) {
       }
     }
   }
-  constexpr size_t most = (size_t)kMost * (kTile * 16 + kMaxTokens * kRows * 4);
-  const size_t lds = (size_t)nw * (kTile * 16 + a.T * kRows * 4);
-  hipError_t e = allow_lds<&moe_down_kernel<kFew, kG, kRows>>(most);
+  constexpr size_t most = (size_t)kMost * (kT * kTile * 16 + kMaxTokens * kCols * 4);
+  const size_t lds = (size_t)nw * (kT * kTile * 16 + a.T * kCols * 4);
+  hipError_t e = allow_lds<&moe_down_kernel<kFew, kG, kCols>>(most);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<kFew, kG, kRows>), dim3(blocks, parts), dim3(nw * 64), lds, s, a);
+  hipLaunchKernelGGL((moe_down_kernel<kFew, kG, kCols>), dim3(blocks, parts), dim3(nw * 64), lds, s, a);
   if ((e = hipGetLastError()) != hipSuccess || parts == 1) return e;
   hipLaunchKernelGGL(moe_sum_kernel, dim3((a.T * a.K / 4 + 255) / 256), dim3(256), 0, s, a, parts);
   return hipGetLastError();
@@ -656,14 +675,19 @@ hipError_t launch_up_act(Act act, const MoeArgs& a, hipStream_t s) {
   return act == Act::kGeluTanh ? launch_up<Act::kGeluTanh, kFew, kG>(a, s) : launch_up<Act::kSilu, kFew, kG>(a, s);
 }
 
-// 16 columns of y to a workgroup; 8 where 16 would need a split and 8 do not,
-// if the tokens are few: a slab of 8 rows takes the token operands of twice
-// the reduction.  At K = 2048 with 2 tokens per expert 46 us (8 columns)
-// against 49 (16, with the sum of the parts), with 8 tokens 77 against 66.
+// 16 columns of y to a workgroup.  A slab's token operands are as many bytes
+// per 8 tokens as its weights for 16 columns, so from 4 tokens per expert on
+// 32 columns.  The whole call, 32 against 16: 48 tokens of 13 x (3456, 2304),
+// 4 each, 174 us against 191; 64 of 64 x (1024, 4096), 8 each, 258 against
+// 279; 64 of 64 x (1024, 2048), 8 each, the same.  With fewer tokens 8
+// columns, where 16 would need a split and 8 do not: at K = 2048 with 2
+// tokens per expert the kernel takes 46 us against 49 (with the parts' sum).
 template <bool kFew, int kG>
-hipError_t launch_down_rows(const MoeArgs& a, hipStream_t s) {
+hipError_t launch_down_cols(const MoeArgs& a, hipStream_t s) {
   if constexpr (kG == 1)
-    if (moe_parts(a.K) > 1 && a.K > 8 * kMoeFullBlocks && a.T * a.k < 4 * a.E) return launch_down<kFew, 1, 8>(a, s);
+    if (moe_parts(a.K, 16) > 1 && a.K > 8 * kMoeFullBlocks && a.T * a.k < 4 * a.E) return launch_down<kFew, 1, 8>(a, s);
+  if constexpr (kG == 2 || kG == 4)
+    if (a.T * a.k >= 4 * a.E) return launch_down<kFew, kG, 32>(a, s);
   return launch_down<kFew, kG, 16>(a, s);
 }
 
@@ -677,10 +701,10 @@ hipError_t launch_few(Act act, const MoeArgs& a, hipStream_t s) {
                        : a.T <= 32 || avg <= 16 ? launch_up_act<kFew, 2>(act, a, s)
                                                 : launch_up_act<kFew, 4>(act, a, s);
   if (e != hipSuccess) return e;
-  if (a.T <= 8 || avg <= 3) return launch_down_rows<kFew, 1>(a, s);
-  if (a.T <= 16 || avg <= 8) return launch_down_rows<kFew, 2>(a, s);
-  if (a.T <= 32 || avg <= 16) return launch_down_rows<kFew, 4>(a, s);
-  return launch_down_rows<kFew, 8>(a, s);
+  if (a.T <= 8 || avg <= 3) return launch_down_cols<kFew, 1>(a, s);
+  if (a.T <= 16 || avg <= 8) return launch_down_cols<kFew, 2>(a, s);
+  if (a.T <= 32 || avg <= 16) return launch_down_cols<kFew, 4>(a, s);
+  return launch_down_cols<kFew, 8>(a, s);
 }
 
 }  // namespace

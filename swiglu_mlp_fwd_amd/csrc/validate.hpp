@@ -294,11 +294,12 @@ inline int moe_shape_status(int64_t T, int64_t N, int64_t K, int64_t k) {
   return SWIGLU_OK;
 }
 
-// Parts that the second product's reduction is split into where its 16-column
-// tiles leave many of the 256 CUs without a workgroup.
+// Parts that the second product's reduction is split into, at most, where its
+// tiles of `cols` columns (16 or 32) leave many of the 256 CUs without a
+// workgroup.
 constexpr int64_t kMoeFullBlocks = 160;
-inline int64_t moe_parts(int64_t K) {
-  const int64_t blocks = (K + 15) / 16;
+inline int64_t moe_parts(int64_t K, int64_t cols) {
+  const int64_t blocks = (K + cols - 1) / cols;
   return blocks == 0 || blocks > kMoeFullBlocks ? 1 : (256 + blocks - 1) / blocks;
 }
 
@@ -310,7 +311,7 @@ struct MoeLayout {
 };
 inline MoeLayout moe_layout(int64_t T, int64_t N, int64_t K, int64_t k) {
   auto a256 = [](size_t v) { return (v + 255) / 256 * 256; };
-  const int64_t parts = moe_parts(K);
+  const int64_t parts = moe_parts(K, 32);          // never fewer than of 16 columns
   MoeLayout L;
   L.off_part = a256((size_t)T * k * N * 4);
   L.total = L.off_part + (parts > 1 ? a256((size_t)parts * T * K * 4) : 0);

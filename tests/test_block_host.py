@@ -39,9 +39,9 @@ def test_moe_validation(L):  # noqa: F811
     f = L.swiglu_moe_fwd
     T, E, k, N, K = 4, 8, 2, 40, 64
     need = L.swiglu_moe_workspace_bytes(T, N, K, k)
-    # The hidden activations in two bf16 parts; y in 64 parts (4 column tiles of 16 for 256 CUs).
-    assert need == T * k * N * 4 + 64 * T * K * 4
-    assert L.swiglu_moe_workspace_bytes(T, N, 4096, k) == T * k * N * 4
+    # The hidden activations in two bf16 parts; y in 128 parts (2 column tiles of 32 for 256 CUs).
+    assert need == T * k * N * 4 + 128 * T * K * 4
+    assert L.swiglu_moe_workspace_bytes(T, N, 8192, k) == T * k * N * 4
 
     def call(act=0, T=T, E=E, k=k, N=N, K=K, x=A, ids=A, w=A, wg=A, sg=N * K, wu=A, su=N * K, wd=A, sd=N * K, y=A, ws=A,
              n=1 << 40):

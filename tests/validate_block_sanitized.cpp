@@ -46,7 +46,8 @@ int main() {
           } else {
             const MoeLayout L = moe_layout(T, N, K, k);
             check(L.total == total && L.off_part <= L.total && L.off_part >= (size_t)T * k * N * 4 &&
-                      L.total - L.off_part >= (moe_parts(K) > 1 ? (size_t)moe_parts(K) * T * K * 4 : 0),
+                      L.total - L.off_part >= (moe_parts(K, 32) > 1 ? (size_t)moe_parts(K, 32) * T * K * 4 : 0) &&
+                      moe_parts(K, 16) <= moe_parts(K, 32),
                   "moe regions");
           }
           for (int64_t stride : {small, int64_t(-8), int64_t(0), int64_t(8), int64_t(1) << 40, int64_t(1) << 49, big})
