@@ -493,6 +493,11 @@ __global__ __launch_bounds__((kDownWaves<kG, kCols> * 64)) void moe_down_kernel(
   float* mine = ys + wave * a.T * kCols;
 
   const int n0 = blockIdx.x * kCols, nch = a.N >> 3, nslab = (nch + kQ * kCPR - 1) / (kQ * kCPR);
+  // Neighbouring workgroups go through an expert's slabs from different ones
+  // on: from slab 0 all of them would read the same 256 of every N * 2 bytes
+  // at a time, which for a power of two is a few of the memory channels.
+  const int turn = nch % 8 == 0 ? blockIdx.x % nslab : 0;
+  auto slab = [&](int s) { return s + turn < nslab ? s + turn : s + turn - nslab; };
   const Tokens x{static_cast<const u32x4*>(a.h), 1, 2 * a.T * a.k};
   const int r8 = lane & 7, half = r16 >> 3;      // token column r16: token r8 of a group of 8, its hi or lo row
   // This wave's share of this workgroup's part of the (pass, slab) sequence.
@@ -526,9 +531,9 @@ __global__ __launch_bounds__((kDownWaves<kG, kCols> * 64)) void moe_down_kernel(
     e = __builtin_amdgcn_readfirstlane(route.expert(at));
     weights_of(e);
     u32x4 v[kT][kInst], b[kG][kSteps * kQ];
-    load_slab<kRows, kT, true>(v, w4, n0, a.K, s, nch, lane);
+    load_slab<kRows, kT, true>(v, w4, n0, a.K, slab(s), nch, lane);
     enter();
-    load_tokens<kQ>(b, x, row, groups, s, nch, lane);
+    load_tokens<kQ>(b, x, row, groups, slab(s), nch, lane);
     f32x4 acc[kT][kG];
 #pragma unroll
     for (int i = 0; i < kT; ++i)
@@ -544,7 +549,7 @@ __global__ __launch_bounds__((kDownWaves<kG, kCols> * 64)) void moe_down_kernel(
           e2 = __builtin_amdgcn_readfirstlane(route.expert(at));
           weights_of(e2);
         }
-        load_slab<kRows, kT, true>(v, w4, n0, a.K, last ? 0 : s + 1, nch, lane);
+        load_slab<kRows, kT, true>(v, w4, n0, a.K, slab(last ? 0 : s + 1), nch, lane);
       }
       multiply<kRows, kT, kG>(tile, b, groups, lane, acc);
       ++s;
@@ -581,7 +586,7 @@ __global__ __launch_bounds__((kDownWaves<kG, kCols> * 64)) void moe_down_kernel(
           enter();
         }
       }
-      if (more) load_tokens<kQ>(b, x, row, groups, s, nch, lane);
+      if (more) load_tokens<kQ>(b, x, row, groups, slab(s), nch, lane);
     }
   }
   __syncthreads();
