@@ -13,7 +13,7 @@
 //
 // The work is bound by HBM: 2 to 4 tensors forward, 4 to 6 backward.  A row
 // is held in registers by `nt` threads as kCH 16-byte chunks each, so each
-// tensor is read once: 16 lanes or one wave of a row for short rows (several
+// tensor is read once: 16, 32 or 64 lanes of a wave for short rows (several
 // rows per workgroup), otherwise a whole workgroup of as many waves as the
 // row has chunks for.
 //
@@ -114,7 +114,7 @@ struct Span {
   }
 };
 
-// Lanes of a row: 16 or 64 of a wave, or (kWide) every thread of the workgroup.
+// Lanes of a row: 16, 32 or 64 of a wave, or (kWide) every thread of the workgroup.
 constexpr int kWide = 0;
 constexpr int kThreads = 512;                    // workgroups of several rows
 constexpr int kMaxThreads = 1024;
@@ -130,6 +130,10 @@ __device__ __forceinline__ float sum16(float v) {
   add(std::integral_constant<int, 0x140>{});     // row_mirror: the other 8 of 16
   return v;
 }
+__device__ __forceinline__ float sum32(float v) {
+  v = sum16(v);
+  return v + __shfl_xor(v, 16);
+}
 __device__ __forceinline__ float sum64(float v) {
   v = sum16(v);
   auto at = [&](int lane) { return bits_f32((uint32_t)__builtin_amdgcn_readlane((int)f32_bits(v), lane)); };
@@ -144,7 +148,7 @@ __device__ __forceinline__ float sum64(float v) {
 template <int kL, int kS>
 __device__ __forceinline__ void row_sum(float (&v)[kS], float (*buf)[kS][kMaxThreads / 64], int slot) {
 #pragma unroll
-  for (int s = 0; s < kS; ++s) v[s] = kL == 16 ? sum16(v[s]) : sum64(v[s]);
+  for (int s = 0; s < kS; ++s) v[s] = kL == 16 ? sum16(v[s]) : kL == 32 ? sum32(v[s]) : sum64(v[s]);
   if constexpr (kL == kWide) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, other = lane & 15;
     if (lane == 0)
@@ -166,6 +170,9 @@ __device__ __forceinline__ float rstd_of(float sumsq, int cols, float eps) {
 // What a row's block adds: nothing, y itself, or y's norm.
 enum class Join { kNone, kPlain, kNorm };
 
+// Bound by HBM: 8192 x 4096 bf16 with both norms (two tensors read, two
+// written, 268 MB) 41 to 45 us, 5.9 to 6.5 TB/s, where a copy reaches 5.1.  A
+// few rows are bound by the chain load, sum, sum, store: 8 x 4096 3.7 us.
 template <typename T, int kL, int kCH, Join J, bool kZ, bool kTiny>
 __global__ __launch_bounds__(kMaxThreads) void norm_fwd_kernel(NormArgs a) {
   constexpr int kN = Ch<T>::kN;
@@ -258,7 +265,11 @@ __global__ __launch_bounds__(kMaxThreads) void norm_fwd_kernel(NormArgs a) {
 // rows at a time, joined in LDS at the end) go to part[0][p] and part[1][p].
 // The weights stay in registers for the whole walk, and with kAhead the next
 // row's tensors are requested before the present row's sums, so the loads
-// are in flight over the barriers.
+// are in flight over the barriers.  Bound by HBM for many rows: 8192 x 4096
+// bf16 with both norms (four tensors read, two written, 403 MB) 79 to 85 us,
+// 4.8 to 5.1 TB/s (and 6 us for the parts); by a row's chain of loads and two
+// sums where a workgroup has few: 1203 x 2051 fp32 in three groups, three
+// rows each, 19 us.
 template <typename T, int kL, int kCH, Join J, bool kZ, bool kTiny, bool kAhead>
 __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
   constexpr int kN = Ch<T>::kN;
@@ -589,12 +600,19 @@ hipError_t launch_cfg(bool fwd, NormArgs a, hipStream_t s) {
   return launch_parts<T>(a, s);
 }
 
+// As few lanes as hold a row one chunk each: 65536 rows of 256 bf16 columns
+// forward 23 us on 32 lanes against 35 on 64, backward 36 against 56; of 128
+// columns forward 12.8 on 16 lanes against 35.  Long forward rows take two
+// chunks to a thread where there are rows enough: 8192 x 4096 bf16 41 us
+// against 43, 2048 x 8192 24 against 27, 8192 x 4096 fp32 91 against 96, with
+// 1024 rows the same, and with fewer the shorter chain of one chunk counts.
 template <typename T, Join J, bool kZ>
 hipError_t launch_cols(bool fwd, const NormArgs& a, hipStream_t s) {
   constexpr int kN = Ch<T>::kN;
   const int nch = (a.cols + kN - 1) / kN;
   if (a.cols < kN) return launch_cfg<T, 16, 1, J, kZ, true>(fwd, a, s);
   if (nch <= 16) return launch_cfg<T, 16, 1, J, kZ>(fwd, a, s);
+  if (nch <= 32) return launch_cfg<T, 32, 1, J, kZ>(fwd, a, s);
   if (nch <= 64) return launch_cfg<T, 64, 1, J, kZ>(fwd, a, s);
   if (fwd && a.rows > 512 && nch > 256 && nch <= 2048) return launch_cfg<T, kWide, 2, J, kZ>(fwd, a, s);
   if (nch <= 1024) return launch_cfg<T, kWide, 1, J, kZ>(fwd, a, s);

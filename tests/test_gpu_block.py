@@ -358,6 +358,14 @@ def test_norm(dt, join, pre, groups, rows, cols):
                f"norm {dt} {join} {pre} {groups} {rows}x{cols}")
 
 
+@pytest.mark.parametrize("join,pre,groups", JOINS)
+@pytest.mark.parametrize("dt,rows,cols", [("bf16", 4, 129), ("bf16", 36, 256), ("bf16", 1036, 251), ("f32", 4, 65),
+                                          ("f32", 36, 128), ("f32", 1036, 99)])
+def test_norm_half_wave_rows(dt, join, pre, groups, rows, cols):
+    check_norm(norm_inputs(rows, cols, dt, join, pre, groups, rows * cols), dt,
+               f"norm {dt} {join} {pre} {groups} {rows}x{cols}")
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,cols,groups", [(1, 8192, 1), (2, 16384, 2), (3, 12289, 0), (1201, 72, 1), (1300, 260, 0),
                                               (2100, 40, 2100), (1800, 136, 600), (1026, 520, 3)])
