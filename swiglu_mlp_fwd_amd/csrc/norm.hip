@@ -259,6 +259,11 @@ __global__ __launch_bounds__(kMaxThreads) void norm_fwd_kernel(NormArgs a) {
   }
 }
 
+// Backward: whether the threads' sums over rows lie in LDS.  With 16 elements
+// of a row to a thread its registers do not hold them too: 2048 x 12288 bf16
+// 138 us in LDS, 204 in registers (spilled).
+template <typename T, int kL, int kCH> constexpr bool kSumsInLds = kL == kWide && kCH * Ch<T>::kN > 8;
+
 // Backward.  A workgroup walks one part of the rows: of group p / per_group,
 // those whose turn is p % per_group when the group's rows are dealt out R at
 // a time (R rows of the workgroup in parallel).  Its sums a and b (over its R
@@ -274,7 +279,7 @@ template <typename T, int kL, int kCH, Join J, bool kZ, bool kTiny, bool kAhead>
 __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
   constexpr int kN = Ch<T>::kN;
   __shared__ float buf[2][2][kMaxThreads / 64];
-  extern __shared__ float joined[];              // several rows per workgroup: [R][cols]
+  extern __shared__ float joined[];              // several rows per workgroup: [R][cols]; or the threads' sums
   const int nt = kL == kWide ? blockDim.x : kL;
   const int tid = kL == kWide ? threadIdx.x : threadIdx.x % nt;
   const int R = kL == kWide ? 1 : blockDim.x / nt, mine = kL == kWide ? 0 : threadIdx.x / nt;
@@ -292,11 +297,18 @@ __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
     if (J != Join::kNone && gated) g[i] = sp.load(static_cast<const T*>(a.gate) + (int64_t)grp * a.cols, a.cols);
     if constexpr (kZ) wi[i] = sp.load(static_cast<const T*>(a.w_in), a.cols);
   }
-  float sa[kCH][kN], sb[kCH][kN];
+  // This thread's sums, 0: a and 1: b, in registers or LDS.
+  float sums[2][kCH][kN];
+  auto sum = [&](int s, int i, int e) -> float& {
+    if constexpr (kSumsInLds<T, kL, kCH>) return joined[((s * kCH + i) * kN + e) * nt + tid];
+    else return sums[s][i][e];
+  };
 #pragma unroll
-  for (int i = 0; i < kCH; ++i)
+  for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int e = 0; e < kN; ++e) sa[i][e] = sb[i][e] = 0.0f;
+    for (int i = 0; i < kCH; ++i)
+#pragma unroll
+      for (int e = 0; e < kN; ++e) sum(s, i, e) = 0.0f;
 
   struct Row { u32x4 t[kCH], dz[kCH], r[kCH], y[kCH]; };
   auto load = [&](int64_t q, Row& x) {
@@ -352,7 +364,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
         for (int e = 0; e < kN; ++e) {
           const float h = Ch<T>::get(x.r[i], e) * k, d = Ch<T>::get(x.dz[i], e);
-          sb[i][e] = __builtin_fmaf(d, h, sb[i][e]);
+          sum(1, i, e) = __builtin_fmaf(d, h, sum(1, i, e));
           t[i][e] = __builtin_fmaf(k, d * (a.w_offset + Ch<T>::get(wi[i], e)) - h * m, t[i][e]);
         }
     }
@@ -392,7 +404,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
           const float h = Ch<T>::get(x.y[i], e) * k;
           float d = a.scale * (a.w_offset + Ch<T>::get(wo[i], e));
           if (gated) d *= Ch<T>::get(g[i], e);
-          sa[i][e] = __builtin_fmaf(t[i][e], h, sa[i][e]);
+          sum(0, i, e) = __builtin_fmaf(t[i][e], h, sum(0, i, e));
           o[e] = k * (t[i][e] * d - h * m);
         }
         sp.store(static_cast<T*>(a.dy) + at, a.cols, Ch<T>::pack(o));
@@ -406,7 +418,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
         for (int e = 0; e < kN; ++e) {
           o[e] = a.scale * t[i][e];
           if (gated) {
-            sa[i][e] = __builtin_fmaf(t[i][e], Ch<T>::get(x.y[i], e), sa[i][e]);
+            sum(0, i, e) = __builtin_fmaf(t[i][e], Ch<T>::get(x.y[i], e), sum(0, i, e));
             o[e] *= Ch<T>::get(g[i], e);
           }
         }
@@ -434,7 +446,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
   }
   // The part's sums.
   const int64_t parts = (int64_t)groups * a.per_group;
-  auto put = [&](float* out, const float (&v)[kCH][kN]) {
+  auto put = [&](float* out, int s) {
     if constexpr (kL == kWide) {
 #pragma unroll
       for (int i = 0; i < kCH; ++i) {
@@ -443,11 +455,12 @@ __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
           for (int e = 0; e < kN; e += 4)
             *reinterpret_cast<u32x4_any*>(out + sp.start + e) =
-                u32x4{f32_bits(v[i][e]), f32_bits(v[i][e + 1]), f32_bits(v[i][e + 2]), f32_bits(v[i][e + 3])};
+                u32x4{f32_bits(sum(s, i, e)), f32_bits(sum(s, i, e + 1)), f32_bits(sum(s, i, e + 2)),
+                      f32_bits(sum(s, i, e + 3))};
         } else {
 #pragma unroll
           for (int e = 0; e < kN; ++e)
-            if (e >= sp.skip && (!kTiny || e < a.cols)) out[sp.start + e] = v[i][e];
+            if (e >= sp.skip && (!kTiny || e < a.cols)) out[sp.start + e] = sum(s, i, e);
         }
       }
     } else {
@@ -457,18 +470,18 @@ __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
         const Span<T, kTiny> sp(i * nt + tid, a.cols);
 #pragma unroll
         for (int e = 0; e < kN; ++e)
-          if (e >= sp.skip && (!kTiny || e < a.cols)) joined[mine * a.cols + sp.start + e] = v[i][e];
+          if (e >= sp.skip && (!kTiny || e < a.cols)) joined[mine * a.cols + sp.start + e] = sum(s, i, e);
       }
       __syncthreads();
       for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-        float s = joined[c];
-        for (int r = 1; r < R; ++r) s += joined[r * a.cols + c];
-        out[c] = s;
+        float total = joined[c];
+        for (int r = 1; r < R; ++r) total += joined[r * a.cols + c];
+        out[c] = total;
       }
     }
   };
-  if (sum_a) put(a.part + (int64_t)p * a.cols, sa);
-  if constexpr (kZ) put(a.part + (parts + p) * a.cols, sb);
+  if (sum_a) put(a.part + (int64_t)p * a.cols, 0);
+  if constexpr (kZ) put(a.part + (parts + p) * a.cols, 1);
 }
 
 // Adds the parts.  A workgroup takes 64 columns of the sums a (blockIdx.y =
@@ -589,13 +602,16 @@ hipError_t launch_cfg(bool fwd, NormArgs a, hipStream_t s) {
   if (per < 1) per = 1;
   const int64_t turns = (rpg + R * per - 1) / (R * per);
   a.per_group = (int)((rpg + R * turns - 1) / (R * turns));
-  const size_t lds = kL == kWide ? 0 : (size_t)R * a.cols * 4;
-  // Next-row loads where the registers hold two rows (128 per thread).
-  constexpr bool kAhead = kCH * kN <= 8;
-  hipLaunchKernelGGL((norm_bwd_kernel<T, kL, kCH, J, kZ, kTiny, kAhead>), dim3((unsigned)(groups * a.per_group)),
-                     dim3(threads), lds, s, a);
-  hipError_t e = hipGetLastError();
+  const size_t lds = kSumsInLds<T, kL, kCH> ? (size_t)2 * kCH * kN * threads * 4 : kL == kWide ? 0 : (size_t)R * a.cols * 4;
+  // Next-row loads where the 128 registers of a thread hold two rows: with
+  // two fp32 chunks each they do not, 2048 x 8192 107 us with them, 87 without.
+  constexpr bool kAhead = kCH == 1;
+  constexpr auto kernel = &norm_bwd_kernel<T, kL, kCH, J, kZ, kTiny, kAhead>;
+  hipError_t e = hipSuccess;
+  if constexpr (kSumsInLds<T, kL, kCH>) e = allow_lds<kernel>((size_t)2 * kCH * kN * kMaxThreads * 4);
   if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(groups * a.per_group)), dim3(threads), lds, s, a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.dw_out == nullptr && a.dgate == nullptr && a.dw_in == nullptr) return hipSuccess;
   return launch_parts<T>(a, s);
 }
