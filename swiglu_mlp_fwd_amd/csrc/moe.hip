@@ -29,6 +29,8 @@
 // Which experts are in use, and by which tokens, every workgroup finds from
 // ids itself: from up to 64 ids without LDS or barriers (kFew), from up to
 // 1024 through a token mask per expert in LDS.
+#include <algorithm>
+
 #include "block.hpp"
 #include "common.hpp"
 #include "validate.hpp"
@@ -474,6 +476,8 @@ template <int kCols> constexpr int kTileRows = kCols < 16 ? kCols : 16;
 // Waves: the operands of more token groups take more registers, and the
 // waves' y of 32 columns more LDS.
 template <int kG, int kCols> constexpr int kDownWaves = kCols == 32 ? 8 : kG <= 2 ? 16 : kG == 4 ? 12 : 8;
+// Waves that fit a CU by their registers.
+template <int kG, int kCols> constexpr int kDownCuWaves = kG <= 2 ? 16 : kG == 4 && kCols < 32 ? 12 : 8;
 template <bool kFew, int kG> using DownRoute = Route<kFew, 8 * kG>;
 
 template <bool kFew, int kG, int kCols>
@@ -650,23 +654,22 @@ hipError_t launch_down(const MoeArgs& a, hipStream_t s) {
   // As many waves as the registers allow, or two workgroups of 8 per CU where
   // there are enough of them.
   const int nw = blocks > 256 ? 8 : kMost;
-  // Parts: as many as shorten the waves' chain of slabs by more than the sum
-  // of the parts takes, about three slabs' time (4.5 us).
-  int parts = 1;
-  if (kCols >= 16) {
-    const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
-    const int64_t units = (int64_t)slots * ((a.N / 8 + kCPR - 1) / kCPR);
-    int64_t best = (units + nw - 1) / nw;
-    for (int p = 2; p <= moe_parts(a.K, kCols); ++p) {
-      const int64_t chain = (units + (int64_t)p * nw - 1) / ((int64_t)p * nw) + 3;
-      if (chain < best) {
-        best = chain;
-        parts = p;
-      }
-    }
-  }
   constexpr size_t most = (size_t)kMost * (kT * kTile * 16 + kMaxTokens * kCols * 4);
   const size_t lds = (size_t)nw * (kT * kTile * 16 + a.T * kCols * 4);
+  // Parts: as many as shorten the waves' chain of slabs, over all rounds of
+  // the workgroups that fit the CUs, by more than the sum of the parts takes,
+  // about three slabs' time (4.5 us).
+  int parts = 1;
+  if (kCols >= 16) {
+    const int per_cu = std::max(1, std::min(kDownCuWaves<kG, kCols> / nw, (int)(160 * 1024 / (lds + sizeof(typename DownRoute<kFew, kG>::Shared)))));
+    const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
+    const int64_t units = (int64_t)slots * ((a.N / 8 + kCPR - 1) / kCPR);
+    auto chain = [&](int64_t p) {
+      return ((blocks * p + 256 * per_cu - 1) / (256 * per_cu)) * ((units + p * nw - 1) / (p * nw)) + (p > 1 ? 3 : 0);
+    };
+    for (int p = 2; p <= moe_parts(a.K, kCols); ++p)
+      if (chain(p) < chain(parts)) parts = p;
+  }
   hipError_t e = allow_lds<&moe_down_kernel<kFew, kG, kCols>>(most);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((moe_down_kernel<kFew, kG, kCols>), dim3(blocks, parts), dim3(nw * 64), lds, s, a);
