@@ -390,7 +390,13 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
   };
   const Tokens x{static_cast<const u32x4*>(a.x), nch, 1};
   u32x4* tile = lds + wave * 2 * kTile;
-  const int s0 = wave * nslab / nw, s1 = (wave + 1) * nslab / nw;   // slabs of each tile for this wave
+  // This wave's slabs of each tile: a run of them, or where rows are not whole
+  // lines every nw-th, so that the waves read neighbouring slabs at the same
+  // time and the lines that two of them share are fetched once: K = 1720, 8
+  // tokens of 32 experts, 72 us against 81 (1.05 and 1.34 times the bytes).
+  // With whole lines runs are as fast or faster (K = 2048: 6 us of 137).
+  const bool lines = nch % 8 == 0;
+  const int s0 = lines ? wave * nslab / nw : wave, s1 = lines ? (wave + 1) * nslab / nw : nslab, ds = lines ? 1 : nw;
   f32x4 acc[2][kG];
   auto clear = [&] {
 #pragma unroll
@@ -412,16 +418,17 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
       route.next(at);
       e2 = __builtin_amdgcn_readfirstlane(route.expert(at));
     }
-    for (int s = s0; s < s1; ++s) {
+    for (int s = s0; s < s1; s += ds) {
+      const bool within = s + ds < s1;           // the next slab is of this tile
       to_tile<16, 2>(v, tile, lane);
-      if (s + 1 < s1) {
-        load_slab<16, 2, false>(v, w4, t * 16, a.N, s + 1, nch, lane);
+      if (within) {
+        load_slab<16, 2, false>(v, w4, t * 16, a.N, s + ds, nch, lane);
       } else if (more) {
         if (other) weights_of(e2);
         load_slab<16, 2, false>(v, w4, t2 * 16, a.N, s0, nch, lane);
       }
       multiply<16, 2, kG>(tile, b, groups, lane, acc);
-      if (s + 1 < s1 || (more && !other)) load_tokens<1>(b, x, row, groups, s + 1 < s1 ? s + 1 : s0, nch, lane);
+      if (within || (more && !other)) load_tokens<1>(b, x, row, groups, within ? s + ds : s0, nch, lane);
     }
     // The waves' sums in wave order: group g and weight w by wave 2 g + w % nw.
     lds_barrier();                               // every wave is done with its tile
