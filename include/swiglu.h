@@ -432,9 +432,9 @@ size_t swiglu_moe_workspace_bytes(int64_t T, int64_t N, int64_t K, int64_t k);
  * other experts are not read.  Products accumulate in fp32 in a fixed
  * order (results are deterministic), the hidden activations are kept to 16
  * significant bits (as a sum of two bf16, so that an infinite weight in wd
- * gives NaN where one of them is 0), and y is rounded once.  Entries with an id outside [0, E)
- * are skipped (no expert had room; a token without experts gets 0); an expert
- * named twice by a token counts twice.
+ * gives NaN where one of them is 0), and y is rounded once.  Entries with an
+ * id outside [0, E) are skipped (no expert had room; a token without experts
+ * gets 0); an expert named twice by a token counts twice.
  *
  *   act           SWIGLU_ACT_SILU or SWIGLU_ACT_GELU_TANH
  *   x             [T, K] bf16;  ids [T, k] int32, weights [T, k] fp32
@@ -475,9 +475,9 @@ int swiglu_moe_fwd(int act, int64_t T, int64_t E, int64_t k, int64_t N, int64_t 
  *               sample; groups is 0 where gate is NULL
  *   res_out, z  [rows, cols] (outputs, dtype)
  * Any cols from 1 to 16384, rows * max(cols, 128) <= 2^33, groups <= 2^20
- * (else SWIGLU_ERR_UNSUPPORTED), and pointers aligned to an element; rows % groups == 0, else SWIGLU_ERR_SHAPE; eps > 0 and
- * finite skip, scale, w_offset, eps, else SWIGLU_ERR_ARG; y and w_in not both
- * NULL. */
+ * (else SWIGLU_ERR_UNSUPPORTED), and pointers aligned to an element;
+ * rows % groups == 0, else SWIGLU_ERR_SHAPE; eps > 0 and finite skip, scale,
+ * w_offset, eps, else SWIGLU_ERR_ARG; y and w_in not both NULL. */
 int swiglu_block_norm_fwd(int dtype, int64_t rows, int64_t cols, int64_t groups,
                           const void* res, const void* y, const void* w_out, const void* gate, const void* w_in,
                           float skip, float scale, float w_offset, float eps,
