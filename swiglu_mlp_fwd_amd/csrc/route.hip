@@ -22,7 +22,7 @@
 // recomputed from the logits, so nothing but ids is kept between the two.
 //
 // The work is HBM's for many tokens (the logits, and in the backward their
-// gradients) and latency for few.  kL lanes (8 to 64, so that a lane holds 8
+// gradients) and latency for few.  kL lanes (1 to 64, so that a lane holds 8
 // or 16 logits) share a token, and a wave takes 64 / kL tokens.  A logit and
 // its index make one key, so that a comparison settles ties too (Key below);
 // each lane sorts its keys once, and a choice is the maximum of the lanes'
@@ -230,10 +230,9 @@ __device__ __forceinline__ V over_lanes(V v, F f) {
       return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kC, 0xF, 0xF, true));
     }
   };
-  static_assert(kL >= 8, "lanes of a token");
-  v = f(v, dpp(v, std::integral_constant<int, 0xB1>{}));    // quad_perm: lane ^ 1
-  v = f(v, dpp(v, std::integral_constant<int, 0x4E>{}));    // quad_perm: lane ^ 2
-  v = f(v, dpp(v, std::integral_constant<int, 0x141>{}));   // row_half_mirror: the other quad of 8
+  if constexpr (kL >= 2) v = f(v, dpp(v, std::integral_constant<int, 0xB1>{}));    // quad_perm: lane ^ 1
+  if constexpr (kL >= 4) v = f(v, dpp(v, std::integral_constant<int, 0x4E>{}));    // quad_perm: lane ^ 2
+  if constexpr (kL >= 8) v = f(v, dpp(v, std::integral_constant<int, 0x141>{}));   // row_half_mirror: the other quad of 8
   if constexpr (kL >= 16) v = f(v, dpp(v, std::integral_constant<int, 0x140>{}));   // row_mirror: the other 8 of 16
   if constexpr (kL >= 32) v = f(v, __shfl_xor(v, 16));
   if constexpr (kL >= 64) v = f(v, __shfl_xor(v, 32));
@@ -263,7 +262,8 @@ __device__ __forceinline__ float chosen_score(float l, float top, bool renorm) {
 }
 
 // Entry j of a token's choice is held by lane j % kL, slot j / kL.
-template <int kL> constexpr int kSlots = (SWIGLU_MAX_TOPK + kL - 1) / kL;
+// (A choice has no more entries than the lanes have experts, 8 each at least.)
+template <int kL> constexpr int kSlots = kL == 1 ? 8 : (SWIGLU_MAX_TOPK + kL - 1) / kL;
 
 template <typename T, Score S, int kL, int kC, bool kTiny>
 __global__ __launch_bounds__(kThreads) void route_fwd_kernel(RouteArgs a) {
@@ -445,9 +445,21 @@ hipError_t launch_lanes(bool fwd, const RouteArgs& a, hipStream_t s) {
 // 32768 x 128, k = 8, forward: 7.5 us bf16 and 11.4 fp32, with 16 logits to
 // a lane 9.3 and 13.8 (a longer sort), with 4 (32 lanes, half without logits)
 // 12.2 and 19.2; backward with 8 or 16 alike (8.5 and 8.3; 9.7 and 9.1).
+// Fewer than 8 lanes for up to 32 experts, only where tokens fill the chip
+// all the same: 524288 x 8 bf16 on one lane each forward 7.1 us and backward
+// 9.4, on 8 27 and 26; 131072 x 32 on 4 lanes 9.0 and 10.3, on 8 12.6 and
+// 13.5; 32768 x 8 3.2 and 4.6 against 4.1 and 4.6; but 8 x 8 2.7 and 3.7
+// against 1.8 and 2.2 (a lane's longer chain).
+constexpr int kManyTokens = 32768;
 template <typename T, Score S>
 hipError_t launch_v(bool fwd, const RouteArgs& a, hipStream_t s) {
   constexpr int kN = Row<T>::kN, kC = 8 / kN;
+  if (a.T >= kManyTokens) {
+    if (a.E < kN) return launch_lanes<T, S, 1, 1, true>(fwd, a, s);
+    if (a.E <= 8) return launch_lanes<T, S, 1, kC>(fwd, a, s);
+    if (a.E <= 16) return launch_lanes<T, S, 2, kC>(fwd, a, s);
+    if (a.E <= 32) return launch_lanes<T, S, 4, kC>(fwd, a, s);
+  }
   if (a.E < kN) return launch_lanes<T, S, 8, 1, true>(fwd, a, s);
   if (a.E <= 64) return launch_lanes<T, S, 8, kC>(fwd, a, s);
   if (a.E <= 128) return launch_lanes<T, S, 16, kC>(fwd, a, s);

@@ -122,6 +122,23 @@ def test_route_masks_and_special_values(dt, score, renorm, E):
     check_route(l, k, score, renorm, 1.0, f"route special {dt} {score} {renorm} {E}")
 
 
+@pytest.mark.parametrize("dt,score,renorm", [("bf16", "softmax", True), ("f32", "softmax", False),
+                                             ("bf16", "sigmoid", False), ("f32", "sigmoid", True)])
+@pytest.mark.parametrize("E,k", [(3, 2), (5, 5), (8, 8), (9, 3), (16, 16), (31, 8)])
+def test_route_many_tokens_few_experts(dt, score, renorm, E, k):
+    """Random rows, with masked, equal, lowest-value and NaN rows among them."""
+    T = 32771
+    l = normal((T, E), 17 * E + k, dt, 2.0)
+    l[torch.arange(0, T, 5), torch.arange(0, T, 5) % E] = -math.inf
+    l[100::997] = -math.inf
+    l[101::997] = 0.25
+    l[102::997] = torch.finfo(l.dtype).min
+    l[103::997, E - 1] = math.nan
+    l[104::997, 0] = math.inf
+    l[T - 1] = torch.linspace(-80, 80, E) if E > 1 else 1.0
+    check_route(l, k, score, renorm, 1.5, f"route many {dt} {score} {renorm} {E} {k}")
+
+
 def test_route_equal_logits_take_the_lowest_index():
     g = torch.Generator().manual_seed(3)
     l = torch.randint(0, 4, (300, 96), generator=g).float().to(DEV)
