@@ -494,17 +494,21 @@ constexpr int kSumWaves = 16, kSumThreads = kSumWaves * 64;
 
 __device__ __forceinline__ float sum_parts(const float* __restrict__ p, int64_t n, int64_t first, int64_t step,
                                            int64_t cols) {
-  constexpr int kU = 8;
   float s = 0.0f;
   int64_t i = first;
-  for (; i + (kU - 1) * step < n; i += kU * step) {
+  auto turn = [&](auto loads) {
+    constexpr int kU = decltype(loads)::value;
     float v[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) v[u] = p[(i + u * step) * cols];
 #pragma unroll
     for (int u = 0; u < kU; ++u) s += v[u];
-  }
-  for (; i < n; i += step) s += p[i * cols];
+    i += kU * step;
+  };
+  while (i + 7 * step < n) turn(std::integral_constant<int, 8>{});
+  if (i + 3 * step < n) turn(std::integral_constant<int, 4>{});
+  if (i + step < n) turn(std::integral_constant<int, 2>{});
+  if (i < n) turn(std::integral_constant<int, 1>{});
   return s;
 }
 
