@@ -488,7 +488,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
 // 0: dgate and dw_out) or b (1: dw_in).  With few groups its 16 waves share
 // each group's parts and are joined in wave order; from 16 groups on a wave
 // takes whole groups.  8 loads are in flight per lane.  At 512 parts of 4096
-// columns (16.8 MB): 4.8 us; one load at a time by 4 waves 63 us; 16 columns
+// columns (16.8 MB): 6 us; one load at a time by 4 waves 63 us; 16 columns
 // per workgroup 9.5 us (two of them, on two L2s, share each 128-byte line).
 constexpr int kSumWaves = 16, kSumThreads = kSumWaves * 64;
 
@@ -604,7 +604,11 @@ hipError_t launch_cfg(bool fwd, NormArgs a, hipStream_t s) {
   // as many turns as the longest has.
   int64_t per = norm_parts((int64_t)threads * 8) / groups;
   if (per < 1) per = 1;
-  const int64_t turns = (rpg + R * per - 1) / (R * per);
+  // Beyond 512 rows at a time a part has three turns at least: a turn more
+  // costs less than the sum of as many more parts (1692 x 395 fp32 in 4 groups
+  // 15.5 us in all against 19.2, 996 x 1864 bf16 16.7 against 18.7).
+  int64_t turns = (rpg + R * per - 1) / (R * per);
+  if (turns < 3 && a.rows > 512 * R) turns = 3;
   a.per_group = (int)((rpg + R * turns - 1) / (R * turns));
   const size_t lds = kSumsInLds<T, kL, kCH> ? (size_t)2 * kCH * kN * threads * 4 : kL == kWide ? 0 : (size_t)R * a.cols * 4;
   // Next-row loads where the 128 registers of a thread hold two rows: with
