@@ -114,7 +114,7 @@ __device__ __forceinline__ int lane_of(int count, int lane, int& n, int& sum) {
 template <int kCap> struct Route<true, kCap> {
   struct Shared {};
   int id, k, T, lane;
-  int passes, before;                            // per lane: of its expert; pairs of the experts before it
+  int passes, before;                            // per lane: of its expert; tokens of the experts before it
   float weight;                                  // per lane: of pair `lane`
   uint64_t first;                                // lanes with passes
   __device__ __forceinline__ void init(Shared&, const MoeArgs& a, int tid, bool weights) {
@@ -132,11 +132,14 @@ template <int kCap> struct Route<true, kCap> {
       same &= (id >> b) & 1 ? m : ~m;
     }
     same &= __ballot(id >= 0);
-    const bool is_first = id >= 0 && (same & ((1ull << lane) - 1)) == 0;
-    // Of pairs, not tokens: a token that names an expert twice may add a pass without tokens.
-    passes = is_first ? passes_of<kCap>(__popcll(same)) : 0;
+    const uint64_t earlier = (1ull << lane) - 1;
+    const bool is_first = id >= 0 && (same & earlier) == 0;
     first = __ballot(is_first);
-    const int n = is_first ? __popcll(same) : 0;
+    // Tokens of the expert: a token that names it again counts once, so that no pass is without tokens.
+    const uint64_t of_token = ((1ull << k) - 1) << (lane / k * k);   // the pairs of this lane's token
+    const uint64_t once = __ballot(id >= 0 && (same & of_token & earlier) == 0);
+    const int n = is_first ? __popcll(same & once) : 0;
+    passes = passes_of<kCap>(n);
     before = running_sum(n, lane) - n;
   }
   __device__ __forceinline__ int count() const {
