@@ -20,8 +20,9 @@
 // Rows need not be aligned nor a whole number of chunks: chunks load at any
 // element's address, and the chunk that would pass the row's end is loaded
 // from cols - kN instead, with the elements it shares with its neighbour
-// (`skip` of them) set to zero on use and left to that neighbour, so every
-// load is full and none is behind a branch.  Threads past the last chunk skip all
+// (`skip` of them) set to zero on use, in the weights and gates as well as in
+// the rows, and left to that neighbour, so every load is full and none is
+// behind a branch.  Threads past the last chunk skip all
 // of theirs.
 #include <type_traits>
 
@@ -202,9 +203,11 @@ __global__ __launch_bounds__(kMaxThreads) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
   for (int i = 0; i < kCH; ++i) {
     const Span<T, kTiny> sp(i * nt + tid, a.cols);
-    if (sp.skip != 0) {
+    if (sp.skip != 0) {                          // weights too: 0 * inf is not 0
       res[i] = sp.own(res[i]);
       if constexpr (J != Join::kNone) y[i] = sp.own(y[i]);
+      if constexpr (J == Join::kNorm) wo[i] = sp.own(wo[i]);
+      if (J != Join::kNone && gated) g[i] = sp.own(g[i]);
     }
   }
   float r[kCH][kN];
@@ -293,9 +296,9 @@ __global__ __launch_bounds__(kMaxThreads) void norm_bwd_kernel(NormArgs a) {
 #pragma unroll
   for (int i = 0; i < kCH; ++i) {
     const Span<T, kTiny> sp(i * nt + tid, a.cols);
-    if constexpr (J == Join::kNorm) wo[i] = sp.load(static_cast<const T*>(a.w_out), a.cols);
-    if (J != Join::kNone && gated) g[i] = sp.load(static_cast<const T*>(a.gate) + (int64_t)grp * a.cols, a.cols);
-    if constexpr (kZ) wi[i] = sp.load(static_cast<const T*>(a.w_in), a.cols);
+    if constexpr (J == Join::kNorm) wo[i] = sp.own(sp.load(static_cast<const T*>(a.w_out), a.cols));
+    if (J != Join::kNone && gated) g[i] = sp.own(sp.load(static_cast<const T*>(a.gate) + (int64_t)grp * a.cols, a.cols));
+    if constexpr (kZ) wi[i] = sp.own(sp.load(static_cast<const T*>(a.w_in), a.cols));
   }
   // This thread's sums, 0: a and 1: b, in registers or LDS.
   float sums[2][kCH][kN];

@@ -57,3 +57,46 @@ def test_moe_repeated_ids_of_an_expert_with_non_finite_weights(T, E, k, full, N,
     assert not torch.isfinite(y[named, ::3]).any()
     keep = torch.arange(K, device=DEV) % 3 != 0
     assert torch.equal(y[:, keep], clean[:, keep])
+
+
+# ------------------------------------------------------------------- norms
+
+# The last chunk of 8 (bf16) or 4 (fp32) of a ragged row is read from cols - 8 or cols - 4; at -2, -4 and -7 from the
+# end lie elements of its own and shared ones.
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [64, 67, 253, 515, 1000, 2051])
+@pytest.mark.parametrize("what", ["w_out", "gate"])
+def test_norm_infinite_weights_forward(dt, cols, what):
+    """One infinite weight or gate: its column of res_out is infinite, so the row's norm gives 0 there and everywhere,
+    but for inf * 0 in that column."""
+    for back in (2, 4, 7):
+        p = G.norm_inputs(5, cols, dt, "norm", True, 1, 7 * cols + back)
+        c = cols - back
+        p["y"][:, c] = 1.5
+        clean, _ = S.block_norm(**p, **G.CONST)
+        p[what].view(-1)[c] = math.inf
+        ro, z = S.block_norm(**p, **G.CONST)
+        others = torch.arange(cols, device=DEV) != c
+        assert torch.isinf(ro[:, c]).all() and torch.equal(ro[:, others], clean[:, others]), back
+        assert torch.isnan(z[:, c]).all() and (z[:, others] == 0).all(), back
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [64, 67, 515, 2051, 8201])
+@pytest.mark.parametrize("what", ["w_out", "gate", "w_in"])
+def test_norm_infinite_weights_backward(dt, cols, what):
+    """One infinite weight or gate: which elements of dres and dy are NaN, and which infinite, is as the formulas say."""
+    for back in (2, 4, 7):
+        rows, c = 3, cols - back
+        p = G.norm_inputs(rows, cols, dt, "norm", what == "w_in", 0 if what == "w_in" else 1, 9 * cols + back)
+        p[what].view(-1)[c] = math.inf
+        ro, dro = G.normal((rows, cols), 11, dt), G.normal((rows, cols), 12, dt)
+        dz = G.normal((rows, cols), 13, dt) if what == "w_in" else None
+        got = S.block_norm_bwd(ro, p["y"], p["w_out"], p["gate"], p["w_in"], dro, dz, **G.CONST)
+        with np.errstate(invalid="ignore"):
+            want, _ = B.block_norm_bwd(G.host(ro), *(G.host(p[n]) for n in ("y", "w_out", "gate", "w_in")), G.host(dro),
+                                       G.host(dz), **G.CONST)
+        for name, g, v in zip(("dres", "dy"), got, want):
+            g = G.host(g)
+            assert np.array_equal(np.isnan(g), np.isnan(v)), f"{name}, {back}: NaN"
+            assert np.array_equal(np.isinf(g), np.isinf(v)), f"{name}, {back}: infinite"
