@@ -36,6 +36,18 @@ def _rows(t: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
     return t.reshape(rows, cols).contiguous()
 
 
+def _rows16(t: torch.Tensor, rows: int, cols: int) -> tuple[torch.Tensor, int]:
+    """The same and its address, on a 16-byte boundary as the library takes logits: a slice that starts elsewhere is
+    copied."""
+    if t.dim() != 2 or not t.is_contiguous():
+        t = t.reshape(rows, cols).contiguous()
+    at = t.data_ptr()
+    if at & 15:
+        t = t.clone()
+        at = t.data_ptr()
+    return t, at
+
+
 def _lead(t: torch.Tensor, lead, cols: int) -> torch.Tensor:
     """[rows, cols] back to [*lead, cols]."""
     return t if len(lead) == 1 else t.reshape(*lead, cols)
@@ -74,11 +86,11 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", renorm: bool = T
         _check_out(w, "weights", (T, k), torch.float32, logits.device)
         _check_out(ids, "ids", (T, k), torch.int32, logits.device)
     _on_gpu(logits)
-    l2 = _rows(logits, T, E)
+    l2, at = _rows16(logits, T, E)   # l2: the copy, if one was made, lives until the launch
     if out is None:
         w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
         ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    check("swiglu_route_fwd", lib().swiglu_route_fwd(sc, int(renorm), dt, T, E, k, _p(l2), float(scale), _p(w),
+    check("swiglu_route_fwd", lib().swiglu_route_fwd(sc, int(renorm), dt, T, E, k, at, float(scale), _p(w),
                                                      _p(ids), _stream(logits)))
     return _lead(w, lead, k), _lead(ids, lead, k)
 
@@ -86,7 +98,7 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", renorm: bool = T
 def route_bwd(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, score: str = "softmax",
               renorm: bool = True, scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
     """dlogits [..., E] (dtype of logits) of L = sum(dweights * weights), with (weights, ids) = route(logits, ...);
-    score, renorm and scale as given there.  `out` may pass a preallocated [T, E]."""
+    score, renorm and scale as given there.  `out` may pass a preallocated [T, E], on a 16-byte boundary."""
     dt, sc = _dtype_code(logits), _score_code(score)
     if ids.dim() < 1:
         raise ValueError("ids must be [..., k]")
@@ -101,9 +113,10 @@ def route_bwd(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, s
     if out is not None:
         _check_out(out, "out", (T, E), logits.dtype, logits.device)
     _on_gpu(logits)
-    l2, i2, d2 = _rows(logits, T, E), _rows(ids, T, k), _rows(dweights, T, k)
+    l2, at = _rows16(logits, T, E)
+    i2, d2 = _rows(ids, T, k), _rows(dweights, T, k)
     d = out if out is not None else torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    check("swiglu_route_bwd", lib().swiglu_route_bwd(sc, int(renorm), dt, T, E, k, _p(l2), float(scale), _p(i2),
+    check("swiglu_route_bwd", lib().swiglu_route_bwd(sc, int(renorm), dt, T, E, k, at, float(scale), _p(i2),
                                                      _p(d2), _p(d), _stream(logits)))
     return _lead(d, lead, E)
 

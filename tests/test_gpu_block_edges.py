@@ -100,3 +100,17 @@ def test_norm_infinite_weights_backward(dt, cols, what):
             g = G.host(g)
             assert np.array_equal(np.isnan(g), np.isnan(v)), f"{name}, {back}: NaN"
             assert np.array_equal(np.isinf(g), np.isinf(v)), f"{name}, {back}: infinite"
+
+
+# ------------------------------------------------------------------ router
+
+@pytest.mark.parametrize("dt,E", [("bf16", 60), ("bf16", 5), ("f32", 5), ("f32", 130)])
+def test_route_takes_slices_that_start_anywhere(dt, E):
+    """Contiguous slices whose first element is not on a 16-byte boundary."""
+    l, dw = G.normal((9, E), E, dt, 1.5), G.normal((8, 3), 5, "f32")
+    part = l[1:]
+    assert part.is_contiguous() and part.data_ptr() % 16 != 0
+    w, ids = S.route(part, 3)
+    want = S.route(part.clone(), 3)
+    assert torch.equal(w, want[0]) and torch.equal(ids, want[1])
+    assert torch.equal(S.route_bwd(part, ids, dw), S.route_bwd(part.clone(), ids, dw))
