@@ -37,8 +37,6 @@
 // Which experts are in use, and by which tokens, every workgroup finds from
 // ids itself: from up to 64 ids without LDS or barriers (kFew), from up to
 // 1024 through a token mask per expert in LDS.
-#include <algorithm>
-
 #include "block.hpp"
 #include "common.hpp"
 #include "validate.hpp"
@@ -80,8 +78,9 @@ __device__ __forceinline__ int nth_set_bit(uint64_t m, int n) {
 // The sequence of (expert in use, pass) and who uses the expert.  A pass
 // takes at most kCap of an expert's tokens; an expert with more has several,
 // each of which reads its weights again.  All values are the same in every
-// lane unless said otherwise.
-template <bool kFew, int kCap> struct Route;
+// lane unless said otherwise.  kPairs: with the pairs' ids and weights (id_of,
+// weight_of), which the first product does not need.
+template <bool kFew, int kCap, bool kPairs> struct Route;
 
 // Passes of n tokens.
 template <int kCap> __device__ __forceinline__ int passes_of(int n) { return (n + kCap - 1) / kCap; }
@@ -111,19 +110,19 @@ __device__ __forceinline__ int lane_of(int count, int lane, int& n, int& sum) {
 
 // Up to 64 (token, choice) pairs: lane p holds the id of pair p, and, where p
 // is the first pair that names its expert, the expert's passes.
-template <int kCap> struct Route<true, kCap> {
+template <int kCap, bool kPairs> struct Route<true, kCap, kPairs> {
   struct Shared {};
   int id, k, T, lane;
   int passes, before;                            // per lane: of its expert; tokens of the experts before it
   float weight;                                  // per lane: of pair `lane`
   uint64_t first;                                // lanes with passes
-  __device__ __forceinline__ void init(Shared&, const MoeArgs& a, int tid, bool weights) {
+  __device__ __forceinline__ void init(Shared&, const MoeArgs& a, int tid) {
     const int pairs = a.T * a.k;
     lane = tid & 63;
     k = a.k;
     T = a.T;
     id = lane < pairs ? a.ids[lane] : -1;
-    weight = weights && lane < pairs ? a.weights[lane] : 0.0f;
+    weight = kPairs && lane < pairs ? a.weights[lane] : 0.0f;
     if (id < 0 || id >= a.E) id = -1;
     uint64_t same = ~0ull;                       // lanes with this lane's id
 #pragma unroll
@@ -174,15 +173,19 @@ template <int kCap> struct Route<true, kCap> {
   __device__ __forceinline__ float weight_of(int pair) const { return __shfl(weight, pair); }
 };
 
-template <int kCap> struct Route<false, kCap> {
-  struct Shared {
+template <bool kPairs> struct PairsOf {
+  int ids[kMaxPairs];
+  float weights[kMaxPairs];
+};
+template <> struct PairsOf<false> {};
+
+template <int kCap, bool kPairs> struct Route<false, kCap, kPairs> {
+  struct Shared : PairsOf<kPairs> {
     uint32_t mask[kMaxExperts][2];               // tokens of each expert
-    int ids[kMaxPairs];
-    float weights[kMaxPairs];
   };
   const Shared* s;
   int E, lane;
-  __device__ __forceinline__ void init(Shared& sh, const MoeArgs& a, int tid, bool weights) {
+  __device__ __forceinline__ void init(Shared& sh, const MoeArgs& a, int tid) {
     s = &sh;
     E = a.E;
     lane = tid & 63;
@@ -190,8 +193,10 @@ template <int kCap> struct Route<false, kCap> {
     __syncthreads();
     for (int p = tid; p < a.T * a.k; p += blockDim.x) {
       const int id = a.ids[p], t = p / a.k;
-      sh.ids[p] = id;
-      if (weights) sh.weights[p] = a.weights[p];
+      if constexpr (kPairs) {
+        sh.ids[p] = id;
+        sh.weights[p] = a.weights[p];
+      }
       if (id >= 0 && id < a.E) atomicOr(&sh.mask[id][t >> 5], 1u << (t & 31));
     }
     __syncthreads();
@@ -362,7 +367,7 @@ __device__ __forceinline__ void multiply(const u32x4* tile, const u32x4 (&b)[kG]
 constexpr int kUpWaves = 8;
 // Waves per SIMD: the operands of more token groups take more registers.
 template <int kG> constexpr int kUpOcc = kG == 1 ? 4 : kG == 2 ? 3 : 2;
-template <bool kFew, int kG> using UpRoute = Route<kFew, 16 * kG>;
+template <bool kFew, int kG> using UpRoute = Route<kFew, 16 * kG, false>;
 
 template <Act A, bool kFew, int kG>
 __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeArgs a) {
@@ -372,7 +377,7 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nw = blockDim.x >> 6, r16 = lane & 15, q4 = lane >> 4;
   R route;
-  route.init(shared, a, tid, false);
+  route.init(shared, a, tid);
   // This workgroup's share of the (pass, tile) sequence.
   const int ntiles = (a.N + 15) / 16;
   const int64_t total = (int64_t)route.count() * ntiles;
@@ -496,7 +501,7 @@ template <int kCols> constexpr int kTileRows = kCols < 16 ? kCols : 16;
 template <int kG, int kCols> constexpr int kDownWaves = kCols == 32 ? 8 : kG <= 2 ? 16 : kG == 4 ? 12 : 8;
 // Waves that fit a CU by their registers.
 template <int kG, int kCols> constexpr int kDownCuWaves = kG <= 2 ? 16 : kG == 4 && kCols < 32 ? 12 : 8;
-template <bool kFew, int kG> using DownRoute = Route<kFew, 8 * kG>;
+template <bool kFew, int kG> using DownRoute = Route<kFew, 8 * kG, true>;
 
 template <bool kFew, int kG, int kCols>
 __global__ __launch_bounds__((kDownWaves<kG, kCols> * 64)) void moe_down_kernel(MoeArgs a) {
@@ -510,7 +515,7 @@ __global__ __launch_bounds__((kDownWaves<kG, kCols> * 64)) void moe_down_kernel(
   float* ys = reinterpret_cast<float*>(lds + nw * kT * kTile);   // [wave][T][kCols]
   for (int i = tid; i < nw * a.T * kCols; i += blockDim.x) ys[i] = 0.0f;
   R route;
-  route.init(shared, a, tid, true);
+  route.init(shared, a, tid);
   __syncthreads();
   float* mine = ys + wave * a.T * kCols;
 
@@ -640,28 +645,33 @@ template <Act A, bool kFew, int kG>
 hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
   const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
   const int nslab = (a.K / 8 + kCPR - 1) / kCPR, ntiles = (a.N + 15) / 16;
-  // As many workgroups as are resident at once (256 CUs), or as there can be
-  // tiles (a second pass of an expert lengthens the shares, it adds no
-  // workgroups).  4 to 8 waves (a slab each at most): those with the shortest
-  // chain of slabs, tiles per workgroup times slabs per wave.  At 2 x 432
-  // tiles of 12 slabs 4 waves (1 x 3) take 19.6 us, 6 (2 x 2) 20.6.
+  // Tiles (8 KiB a wave) or sums (2 kG KiB a wave).
+  auto lds_of = [](int n) { return (size_t)n * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8); };
+  // As many workgroups as are resident at once by their registers and LDS
+  // (256 CUs), or as there can be tiles (a second pass of an expert lengthens
+  // the shares, it adds no workgroups).  4 to 8 waves (a slab each at most):
+  // those with the shortest chain of slabs, tiles per workgroup times slabs
+  // per wave.  At 2 x 432 tiles of 12 slabs 4 waves (1 x 3) take 19.6 us, 6
+  // (2 x 2) 20.6.  LDS is what binds from 65 pairs on, and a workgroup more
+  // than it holds is a second round: 64 tokens of 64 x (256, 1536), four of 40
+  // KiB to a CU, 22.5 us; with the pairs' ids and weights in it too (48 KiB,
+  // three to a CU) 27.6.
   const int64_t tiles = (int64_t)ntiles * slots;
   int nw = 0;
   int64_t resident = 0, best = 0;
   for (int n = nslab < kUpWaves ? nslab : kUpWaves; n >= 4 || nw == 0; --n) {
-    const int64_t res = 256 * (4 * kUpOcc<kG> / n), chain = (tiles + res - 1) / res * ((nslab + n - 1) / n);
+    const int64_t res = 256 * moe_resident(n, 4 * kUpOcc<kG>, lds_of(n) + sizeof(typename UpRoute<kFew, kG>::Shared));
+    const int64_t chain = (tiles + res - 1) / res * ((nslab + n - 1) / n);
     if (nw == 0 || chain < best) {
       nw = n;
       resident = res;
       best = chain;
     }
   }
-  constexpr size_t most = (size_t)kUpWaves * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);
-  const size_t lds = (size_t)nw * 64 * 16 * (2 * kG > 8 ? 2 * kG : 8);   // tiles (8 KiB a wave) or sums (2 kG KiB)
-  const hipError_t e = allow_lds<&moe_up_kernel<A, kFew, kG>>(most);
+  const hipError_t e = allow_lds<&moe_up_kernel<A, kFew, kG>>(lds_of(kUpWaves));
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((moe_up_kernel<A, kFew, kG>), dim3((unsigned)(tiles < resident ? tiles : resident)),
-                     dim3(nw * 64), lds, s, a);
+                     dim3(nw * 64), lds_of(nw), s, a);
   return hipGetLastError();
 }
 
@@ -679,7 +689,7 @@ hipError_t launch_down(const MoeArgs& a, hipStream_t s) {
   // about three slabs' time (4.5 us).
   int parts = 1;
   if (kCols >= 16) {
-    const int per_cu = std::max(1, std::min(kDownCuWaves<kG, kCols> / nw, (int)(160 * 1024 / (lds + sizeof(typename DownRoute<kFew, kG>::Shared)))));
+    const int per_cu = moe_resident(nw, kDownCuWaves<kG, kCols>, lds + sizeof(typename DownRoute<kFew, kG>::Shared));
     const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
     const int64_t units = (int64_t)slots * ((a.N / 8 + kCPR - 1) / kCPR);
     auto chain = [&](int64_t p) {

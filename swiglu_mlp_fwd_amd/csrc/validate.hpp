@@ -303,6 +303,15 @@ inline int64_t moe_parts(int64_t K, int64_t cols) {
   return blocks == 0 || blocks > kMoeFullBlocks ? 1 : (256 + blocks - 1) / blocks;
 }
 
+// Workgroups of `waves` waves and `lds` bytes of LDS (static and dynamic) that
+// a CU holds at a time, where `cu_waves` of their waves fit its registers; 1
+// at least.
+inline int moe_resident(int waves, int cu_waves, size_t lds) {
+  const int by_waves = cu_waves / waves, by_lds = lds == 0 ? by_waves : (int)(size_t(160 * 1024) / lds);
+  const int n = by_waves < by_lds ? by_waves : by_lds;
+  return n < 1 ? 1 : n;
+}
+
 // Workspace of the few-token experts, regions on 256-byte boundaries: the
 // hidden activations of T k (token, expert) entries, two bf16 each, and the
 // parts of y in fp32.
