@@ -498,13 +498,13 @@ __global__ __launch_bounds__(kUpWaves * 64, kUpOcc<kG>) void moe_up_kernel(MoeAr
 template <int kCols> constexpr int kTileRows = kCols < 16 ? kCols : 16;
 // Waves: the operands of more token groups take more registers, and the
 // waves' y of 32 columns more LDS.
-template <int kG, int kCols> constexpr int kDownWaves = kCols == 32 ? 8 : kG <= 2 ? 16 : kG == 4 ? 12 : 8;
+template <int kG> constexpr int kDownWaves = kG == 1 ? 16 : 8;
 // Waves that fit a CU by their registers.
-template <int kG, int kCols> constexpr int kDownCuWaves = kG <= 2 ? 16 : kG == 4 && kCols < 32 ? 12 : 8;
+template <int kG> constexpr int kDownCuWaves = kG <= 2 ? 16 : 8;
 template <bool kFew, int kG> using DownRoute = Route<kFew, 8 * kG, true>;
 
 template <bool kFew, int kG, int kCols>
-__global__ __launch_bounds__((kDownWaves<kG, kCols> * 64)) void moe_down_kernel(MoeArgs a) {
+__global__ __launch_bounds__((kDownWaves<kG> * 64)) void moe_down_kernel(MoeArgs a) {
   constexpr int kRows = kTileRows<kCols>, kT = kCols / kRows, kQ = kPieces<kRows>;
   extern __shared__ u32x4 lds[];
   using R = DownRoute<kFew, kG>;
@@ -677,7 +677,7 @@ hipError_t launch_up(const MoeArgs& a, hipStream_t s) {
 
 template <bool kFew, int kG, int kCols>
 hipError_t launch_down(const MoeArgs& a, hipStream_t s) {
-  constexpr int kMost = kDownWaves<kG, kCols>, kT = kCols / kTileRows<kCols>;
+  constexpr int kMost = kDownWaves<kG>, kT = kCols / kTileRows<kCols>;
   const int blocks = (a.K + kCols - 1) / kCols;
   // As many waves as the registers allow, or two workgroups of 8 per CU where
   // there are enough of them.
@@ -689,7 +689,7 @@ hipError_t launch_down(const MoeArgs& a, hipStream_t s) {
   // about three slabs' time (4.5 us).
   int parts = 1;
   if (kCols >= 16) {
-    const int per_cu = moe_resident(nw, kDownCuWaves<kG, kCols>, lds + sizeof(typename DownRoute<kFew, kG>::Shared));
+    const int per_cu = moe_resident(nw, kDownCuWaves<kG>, lds + sizeof(typename DownRoute<kFew, kG>::Shared));
     const int slots = a.E < a.T * a.k ? a.E : a.T * a.k;
     const int64_t units = (int64_t)slots * ((a.N / 8 + kCPR - 1) / kCPR);
     auto chain = [&](int64_t p) {
@@ -711,20 +711,23 @@ hipError_t launch_up_act(Act act, const MoeArgs& a, hipStream_t s) {
   return act == Act::kGeluTanh ? launch_up<Act::kGeluTanh, kFew, kG>(a, s) : launch_up<Act::kSilu, kFew, kG>(a, s);
 }
 
-// 16 columns of y to a workgroup.  A slab's token operands are as many bytes
-// per 8 tokens as its weights for 16 columns, so from 4 tokens per expert on
-// 32 columns.  The whole call, 32 against 16: 48 tokens of 13 x (3456, 2304),
-// 4 each, 174 us against 191; 64 of 64 x (1024, 4096), 8 each, 258 against
-// 279; 64 of 64 x (1024, 2048), 8 each, the same.  With fewer tokens 8
-// columns, where 16 would need a split and 8 do not: at K = 2048 with 2
-// tokens per expert the kernel takes 46 us against 49 (with the parts' sum).
+// Columns of y to a workgroup, by the token groups of a pass.
+// kG 2 and 4 (more than 8 tokens, 4 or more per expert): 32.  A slab's token
+//   operands are as many bytes per 8 tokens as its weights for 16 columns.  The
+//   whole call, 32 against 16: 48 tokens of 13 x (3456, 2304), 4 each, 174 us
+//   against 191; 64 of 64 x (1024, 4096), 8 each, 258 against 279; 64 of 64 x
+//   (1024, 2048), 8 each, the same.
+// kG 1: 16, or with fewer than 4 tokens per expert 8, where 16 would need a
+//   split and 8 do not: at K = 2048 with 2 tokens per expert the kernel takes
+//   46 us against 49 (with the parts' sum).
+// kG 8 (over 32 tokens, 17 or more per expert): 16; with 32 the kernel takes,
+//   parts' sum included, 47 us against 53 at 64 tokens of 8 x (2048, 4096),
+//   4 each, 50 against 61 at 8 x (8192, 1024).
 template <bool kFew, int kG>
 hipError_t launch_down_cols(const MoeArgs& a, hipStream_t s) {
   if constexpr (kG == 1)
     if (moe_parts(a.K, 16) > 1 && a.K > 8 * kMoeFullBlocks && a.T * a.k < 4 * a.E) return launch_down<kFew, 1, 8>(a, s);
-  if constexpr (kG == 2 || kG == 4)
-    if (a.T * a.k >= 4 * a.E) return launch_down<kFew, kG, 32>(a, s);
-  return launch_down<kFew, kG, 16>(a, s);
+  return launch_down<kFew, kG, kG == 2 || kG == 4 ? 32 : 16>(a, s);
 }
 
 // Tokens of one expert that a pass takes: all that there can be where T is

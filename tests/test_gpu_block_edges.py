@@ -114,3 +114,23 @@ def test_route_takes_slices_that_start_anywhere(dt, E):
     want = S.route(part.clone(), 3)
     assert torch.equal(w, want[0]) and torch.equal(ids, want[1])
     assert torch.equal(S.route_bwd(part, ids, dw), S.route_bwd(part.clone(), ids, dw))
+
+
+# ------------------------------------------------- launch variants and sizes
+
+@pytest.mark.parametrize("spread", ["even", "holes"])
+@pytest.mark.parametrize("T,E,k,N,K", [
+    (40, 2, 1, 136, 200), (64, 3, 1, 72, 264), (33, 1, 1, 264, 1032),        # up to 64 pairs, over 16 an expert
+    (64, 3, 1, 200, 4104), (64, 4, 4, 136, 520),
+    (48, 13, 4, 456, 1304), (64, 8, 2, 264, 2056), (30, 4, 2, 520, 712)])     # 32 columns to a workgroup
+def test_moe_many_tokens_for_each_expert(T, E, k, N, K, spread):
+    G.moe_case(T, E, k, N, K, 800 + T + E, spread=spread)
+
+
+@pytest.mark.parametrize("T,E,k,N,K", [(1, 8, 2, 136, 256), (8, 8, 2, 72, 4104), (24, 6, 3, 136, 264), (64, 16, 4, 72, 520),
+                                       (48, 13, 4, 456, 1304), (40, 2, 1, 264, 1032)])
+def test_moe_stays_inside_its_workspace(T, E, k, N, K):
+    x, wg, wu, wd, ids, w, y = G.moe_case(T, E, k, N, K, 820 + T)
+    ws, yg = guarded((S.moe_workspace_bytes(T, N, K, k),), torch.uint8), guarded((T, K), torch.bfloat16)
+    assert torch.equal(S.moe_fwd(x, wg, wu, wd, ids, w, workspace=ws.t, out=yg.t), y)
+    check_guards("moe workspace", ws, yg)
