@@ -117,7 +117,6 @@ struct Span {
 
 // Lanes of a row: 16, 32 or 64 of a wave, or (kWide) every thread of the workgroup.
 constexpr int kWide = 0;
-constexpr int kThreads = 512;                    // workgroups of several rows
 constexpr int kMaxThreads = 1024;
 
 // The sum over the 16 lanes of a DPP row, in each of them.
@@ -590,7 +589,7 @@ template <typename T, int kL, int kCH, Join J, bool kZ, bool kTiny = false>
 hipError_t launch_cfg(bool fwd, NormArgs a, hipStream_t s) {
   constexpr int kN = Ch<T>::kN;
   const int nch = (a.cols + kN - 1) / kN;
-  int threads = ((nch + kCH - 1) / kCH + 63) / 64 * 64;
+  int threads = norm_wide_threads(nch, kCH);
   if (fwd) {
     const int R = kL == kWide ? 1 : 256 / (kL == kWide ? 1 : kL);
     if (kL != kWide) threads = 256;
@@ -598,21 +597,10 @@ hipError_t launch_cfg(bool fwd, NormArgs a, hipStream_t s) {
                        dim3(threads), 0, s, a);
     return hipGetLastError();
   }
-  const int64_t groups = a.groups > 0 ? a.groups : 1, rpg = a.rows / groups;
-  const int R = kL == kWide ? 1 : kThreads / (kL == kWide ? 1 : kL);
-  if (kL != kWide) threads = kThreads;
-  // Parts: two workgroups of 512 threads per CU, more of smaller ones (512
-  // against 1024 parts: 8192 x 4096 bf16 98 against 102 us with the sums of
-  // the parts, 32768 x 1024 154 against 97); then as few as give every part
-  // as many turns as the longest has.
-  int64_t per = norm_parts((int64_t)threads * 8) / groups;
-  if (per < 1) per = 1;
-  // Beyond 512 rows at a time a part has three turns at least: a turn more
-  // costs less than the sum of as many more parts (1692 x 395 fp32 in 4 groups
-  // 15.5 us in all against 19.2, 996 x 1864 bf16 16.7 against 18.7).
-  int64_t turns = (rpg + R * per - 1) / (R * per);
-  if (turns < 3 && a.rows > 512 * R) turns = 3;
-  a.per_group = (int)((rpg + R * turns - 1) / (R * turns));
+  const int64_t groups = a.groups > 0 ? a.groups : 1;
+  const int R = kL == kWide ? 1 : kNormThreads / (kL == kWide ? 1 : kL);
+  if (kL != kWide) threads = kNormThreads;
+  a.per_group = (int)norm_bwd_parts((int)sizeof(T), a.rows, a.cols, a.groups);
   const size_t lds = kSumsInLds<T, kL, kCH> ? (size_t)2 * kCH * kN * threads * 4 : kL == kWide ? 0 : (size_t)R * a.cols * 4;
   // Next-row loads where the 128 registers of a thread hold two rows: with
   // two fp32 chunks each they do not, 2048 x 8192 107 us with them, 87 without.
@@ -638,15 +626,14 @@ hipError_t launch_cols(bool fwd, const NormArgs& a, hipStream_t s) {
   constexpr int kN = Ch<T>::kN;
   const int nch = (a.cols + kN - 1) / kN;
   if (a.cols < kN) return launch_cfg<T, 16, 1, J, kZ, true>(fwd, a, s);
-  if (nch <= 16) return launch_cfg<T, 16, 1, J, kZ>(fwd, a, s);
-  if (nch <= 32) return launch_cfg<T, 32, 1, J, kZ>(fwd, a, s);
-  if (nch <= 64) return launch_cfg<T, 64, 1, J, kZ>(fwd, a, s);
-  if (fwd && a.rows > 512 && nch > 256 && nch <= 2048) return launch_cfg<T, kWide, 2, J, kZ>(fwd, a, s);
-  if (nch <= 1024) return launch_cfg<T, kWide, 1, J, kZ>(fwd, a, s);
-  if (nch <= 2048) return launch_cfg<T, kWide, 2, J, kZ>(fwd, a, s);
-  if constexpr (sizeof(T) == 4) {
-    if (nch <= 4096) return launch_cfg<T, kWide, 4, J, kZ>(fwd, a, s);
-  }
+  const int lanes = norm_lanes(nch), chunks = norm_chunks(nch);
+  if (lanes == 16) return launch_cfg<T, 16, 1, J, kZ>(fwd, a, s);
+  if (lanes == 32) return launch_cfg<T, 32, 1, J, kZ>(fwd, a, s);
+  if (lanes == 64) return launch_cfg<T, 64, 1, J, kZ>(fwd, a, s);
+  if (fwd && a.rows > 512 && nch > 256 && chunks == 1) return launch_cfg<T, kWide, 2, J, kZ>(fwd, a, s);
+  if (chunks == 1) return launch_cfg<T, kWide, 1, J, kZ>(fwd, a, s);
+  if (chunks == 2) return launch_cfg<T, kWide, 2, J, kZ>(fwd, a, s);
+  if constexpr (sizeof(T) == 4) return launch_cfg<T, kWide, 4, J, kZ>(fwd, a, s);
   return hipErrorInvalidValue;                   // past the checked number of columns
 }
 

@@ -31,8 +31,32 @@ static void resident() {
         "first product");
 }
 
+// The backward's parts: no more than the workspace has room for, and every
+// row in one part's turn, for both element sizes and every launch shape.
+static void parts() {
+  using namespace swg;
+  const int64_t cols[] = {1, 7, 8, 64, 65, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1024, 1864, 2048, 2051, 4096, 4097,
+                          6001, 8192, 8193, 8201, 12288, 12289, 16383, 16384};
+  const int64_t per_group[] = {1, 2, 3, 7, 16, 33, 170, 171, 511, 512, 513, 1024, 1537, 2048, 5000, 16385, 65536};
+  for (int64_t c : cols)
+    for (int64_t g : {0, 1, 2, 3, 5, 16, 17, 511, 512, 513, 2048, 2100, 1 << 20})
+      for (int64_t n : per_group) {
+        const int64_t rows = n * (g > 0 ? g : 1), groups = g > 0 ? g : 1;
+        if (norm_shape_status(rows, c, g) != SWIGLU_OK) continue;
+        const size_t total = norm_bwd_workspace_total(rows, c, g);
+        check(total == (size_t)(2 * groups * norm_most_parts(rows, c, g) * c * 4 + 255) / 256 * 256, "norm workspace");
+        for (int elem : {2, 4}) {
+          const int64_t nch = (c * elem + 15) / 16, per = norm_bwd_parts(elem, rows, c, g);
+          check(per >= 1 && per <= n && (size_t)(2 * groups * per * c * 4) <= total, "norm parts fit the workspace");
+          check(norm_lanes(nch) || norm_wide_threads(nch, norm_chunks(nch)) <= 1024, "norm threads");
+        }
+      }
+  check(norm_bwd_parts(2, 0, 64, 3) == 0 && norm_bwd_workspace_total(0, 64, 3) == 0, "no rows");
+}
+
 int main() {
   resident();
+  parts();
   if (failures) return 1;
   printf("block rules: ok\n");
   return 0;
