@@ -12,6 +12,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._lib import MAX_EXPERTS, MAX_TOPK, MOE_MAX_TOKENS, SWIGLU_SCORE_SIGMOID, SWIGLU_SCORE_SOFTMAX, check, lib
 from .ops import _act_code, _check_out, _dtype_code, _on_gpu, _p, _same
@@ -317,7 +318,8 @@ def block_norm_bwd(res_out: torch.Tensor | None, y: torch.Tensor | None = None, 
 
 
 class RouterFunction(torch.autograd.Function):
-    """Autograd wrapper of route: gradients of the weights; ids have none."""
+    """Autograd wrapper of route: gradients of the weights; ids have none.  The gradients have no derivative of their
+    own (asking for one raises)."""
 
     @staticmethod
     def forward(ctx, logits, k, score="softmax", renorm=True, scale=1.0):
@@ -328,6 +330,7 @@ class RouterFunction(torch.autograd.Function):
         return w, ids
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dw, _):
         logits, ids = ctx.saved_tensors
         score, renorm, scale = ctx.cfg
@@ -340,7 +343,8 @@ def router(logits, k: int, score: str = "softmax", renorm: bool = True, scale: f
 
 
 class BlockNormFunction(torch.autograd.Function):
-    """Autograd wrapper of block_norm; the constants skip, scale, w_offset and eps are not trained."""
+    """Autograd wrapper of block_norm; the constants skip, scale, w_offset and eps are not trained.  The gradients have
+    no derivative of their own (asking for one raises)."""
 
     @staticmethod
     def forward(ctx, res, y, w_out, gate, w_in, skip=1.0, scale=1.0, w_offset=0.0, eps=1e-6):
@@ -352,6 +356,7 @@ class BlockNormFunction(torch.autograd.Function):
         return ro, z
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dro, dz):
         ro, y, w_out, gate, w_in = ctx.saved_tensors
         if w_in is not None and dz is None:
