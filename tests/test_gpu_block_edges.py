@@ -134,3 +134,24 @@ def test_moe_stays_inside_its_workspace(T, E, k, N, K):
     ws, yg = guarded((S.moe_workspace_bytes(T, N, K, k),), torch.uint8), guarded((T, K), torch.bfloat16)
     assert torch.equal(S.moe_fwd(x, wg, wu, wd, ids, w, workspace=ws.t, out=yg.t), y)
     check_guards("moe workspace", ws, yg)
+
+
+@pytest.mark.parametrize("dt,rows,cols,groups", [
+    ("bf16", 530, 8201, 1), ("bf16", 530, 8201, 2), ("f32", 530, 4101, 2), ("f32", 530, 8201, 0), ("f32", 530, 8201, 2),
+    ("bf16", 600, 2051, 1), ("bf16", 600, 2051, 4), ("f32", 600, 2051, 2), ("bf16", 1540, 4096, 1)])
+def test_norm_long_rows_by_several_to_a_workgroup(dt, rows, cols, groups):
+    """Forward rows of two chunks to a thread, and backward parts of two or three rows, in an exact workspace."""
+    p = G.norm_inputs(rows, cols, dt, "norm", True, groups, rows + cols + groups)
+    G.check_norm(p, dt, f"norm {dt} {rows}x{cols} {groups} groups")
+    ro, z = S.block_norm(**p, **G.CONST)
+    first = S.block_norm_bwd(ro, p["y"], p["w_out"], p["gate"], p["w_in"], z, ro, **G.CONST)
+    ws = guarded((S.block_norm_bwd_workspace_bytes(rows, cols, groups),), torch.uint8)
+    again = S.block_norm_bwd(ro, p["y"], p["w_out"], p["gate"], p["w_in"], z, ro, **G.CONST, workspace=ws.t)
+    assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(first, again))
+    check_guards("norm workspace", ws)
+
+
+@pytest.mark.parametrize("join,pre,groups", [("plain", True, 2), ("plain", False, 1), ("norm", False, 2), ("none", True, 0)])
+@pytest.mark.parametrize("dt,cols", [("bf16", 8201), ("f32", 8201), ("f32", 4101)])
+def test_norm_long_rows_of_other_forms(dt, cols, join, pre, groups):
+    G.check_norm(G.norm_inputs(522, cols, dt, join, pre, groups, cols + groups), dt, f"norm {dt} {join} {pre} {groups} {cols}")
