@@ -171,8 +171,8 @@ __device__ __forceinline__ float rstd_of(float sumsq, int cols, float eps) {
 enum class Join { kNone, kPlain, kNorm };
 
 // Bound by HBM: 8192 x 4096 bf16 with both norms (two tensors read, two
-// written, 268 MB) 41 to 45 us, 5.9 to 6.5 TB/s, where a copy reaches 5.1.  A
-// few rows are bound by the chain load, sum, sum, store: 8 x 4096 3.7 us.
+// written, 268 MB) 45 to 48 us, 5.6 to 6.0 TB/s, where a copy reaches 5.1.  A
+// few rows are bound by the chain load, sum, sum, store: 8 x 4096 3.5 us.
 template <typename T, int kL, int kCH, Join J, bool kZ, bool kTiny>
 __global__ __launch_bounds__(kMaxThreads) void norm_fwd_kernel(NormArgs a) {
   constexpr int kN = Ch<T>::kN;
@@ -618,9 +618,9 @@ hipError_t launch_cfg(bool fwd, NormArgs a, hipStream_t s) {
 // As few lanes as hold a row one chunk each: 65536 rows of 256 bf16 columns
 // forward 23 us on 32 lanes against 35 on 64, backward 36 against 56; of 128
 // columns forward 12.8 on 16 lanes against 35.  Long forward rows take two
-// chunks to a thread where there are rows enough: 8192 x 4096 bf16 41 us
-// against 43, 2048 x 8192 24 against 27, 8192 x 4096 fp32 91 against 96, with
-// 1024 rows the same, and with fewer the shorter chain of one chunk counts.
+// chunks to a thread where there are rows enough: 8192 x 4096 bf16 47.8 us
+// against 50.2, 2048 x 8192 26.6 against 30.6, 8192 x 4096 fp32 98 against 104,
+// with 1024 rows the same, and with fewer the shorter chain of one chunk counts.
 template <typename T, Join J, bool kZ>
 hipError_t launch_cols(bool fwd, const NormArgs& a, hipStream_t s) {
   constexpr int kN = Ch<T>::kN;

@@ -27,10 +27,12 @@
 // its index make one key, so that a comparison settles ties too (Key below);
 // each lane sorts its keys once, and a choice is the maximum of the lanes'
 // first keys (on DPP moves for up to 16 lanes), after which its lane moves up
-// by one.  32768 x 128, k = 8, bf16 7.1 us, fp32 11.2 (10.5 and 18.9 MB at
-// 1.5 and 1.7 TB/s: the sort and the choices bound it, in fp32 their fp64
-// keys); with maxima over all of a lane's logits per choice 10.8 and 11.5;
-// with one wave per token and shuffles through LDS 38 (fp32).
+// by one.  32768 x 128, k = 8, bf16 6.9 us, fp32 10.5 (10.5 and 18.9 MB at
+// 1.5 and 1.8 TB/s: the sort and the choices bound it, in fp32 their fp64
+// keys).  Earlier forms: maxima over all of a lane's logits per choice 10.8 and
+// 11.5; one wave per token and shuffles through LDS 38 (fp32).
+// Times in this file are a launch's in a graph of 12 inputs in turn, in all
+// more than the caches hold; where they hold them it is up to a fifth less.
 //
 // Chunks of 16 bytes load at any element's address; the one that would pass
 // the row's end loads from E - kN instead and skips what its neighbour has.
@@ -333,7 +335,7 @@ __global__ __launch_bounds__(kThreads) void route_fwd_kernel(RouteArgs a) {
 // The gradient: the chosen logits and their weights again from the logits, a
 // sum over the choice, and for a plain softmax one over the row, which every
 // form reads: a NaN in it is one in all of its gradients.  32768 x 128, k = 8:
-// bf16 8.5 us (18.9 MB, 2.2 TB/s), fp32 9.7 (35.7 MB, 3.7 TB/s), of which 4.5
+// bf16 10.6 us (18.9 MB, 1.8 TB/s), fp32 14.5 (35.7 MB, 2.5 TB/s), of which 4
 // are a latency that 2048 tokens take too.
 template <typename T, Score S, int kL, int kC, bool kTiny>
 __global__ __launch_bounds__(kThreads) void route_bwd_kernel(RouteArgs a) {
@@ -442,14 +444,15 @@ hipError_t launch_lanes(bool fwd, const RouteArgs& a, hipStream_t s) {
 }
 
 // 8 logits to a lane: 8 to 64 lanes for up to 512 experts, 16 beyond.
-// 32768 x 128, k = 8, forward: 7.5 us bf16 and 11.4 fp32, with 16 logits to
-// a lane 9.3 and 13.8 (a longer sort), with 4 (32 lanes, half without logits)
-// 12.2 and 19.2; backward with 8 or 16 alike (8.5 and 8.3; 9.7 and 9.1).
+// 32768 x 128, k = 8, forward: 6.9 us bf16 and 10.5 fp32, with 16 logits to
+// a lane 8.8 and 13.2 (a longer sort), with 4 (32 lanes, half without logits)
+// 11.6 and 17.7; backward with 8 or 16 nearly alike (10.6 and 10.7; 14.5 and
+// 14.9), with 4 15.8 and 17.2.
 // Fewer than 8 lanes for up to 32 experts, only where tokens fill the chip
 // all the same: 524288 x 8 bf16 on one lane each forward 7.1 us and backward
 // 9.4, on 8 27 and 26; 131072 x 32 on 4 lanes 9.0 and 10.3, on 8 12.6 and
 // 13.5; 32768 x 8 3.2 and 4.6 against 4.1 and 4.6; but 8 x 8 2.7 and 3.7
-// against 1.8 and 2.2 (a lane's longer chain).
+// against 1.8 and 2.2 (a lane's longer chain; these by a kernel trace).
 constexpr int kManyTokens = 32768;
 template <typename T, Score S>
 hipError_t launch_v(bool fwd, const RouteArgs& a, hipStream_t s) {
