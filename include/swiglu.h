@@ -517,6 +517,152 @@ int swiglu_block_norm_bwd(int dtype, int64_t rows, int64_t cols, int64_t groups,
                           void* dres, void* dy, void* dw_out, void* dgate, void* dw_in,
                           void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The routed block over any number of tokens: rows in order of expert, the
+ * products of each run of rows with its expert's weights, their gradients.
+ * ------------------------------------------------------------------------ */
+
+/* Bytes of device workspace swiglu_expert_plan needs (0 for sizes it rejects
+ * and for up to 8192 pairs, which need none). */
+size_t swiglu_expert_plan_workspace_bytes(int64_t T, int64_t k, int64_t E);
+
+/* The order of T * k pairs (token, choice) by expert: pair p = t * k + j of
+ * expert ids[t, j] gets a row, the rows of expert 0 first, those of one expert
+ * in order of their pairs.  A pair whose id is outside [0, E) was dropped: the
+ * dropped pairs' rows lie behind the last expert's, in order of the pairs, and
+ * are named by complements.
+ *   offsets[e]   the first row of expert e; offsets[E] the rows of all
+ *                experts, [E + 1]
+ *   src[r]       the pair of row r, ~pair (negative) for a dropped one, [T k]
+ *   pos[t, j]    the row of the pair, ~row for a dropped one, [T, k]
+ * The order is the same in every run.
+ *
+ *   ids          [T, k] int32, as swiglu_route_fwd gives them
+ *   workspace    swiglu_expert_plan_workspace_bytes(T, k, E) bytes, 256-byte
+ *                aligned (NULL where none is needed); scratch
+ * 1 <= E <= SWIGLU_MAX_EXPERTS, 1 <= k <= SWIGLU_MAX_TOPK, T * k < 2^31, else
+ * SWIGLU_ERR_SHAPE.  int32 arrays need 4-byte alignment. */
+int swiglu_expert_plan(int64_t T, int64_t k, int64_t E, const int32_t* ids, int32_t* offsets, int32_t* src,
+                       int32_t* pos, void* workspace, size_t workspace_bytes, void* stream);
+
+/* rows[r] = x[src[r] / k], zeros where src[r] is negative (or names no pair).
+ *   x [T, K], rows [T k, K] (dtype; rows of whole 16-byte chunks: K % 8 == 0
+ *   for bf16, K % 4 == 0 for fp32, else SWIGLU_ERR_SHAPE)
+ * T <= 2^23 and T * k * ceil(K / 512 (bf16) or 256) <= 2^25, else
+ * SWIGLU_ERR_UNSUPPORTED.  Its gradient is swiglu_expert_combine without
+ * weights. */
+int swiglu_expert_gather(int dtype, int64_t T, int64_t k, int64_t K, const void* x, const int32_t* src, void* rows,
+                         void* stream);
+
+/* y[t] = sum_j weights[t, j] * rows[pos[t, j]], in order of j, in fp32, rounded
+ * once; entries with a negative pos (or none of the rows) are left out.
+ *   rows [T k, K], y [T, K] (dtype); weights [T, k] fp32, or NULL for ones
+ * Sizes as swiglu_expert_gather. */
+int swiglu_expert_combine(int dtype, int64_t T, int64_t k, int64_t K, const void* rows, const int32_t* pos,
+                          const float* weights, void* y, void* stream);
+
+/* Gradients of swiglu_expert_combine:
+ *   drows[pos[t, j]] = weights[t, j] * dy[t]
+ *   dweights[t, j]   = sum over columns of dy[t] * rows[pos[t, j]]   (fp32)
+ * and zeros for a dropped pair: dweights and the row ~pos names.  With pos of
+ * swiglu_expert_plan every row of drows is written.  dweights may be NULL. */
+int swiglu_expert_combine_bwd(int dtype, int64_t T, int64_t k, int64_t K, const void* dy, const void* rows,
+                              const int32_t* pos, const float* weights, void* drows, float* dweights, void* stream);
+
+/* The gate/up stage of rows in order of expert: for the rows r of expert e,
+ * offsets[e] <= r < offsets[e + 1],
+ *   h[r] = act(x_r Wg_e^T) * (x_r Wu_e^T)
+ * with x_r = x[r], or, where src is given, x[src[r] / k] (the rows are gathered
+ * on the way; a negative src[r] stands for a row of zeros).  Rows of no expert
+ * (in front of offsets[0], behind offsets[E]) get zeros.  Products accumulate
+ * in fp32, h is rounded once; results are deterministic.
+ *
+ *   x            [R, K]; with src [T, K], R = T k
+ *   offsets      [E + 1] int32 on the device, not decreasing, within [0, R]
+ *                (values that break this give undefined rows of h, but no
+ *                access outside the arrays)
+ *   wg, wu       expert e's [N, K] at wg + e * wg_stride, wu + e * wu_stride
+ *                (elements), as swiglu_moe_fwd takes them
+ *   h            [R, N] (output)
+ * Layout rules: N and K whole 16-byte chunks (% 8 bf16, % 4 fp32), strides too
+ * and at least N * K (E > 1), else SWIGLU_ERR_SHAPE; 1 <= E <=
+ * SWIGLU_MAX_EXPERTS; 2 N and K below 2^22, and (R / 128 + E + 2) *
+ * ceil(max(N, K) / 64) and 2 E ceil(N / 128) ceil(K / 128) below 2^23, else
+ * SWIGLU_ERR_UNSUPPORTED; so is src with x of 2^31 bytes or more (gather the
+ * rows first). */
+int swiglu_grouped_fwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
+                       int64_t k, const int32_t* src, const int32_t* offsets, const void* wg, int64_t wg_stride,
+                       const void* wu, int64_t wu_stride, void* h, void* stream);
+
+/* Bytes of device workspace swiglu_grouped_bwd needs, with src or without
+ * (gathered; 0 for sizes it rejects). */
+size_t swiglu_grouped_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, int64_t K, int gathered);
+
+/* Gradients of swiglu_grouped_fwd, g and u computed again (as swiglu_bwd):
+ *   du = dh * act(g),  dg = dh * u * act'(g)       (rounded to dtype)
+ *   dx[r]  = dg[r] Wg_e + du[r] Wu_e     of the rows, also with src: the
+ *            tokens' gradients are swiglu_expert_combine of dx without weights
+ *   dwg[e] = sum over the expert's rows of dg[r]^T x_r,  dwu[e] of du[r]
+ * Rows of no expert have dx = 0 and are not read; experts without rows get
+ * dwg = dwu = 0.
+ *
+ *   dh           [R, N];  dx [R, K], or NULL if it is not wanted
+ *   dwg, dwu     [E, N, K] dense outputs, or both NULL
+ *   workspace    at least swiglu_grouped_bwd_workspace_bytes(...) bytes,
+ *                256-byte aligned; scratch
+ * Errors as the forward's; one of dwg, dwu alone: SWIGLU_ERR_ARG. */
+int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
+                       int64_t k, const int32_t* src, const int32_t* offsets, const void* wg, int64_t wg_stride,
+                       const void* wu, int64_t wu_stride, const void* dh, void* dx, void* dwg, void* dwu,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* y[r] = x[r] W_e^T of rows in order of expert (the down projection of the
+ * routed MLP, or any linear layer with a weight per expert); rows of no expert
+ * get zeros.
+ *   x [R, K], w: expert e's [N, K] at w + e * w_stride, y [R, N]
+ * Sizes, offsets and errors as swiglu_grouped_fwd. */
+int swiglu_grouped_mm(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, const int32_t* offsets,
+                      const void* w, int64_t w_stride, void* y, void* stream);
+
+/* Gradients of swiglu_grouped_mm: dx[r] = dy[r] W_e [R, K] (0 for rows of no
+ * expert), dw[e] = sum over the expert's rows of dy[r]^T x[r], [E, N, K] dense
+ * (0 without rows).  dx or dw may be NULL; x is read for dw only, w for dx. */
+int swiglu_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x,
+                          const int32_t* offsets, const void* w, int64_t w_stride, const void* dy, void* dx, void* dw,
+                          void* stream);
+
+/* Bytes of device workspace the norm and the clipping of `count` gradients
+ * need (0 for a count they reject). */
+size_t swiglu_grad_norm_workspace_bytes(int64_t count);
+
+/* norm = sqrt(sum of the squares of all elements of `count` tensors), the
+ * squares and their sum in fp64 (no overflow or underflow on the way), rounded
+ * to fp32.  An infinite element gives infinity, a NaN NaN.  No tensors: 0.
+ *
+ *   dtypes, grads, sizes   HOST arrays [count]: SWIGLU_F32 or SWIGLU_BF16, the
+ *                device pointer (aligned to an element; NULL for a size of 0)
+ *                and the elements of each dense tensor
+ *   norm         one float on the device
+ *   workspace    swiglu_grad_norm_workspace_bytes(count) bytes, 256-byte
+ *                aligned; scratch
+ * count <= 2^20, else SWIGLU_ERR_SHAPE; sizes <= 2^35 each, else
+ * SWIGLU_ERR_UNSUPPORTED.  The host arrays are read before the call returns. */
+int swiglu_grad_norm(int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes, float* norm,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same norm, and every gradient times f = min(1, max_norm / (norm + eps)),
+ * one fp32 product rounded to its type: in place (outs NULL; where f is 1 the
+ * gradients are not written), or to outs[i], dense tensors of the gradients'
+ * types and sizes (a HOST array; outs[i] may be grads[i]).  A norm that is NaN
+ * makes every gradient NaN; an infinite one makes finite elements 0 and
+ * infinite ones NaN.
+ * What is written must not overlap anything else that is read or written
+ * (a tensor given twice, say): SWIGLU_ERR_ARG.  max_norm and eps at least 0
+ * and not NaN, eps finite, else SWIGLU_ERR_ARG. */
+int swiglu_clip_grads(int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes,
+                      void* const* outs, double max_norm, double eps, float* norm, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 /* Measurement aid: the decode kernel's read-only twin.  The same launch as
  * swiglu_gemv_fwd for (M, N, K) -- the same kernel's grid, LDS footprint,
  * x loads and weight loads (and, for M >= 4, the weights' trip through LDS),

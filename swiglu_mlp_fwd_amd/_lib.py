@@ -82,6 +82,28 @@ SIGNATURES = {
                                              _c_ptr, _c_ptr, _c_ptr, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                              ctypes.c_float, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
                                              ctypes.c_size_t, _c_ptr]),
+    "swiglu_expert_plan_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64, _c_i64]),
+    "swiglu_expert_plan": (ctypes.c_int, [_c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                          ctypes.c_size_t, _c_ptr]),
+    "swiglu_expert_gather": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+    "swiglu_expert_combine": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr,
+                                             _c_ptr]),
+    "swiglu_expert_combine_bwd": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr,
+                                                 _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+    "swiglu_grouped_fwd": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_i64,
+                                          _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr]),
+    "swiglu_grouped_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _c_i64, _c_i64, _c_i64, ctypes.c_int]),
+    "swiglu_grouped_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_i64,
+                                          _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr,
+                                          _c_ptr, _c_ptr, _c_ptr, ctypes.c_size_t, _c_ptr]),
+    "swiglu_grouped_mm": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64,
+                                         _c_ptr, _c_ptr]),
+    "swiglu_grouped_mm_bwd": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr,
+                                             _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
+    "swiglu_grad_norm_workspace_bytes": (ctypes.c_size_t, [_c_i64]),
+    "swiglu_grad_norm": (ctypes.c_int, [_c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr, ctypes.c_size_t, _c_ptr]),
+    "swiglu_clip_grads": (ctypes.c_int, [_c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, ctypes.c_double, ctypes.c_double,
+                                         _c_ptr, _c_ptr, ctypes.c_size_t, _c_ptr]),
     "swiglu_probe_mfma": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _c_ptr, _c_ptr]),
     "swiglu_probe_gemv_read": (ctypes.c_int, [_c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),
     "swiglu_probe_act_quant_stream": (ctypes.c_int, [_c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, _c_ptr]),

@@ -6,6 +6,7 @@
 
 #include "block.hpp"
 #include "gemm.hpp"
+#include "grouped.hpp"
 #include "swiglu.h"
 #include "validate.hpp"
 
@@ -403,6 +404,188 @@ int swiglu_block_norm_bwd(int dtype, int64_t rows, int64_t cols, int64_t groups,
   a.dres = dres; a.dy = dy; a.dw_out = dw_out; a.dgate = dgate; a.dw_in = dw_in;
   a.part = static_cast<float*>(workspace);
   return hip_status(swg::launch_norm_bwd(as_dt(dtype), a, as_stream(stream)));
+}
+
+size_t swiglu_expert_plan_workspace_bytes(int64_t T, int64_t k, int64_t E) {
+  return swg::plan_workspace_total(T, k, E);
+}
+
+int swiglu_expert_plan(int64_t T, int64_t k, int64_t E, const int32_t* ids, int32_t* offsets, int32_t* src,
+                       int32_t* pos, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = swg::validate_plan(T, k, E, ids, offsets, src, pos, workspace, workspace_bytes);
+  if (st != SWIGLU_OK) return st;
+  swg::PlanArgs a{};
+  a.ids = ids; a.n = (int)(T * k); a.E = (int)E;
+  a.offsets = offsets; a.src = src; a.pos = pos;
+  a.hist = static_cast<int32_t*>(workspace);
+  return hip_status(swg::launch_plan(a, as_stream(stream)));
+}
+
+int swiglu_expert_gather(int dtype, int64_t T, int64_t k, int64_t K, const void* x, const int32_t* src, void* rows,
+                         void* stream) {
+  int st = swg::validate_rows(dtype, T, k, K, {x, rows}, {src}, {});
+  if (st != SWIGLU_OK || T == 0 || K == 0) return st;
+  return hip_status(swg::launch_gather(as_dt(dtype), (int)T, (int)k, (int)K, x, src, rows, as_stream(stream)));
+}
+
+int swiglu_expert_combine(int dtype, int64_t T, int64_t k, int64_t K, const void* rows, const int32_t* pos,
+                          const float* weights, void* y, void* stream) {
+  int st = swg::validate_rows(dtype, T, k, K, {rows, y}, {pos}, {weights});
+  if (st != SWIGLU_OK || T == 0 || K == 0) return st;
+  swg::CombineArgs a{};
+  a.T = (int)T; a.k = (int)k; a.K = (int)K;
+  a.pos = pos; a.weights = weights; a.y = rows; a.out = y;
+  return hip_status(swg::launch_combine(as_dt(dtype), a, as_stream(stream)));
+}
+
+int swiglu_expert_combine_bwd(int dtype, int64_t T, int64_t k, int64_t K, const void* dy, const void* rows,
+                              const int32_t* pos, const float* weights, void* drows, float* dweights, void* stream) {
+  int st = swg::validate_rows(dtype, T, k, K, {dy, rows, drows}, {pos}, {weights, dweights});
+  if (st != SWIGLU_OK || T == 0) return st;
+  swg::CombineArgs a{};
+  a.T = (int)T; a.k = (int)k; a.K = (int)K;
+  a.pos = pos; a.weights = weights; a.y = rows; a.dy = dy; a.dyr = drows; a.dweights = dweights;
+  return hip_status(swg::launch_combine_bwd(as_dt(dtype), a, as_stream(stream)));
+}
+
+int swiglu_grouped_fwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
+                       int64_t k, const int32_t* src, const int32_t* offsets, const void* wg, int64_t wg_stride,
+                       const void* wu, int64_t wu_stride, void* h, void* stream) {
+  if (act != SWIGLU_ACT_SILU && act != SWIGLU_ACT_GELU_TANH) return SWIGLU_ERR_ARG;
+  int st = swg::validate_grouped_fwd(dtype, R, E, N, K, x, T, k, src, offsets, wg, wg_stride, wu, wu_stride, h);
+  if (st != SWIGLU_OK || R == 0 || N == 0) return st;
+  swg::GroupedArgs a{};
+  a.offsets = offsets; a.E = (int)E; a.R = (int)R;
+  a.a = x; a.lda = K; a.src = src; a.T = (int)T; a.k = (int)k;
+  a.b0 = wg; a.b1 = wu; a.ldb = K; a.b0_stride = wg_stride; a.b1_stride = wu_stride;
+  a.n = (int)N; a.r = (int)K;
+  a.out0 = h; a.ldo = N;
+  return hip_status(swg::launch_grouped_gated(as_dt(dtype), static_cast<swg::Act>(act), a, as_stream(stream)));
+}
+
+size_t swiglu_grouped_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, int64_t K, int gathered) {
+  return swg::grouped_bwd_workspace_total(dtype, R, N, K, gathered != 0);
+}
+
+int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
+                       int64_t k, const int32_t* src, const int32_t* offsets, const void* wg, int64_t wg_stride,
+                       const void* wu, int64_t wu_stride, const void* dh, void* dx, void* dwg, void* dwu,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (act != SWIGLU_ACT_SILU && act != SWIGLU_ACT_GELU_TANH) return SWIGLU_ERR_ARG;
+  int st = swg::validate_grouped_bwd(dtype, R, E, N, K, x, T, k, src, offsets, wg, wg_stride, wu, wu_stride, dh, dx,
+                                     dwg, dwu, workspace, workspace_bytes);
+  if (st != SWIGLU_OK || K == 0 || (R == 0 && N == 0)) return st;
+  hipStream_t s = as_stream(stream);
+  const swg::Dt dt = as_dt(dtype);
+  hipError_t e;
+  char* ws = static_cast<char*>(workspace);
+  const void* rows = x;
+  if (R > 0 && N > 0) {
+    if (src != nullptr) {
+      // x's rows in order: the weights' gradients read them along the reduction.
+      void* xr = ws + swg::grouped_bwd_layout(dtype, R, N, K, true).off_x;
+      if ((e = swg::launch_gather(dt, (int)T, (int)k, (int)K, x, src, xr, s)) != hipSuccess) return hip_status(e);
+      rows = xr;
+    }
+    // 1. g and u again, D = [dg | du].
+    swg::GroupedArgs d{};
+    d.offsets = offsets; d.E = (int)E; d.R = (int)R;
+    d.a = rows; d.lda = K;
+    d.b0 = wg; d.b1 = wu; d.ldb = K; d.b0_stride = wg_stride; d.b1_stride = wu_stride;
+    d.n = (int)N; d.r = (int)K;
+    d.dh = dh; d.out0 = ws; d.ldo = 2 * N;
+    if ((e = swg::launch_grouped_dgated(dt, static_cast<swg::Act>(act), d, s)) != hipSuccess) return hip_status(e);
+  }
+  // 2. dX = dg Wg + du Wu, reducing over both halves of D.
+  if (dx != nullptr && R > 0) {
+    swg::GroupedArgs g{};
+    g.offsets = offsets; g.E = (int)E; g.R = (int)R;
+    g.a = ws; g.lda = 2 * N;
+    g.b0 = wg; g.b1 = wu; g.ldb = K; g.b0_stride = wg_stride; g.b1_stride = wu_stride;
+    g.n = (int)K; g.r = (int)N; g.halves = 2;
+    g.out0 = dx; g.ldo = K;
+    if ((e = swg::launch_grouped_nn(dt, g, s)) != hipSuccess) return hip_status(e);
+  }
+  // 3. dWg = dg^T x, dWu = du^T x, reducing over each expert's rows.
+  if (dwg != nullptr && N > 0) {
+    swg::GroupedArgs g{};
+    g.offsets = offsets; g.E = (int)E; g.R = (int)R;
+    g.a = ws; g.lda = 2 * N;
+    g.b0 = rows; g.ldb = K;
+    g.m = (int)N; g.n = (int)K; g.halves = 2;
+    g.out0 = dwg; g.out1 = dwu; g.ldo = K;
+    if ((e = swg::launch_grouped_tn(dt, g, s)) != hipSuccess) return hip_status(e);
+  }
+  return SWIGLU_OK;
+}
+
+int swiglu_grouped_mm(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, const int32_t* offsets,
+                      const void* w, int64_t w_stride, void* y, void* stream) {
+  int st = swg::validate_grouped_mm(dtype, R, E, N, K, x, offsets, w, w_stride, y);
+  if (st != SWIGLU_OK || R == 0 || N == 0) return st;
+  swg::GroupedArgs a{};
+  a.offsets = offsets; a.E = (int)E; a.R = (int)R;
+  a.a = x; a.lda = K;
+  a.b0 = w; a.ldb = K; a.b0_stride = w_stride;
+  a.n = (int)N; a.r = (int)K;
+  a.out0 = y; a.ldo = N;
+  return hip_status(swg::launch_grouped_nt(as_dt(dtype), a, as_stream(stream)));
+}
+
+int swiglu_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x,
+                          const int32_t* offsets, const void* w, int64_t w_stride, const void* dy, void* dx, void* dw,
+                          void* stream) {
+  int st = swg::validate_grouped_mm_bwd(dtype, R, E, N, K, x, offsets, w, w_stride, dy, dx, dw);
+  if (st != SWIGLU_OK || K == 0) return st;
+  const swg::Dt dt = as_dt(dtype);
+  hipError_t e = hipSuccess;
+  if (dx != nullptr && R > 0) {
+    swg::GroupedArgs a{};
+    a.offsets = offsets; a.E = (int)E; a.R = (int)R;
+    a.a = dy; a.lda = N;
+    a.b0 = w; a.ldb = K; a.b0_stride = w_stride;
+    a.n = (int)K; a.r = (int)N; a.halves = 1;
+    a.out0 = dx; a.ldo = K;
+    if ((e = swg::launch_grouped_nn(dt, a, as_stream(stream))) != hipSuccess) return hip_status(e);
+  }
+  if (dw != nullptr && N > 0) {
+    swg::GroupedArgs a{};
+    a.offsets = offsets; a.E = (int)E; a.R = (int)R;
+    a.a = dy; a.lda = N;
+    a.b0 = x; a.ldb = K;
+    a.m = (int)N; a.n = (int)K; a.halves = 1;
+    a.out0 = dw; a.ldo = K;
+    e = swg::launch_grouped_tn(dt, a, as_stream(stream));
+  }
+  return hip_status(e);
+}
+
+size_t swiglu_grad_norm_workspace_bytes(int64_t count) { return swg::grad_norm_workspace_total(count); }
+
+int swiglu_grad_norm(int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes, float* norm,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  int st = swg::validate_grads(count, dtypes, grads, sizes, nullptr, false, 0.0, 0.0, norm, workspace, workspace_bytes);
+  if (st != SWIGLU_OK) return st;
+  swg::ClipArgs a{};
+  a.count = count; a.dtypes = dtypes; a.grads = grads; a.sizes = sizes;
+  a.norm = norm;
+  a.part = reinterpret_cast<double*>(static_cast<char*>(workspace) + 256);
+  return hip_status(swg::launch_clip(a, as_stream(stream)));
+}
+
+int swiglu_clip_grads(int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes,
+                      void* const* outs, double max_norm, double eps, float* norm, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int st = swg::validate_grads(count, dtypes, grads, sizes, outs, true, max_norm, eps, norm, workspace,
+                               workspace_bytes);
+  if (st != SWIGLU_OK) return st;
+  swg::ClipArgs a{};
+  a.count = count; a.dtypes = dtypes; a.grads = grads; a.sizes = sizes; a.outs = outs;
+  a.clip = true; a.max_norm = max_norm; a.eps = eps;
+  a.norm = norm;
+  a.factor = static_cast<float*>(workspace);
+  a.part = reinterpret_cast<double*>(static_cast<char*>(workspace) + 256);
+  return hip_status(swg::launch_clip(a, as_stream(stream)));
 }
 
 int swiglu_probe_mfma(int iters, int blocks, float* sink, void* stream) {

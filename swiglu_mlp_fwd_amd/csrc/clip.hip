@@ -1,0 +1,300 @@
+// The norm of many gradients together, and their clipping.
+//
+//   norm = sqrt(sum over all elements of g^2)
+//   g   <- g * min(1, max_norm / (norm + eps))
+//
+// The tensors' addresses and sizes are kernel arguments (a table of up to
+// kClipNormTensors or kClipScaleTensors of them to a launch), so nothing is
+// copied to the device and a captured call replays by itself.  A workgroup
+// takes chunks of 32 KiB in turn, a chunk of one tensor, found by a binary
+// search over the tensors' first chunks.  Squares are formed and added in
+// fp64 (exact products of the inputs, no overflow or underflow for any fp32
+// value); every workgroup writes its sum to a place of its own and one
+// workgroup adds them, all in a fixed order.  The scaling pass reads the
+// factor that this leaves in memory and ends at once where it is 1 and the
+// gradients stay where they are: a step under the limit reads them once.
+#include "common.hpp"
+#include "grouped.hpp"
+#include "validate.hpp"
+
+namespace swg {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// Addresses have 48 bits: a tensor's address and the elements of its last
+// chunk, less one, in one word.
+template <int kTensors, bool kOut>
+struct Table {
+  uint64_t at[kTensors];
+  uint64_t to[kOut ? kTensors : 1];
+  uint32_t first[kTensors + 1];       // first chunk of each tensor; behind the last: all chunks
+  int count;
+};
+static_assert(sizeof(Table<kClipNormTensors, false>) <= 4096 - 64, "kernel arguments");
+static_assert(sizeof(Table<kClipScaleTensors, true>) <= 4096 - 64, "kernel arguments");
+
+template <typename T> constexpr int64_t kChunk = kClipChunkBytes / (int64_t)sizeof(T);
+
+template <typename T> struct Elems;
+template <> struct Elems<bf16> {
+  static constexpr int kN = 8;
+  __device__ static float get(const u32x4& v, int i) {
+    return bits_f32((i & 1) ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+  }
+};
+template <> struct Elems<float> {
+  static constexpr int kN = 4;
+  __device__ static float get(const u32x4& v, int i) { return bits_f32(v[i]); }
+};
+
+// Addresses out of the table's words, known to be global memory's; 16 bytes
+// at any element boundary.
+typedef __attribute__((address_space(1))) char global_char;
+typedef u32x4 piece_t __attribute__((aligned(2)));
+typedef __attribute__((address_space(1))) piece_t global_piece;
+__device__ __forceinline__ u32x4 load16(const global_char* p) { return *(const global_piece*)p; }
+__device__ __forceinline__ void store16(global_char* p, const u32x4& v) { *(global_piece*)p = v; }
+__device__ __forceinline__ float load1(bf16, const global_char* p) {
+  return bits_f32((uint32_t) * (const __attribute__((address_space(1))) uint16_t*)p << 16);
+}
+__device__ __forceinline__ float load1(float, const global_char* p) {
+  return *(const __attribute__((address_space(1))) float*)p;
+}
+__device__ __forceinline__ void store1(bf16, global_char* p, float v) {
+  *(__attribute__((address_space(1))) uint16_t*)p = __builtin_bit_cast(uint16_t, to_bf16(v));
+}
+__device__ __forceinline__ void store1(float, global_char* p, float v) {
+  *(__attribute__((address_space(1))) float*)p = v;
+}
+
+template <class Tab>
+__device__ __forceinline__ int tensor_of(const Tab& t, uint32_t chunk) {
+  int lo = 0, hi = t.count - 1;                           // the last tensor whose first chunk is not past it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Chunk `c`: its first element's address and its elements.
+template <typename T, class Tab>
+__device__ __forceinline__ void chunk_of(const Tab& t, uint32_t c, int& tensor, int64_t& offset, int& n) {
+  tensor = tensor_of(t, c);
+  const uint32_t k = c - t.first[tensor];
+  offset = (int64_t)k * kChunk<T>;
+  n = c + 1 == t.first[tensor + 1] ? (int)(t.at[tensor] & 0xFFFF) + 1 : (int)kChunk<T>;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void norm_kernel(Table<kClipNormTensors, false> t, double* part) {
+  constexpr int kN = Elems<T>::kN;
+  const int tid = threadIdx.x;
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
+  for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
+    int i, n;
+    int64_t off;
+    chunk_of<T>(t, c, i, off, n);
+    const global_char* g = (const global_char*)((t.at[i] >> 16) + (uint64_t)off * sizeof(T));
+    const int full = n / kN;                              // whole 16-byte pieces
+    constexpr int kU = 8;                                 // pieces of a whole chunk per thread
+    static_assert(kChunk<T> == (int64_t)kU * kThreads * kN, "a chunk is kU pieces per thread");
+    if (n == (int)kChunk<T>) {
+      u32x4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) v[u] = load16(g + (u * kThreads + tid) * 16);
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int q = 0; q < kN; ++q) {
+          const double d = (double)Elems<T>::get(v[u], q);
+          acc[q & 3] = __builtin_fma(d, d, acc[q & 3]);
+        }
+    } else {
+      for (int u = tid; u < full; u += kThreads) {
+        const u32x4 v = load16(g + u * 16);
+#pragma unroll
+        for (int q = 0; q < kN; ++q) {
+          const double d = (double)Elems<T>::get(v, q);
+          acc[q & 3] = __builtin_fma(d, d, acc[q & 3]);
+        }
+      }
+      if (full * kN + tid < n) {
+        const double d = (double)load1(T{}, g + (full * kN + tid) * (int)sizeof(T));
+        acc[0] = __builtin_fma(d, d, acc[0]);
+      }
+    }
+  }
+  double s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  __shared__ double wave[kThreads / 64];
+  if ((tid & 63) == 0) wave[tid >> 6] = s;
+  __syncthreads();
+  if (tid == 0) part[blockIdx.x] = (wave[0] + wave[1]) + (wave[2] + wave[3]);
+}
+
+// One workgroup: the norm and, where factor is asked for, the factor.
+constexpr int kTotalThreads = 1024;
+__global__ __launch_bounds__(kTotalThreads) void total_kernel(const double* part, int n, double max_norm, double eps,
+                                                              float* norm, float* factor) {
+  const int tid = threadIdx.x;
+  double s = 0.0;
+  for (int i = tid; i < n; i += kTotalThreads) s += part[i];
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  __shared__ double wave[kTotalThreads / 64];
+  if ((tid & 63) == 0) wave[tid >> 6] = s;
+  __syncthreads();
+  if (tid == 0) {
+    double all = 0.0;
+    for (int w = 0; w < kTotalThreads / 64; ++w) all += wave[w];
+    const double r = sqrt(all);
+    *norm = (float)r;
+    if (factor != nullptr) {
+      const double f = max_norm / (r + eps);
+      *factor = f > 1.0 ? 1.0f : (float)f;                // a NaN stays one
+    }
+  }
+}
+
+template <typename T> __device__ __forceinline__ u32x4 scaled(const u32x4& v, float f) {
+  u32x4 o;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      o[q] = __builtin_bit_cast(uint32_t, bf16x2{to_bf16(f * bits_f32(v[q] << 16)), to_bf16(f * bits_f32(v[q] & 0xFFFF0000u))});
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = f32_bits(f * bits_f32(v[q]));
+  }
+  return o;
+}
+
+template <typename T, class Tab, bool kOut>
+__global__ __launch_bounds__(kThreads) void scale_kernel(Tab t, const float* factor) {
+  constexpr int kN = Elems<T>::kN;
+  const float f = *factor;
+  if (!kOut && f == 1.0f) return;
+  const int tid = threadIdx.x;
+  for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
+    int i, n;
+    int64_t off;
+    chunk_of<T>(t, c, i, off, n);
+    const global_char* g = (const global_char*)((t.at[i] >> 16) + (uint64_t)off * sizeof(T));
+    global_char* o = (global_char*)((kOut ? t.to[i] : t.at[i] >> 16) + (uint64_t)off * sizeof(T));
+    const int full = n / kN;
+    constexpr int kU = 8;
+    if (n == (int)kChunk<T>) {
+      u32x4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) v[u] = load16(g + (u * kThreads + tid) * 16);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const u32x4 w = scaled<T>(v[u], f);
+        store16(o + (u * kThreads + tid) * 16, w);
+      }
+    } else {
+      for (int u = tid; u < full; u += kThreads) {
+        const u32x4 w = scaled<T>(load16(g + u * 16), f);
+        store16(o + u * 16, w);
+      }
+      const int j = full * kN + tid;
+      if (j < n) store1(T{}, o + j * (int)sizeof(T), f * load1(T{}, g + j * (int)sizeof(T)));
+    }
+  }
+}
+
+template <typename T, class Tab>
+uint32_t fill(Tab& t, const GradSpan* spans, int count, bool out) {
+  uint32_t chunks = 0;
+  for (int i = 0; i < count; ++i) {
+    const int64_t n = (spans[i].n + kChunk<T> - 1) / kChunk<T>;
+    const int64_t tail = spans[i].n - (n - 1) * kChunk<T>;
+    t.at[i] = (reinterpret_cast<uint64_t>(spans[i].g) << 16) | (uint64_t)(tail - 1);
+    if (out) t.to[i] = reinterpret_cast<uint64_t>(spans[i].out);
+    t.first[i] = chunks;
+    chunks += (uint32_t)n;
+  }
+  t.first[count] = chunks;
+  t.count = count;
+  return chunks;
+}
+
+template <typename T>
+hipError_t norm_t(const GradSpan* spans, int count, int* blocks, double* part, hipStream_t s) {
+  Table<kClipNormTensors, false> t;
+  const uint32_t chunks = fill<T>(t, spans, count, false);
+  *blocks = chunks < (uint32_t)kClipBlocks ? (int)chunks : kClipBlocks;
+  hipLaunchKernelGGL((norm_kernel<T>), dim3(*blocks), dim3(kThreads), 0, s, t, part);
+  return hipGetLastError();
+}
+
+template <typename T, bool kOut, int kTensors>
+hipError_t scale_t(const GradSpan* spans, int count, const float* factor, hipStream_t s) {
+  using Tab = Table<kTensors, kOut>;
+  Tab t;
+  const uint32_t chunks = fill<T>(t, spans, count, kOut);
+  const unsigned blocks = chunks < 2u * kClipBlocks ? chunks : 2u * kClipBlocks;
+  hipLaunchKernelGGL((scale_kernel<T, Tab, kOut>), dim3(blocks), dim3(kThreads), 0, s, t, factor);
+  return hipGetLastError();
+}
+
+// The spans of one type in runs of at most `most`, in the order given.
+template <class F>
+hipError_t for_runs(Dt dt, int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes,
+                    void* const* outs, int most, F&& f) {
+  GradSpan run[kClipNormTensors];
+  int n = 0;
+  hipError_t e = hipSuccess;
+  for (int64_t i = 0; i < count && e == hipSuccess; ++i) {
+    if (sizes[i] == 0 || dtypes[i] != (dt == Dt::kBF16 ? SWIGLU_BF16 : SWIGLU_F32)) continue;
+    run[n++] = GradSpan{grads[i], outs != nullptr ? outs[i] : const_cast<void*>(grads[i]), sizes[i]};
+    if (n == most) {
+      e = f(run, n);
+      n = 0;
+    }
+  }
+  if (n > 0 && e == hipSuccess) e = f(run, n);
+  return e;
+}
+
+}  // namespace
+
+hipError_t launch_clip(const ClipArgs& a, hipStream_t s) {
+  int parts = 0;
+  hipError_t e = hipSuccess;
+  for (Dt dt : {Dt::kBF16, Dt::kF32}) {
+    e = for_runs(dt, a.count, a.dtypes, a.grads, a.sizes, nullptr, kClipNormTensors, [&](const GradSpan* r, int n) {
+      int blocks = 0;
+      const hipError_t err = dt == Dt::kBF16 ? norm_t<bf16>(r, n, &blocks, a.part + parts, s)
+                                             : norm_t<float>(r, n, &blocks, a.part + parts, s);
+      parts += blocks;
+      return err;
+    });
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(total_kernel, dim3(1), dim3(kTotalThreads), 0, s, a.part, parts, a.max_norm, a.eps, a.norm,
+                     a.clip ? a.factor : nullptr);
+  if ((e = hipGetLastError()) != hipSuccess || !a.clip) return e;
+  for (Dt dt : {Dt::kBF16, Dt::kF32}) {
+    const bool b16 = dt == Dt::kBF16;
+    if (a.outs != nullptr)
+      e = for_runs(dt, a.count, a.dtypes, a.grads, a.sizes, a.outs, kClipScaleTensors, [&](const GradSpan* r, int n) {
+        return b16 ? scale_t<bf16, true, kClipScaleTensors>(r, n, a.factor, s)
+                   : scale_t<float, true, kClipScaleTensors>(r, n, a.factor, s);
+      });
+    else
+      e = for_runs(dt, a.count, a.dtypes, a.grads, a.sizes, nullptr, kClipNormTensors, [&](const GradSpan* r, int n) {
+        return b16 ? scale_t<bf16, false, kClipNormTensors>(r, n, a.factor, s)
+                   : scale_t<float, false, kClipNormTensors>(r, n, a.factor, s);
+      });
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace swg

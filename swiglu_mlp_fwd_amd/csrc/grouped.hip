@@ -1,0 +1,685 @@
+// Matrix products grouped by expert, with ragged groups, on gfx950 matrix
+// cores.
+//
+// R rows lie in order of expert, those of expert e from offsets[e] up to
+// offsets[e + 1], which only the device knows.  Three forms of product, each
+// C[m, n] = sum_r A(m, r) B(n, r) within one expert:
+//   NT  m a row, n an output column, r an input column: A and B have the
+//       reduction contiguous (y = x W^T; with two B operands the gate/up
+//       stage and its recompute in the backward);
+//   NN  m a row, n an input column, r an output column: B = W [r, n] has the
+//       reduction along its rows (dx = dy W; with two halves dg Wg + du Wu);
+//   TN  m an output column, n an input column, r the expert's rows: A and B
+//       both have the reduction along their rows (dW = dy^T x).
+// An operand whose reduction is contiguous is staged in LDS as rows of 128
+// bytes of reduction; one whose reduction runs along its rows as k rows of
+// its columns, and its MFMA fragments are formed by the transposing LDS
+// reads of gfx950 (ds_read_b64_tr_b16: 16 lanes address a 4 x 16 block and
+// receive a column each), so no operand is ever transposed in memory.
+//
+// Tiles: NT and NN cut every expert's rows into tiles of BM; a workgroup
+// finds its tile by a scan over the experts' tile counts, one expert to a
+// lane, so the host needs no sizes and nothing has to be planned.  Rows in
+// front of the first and behind the last expert form two groups of zero rows.
+// The grid covers the most tiles that R rows in E groups can make; the
+// workgroups beyond the tiles there are end at once.  In an expert's last
+// tile, waves whose rows all lie behind its end load their share of the
+// operands and skip the products, so the others have the matrix cores.
+//
+// The main loop is that of the ungrouped products (gemm.hip): a ring of two
+// k-steps in LDS filled by 16-byte LDS DMA, fragments double-buffered in
+// registers, one barrier per k-step.  Every wave moves a share of every
+// operand.
+#include "common.hpp"
+#include "grouped.hpp"
+#include "mfma.hpp"
+
+namespace swg {
+
+namespace {
+
+enum class Form { kNT, kNN, kTN };
+enum class Out { kGated, kDGated, kStore };
+
+// act(z) and, for the gradient, act'(z): SiLU a = z s, a' = s (1 + z (1 - s)),
+// s = sigma(z); GELU (tanh form) a = z s, a' = s + z s (1 - s) t'(z),
+// s = sigma(t), t = z (c1 + c3 z^2).  kShort: for results rounded to bf16.
+template <Act A, bool kShort>
+__device__ __forceinline__ float act_of(float z) {
+  if constexpr (A == Act::kGeluTanh) return kShort ? gelu_tanh_bf16out(z) : gelu_tanh_f32(z);
+  else if constexpr (kShort) {
+    float s, a;
+    sigmoid_silu_bf16out(z, s, a);
+    return a;
+  } else {
+    return silu_f32(z);
+  }
+}
+
+template <Act A, bool kShort>
+__device__ __forceinline__ void act_and_slope(float z, float& a, float& da) {
+  if constexpr (A == Act::kGeluTanh) {
+    const float z2 = z * z;
+    const float t = z * __builtin_fmaf(kGeluC3, z2, kGeluC1);
+    float s, c;
+    if constexpr (kShort) {
+      constexpr float kL2e = 1.44269504088896340736f;
+      s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-t * kL2e));
+      c = 1.0f - s;
+    } else {
+      sigmoid_pair_f32(t, s, c);
+    }
+    a = z * s;
+    da = s + a * c * __builtin_fmaf(3.0f * kGeluC3, z2, kGeluC1);
+  } else {
+    float s;
+    if constexpr (kShort) sigmoid_silu_bf16out(z, s, a);
+    else sigmoid_silu_f32(z, s, a);
+    da = s * (1.0f + z * (1.0f - s));
+  }
+}
+
+// ------------------------------------------------------------ tile of rows
+
+struct Spot {
+  int e;        // expert; -1: rows of no expert
+  int row0;     // first row of the tile
+  int rows;     // its rows
+  int tn;
+};
+
+__device__ __forceinline__ int wave_scan(int v) {   // inclusive, over 64 lanes
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    if ((int)(threadIdx.x & 63) >= d) v += o;
+  }
+  return v;
+}
+
+// The rows of group g: 0 in front of the first expert, 1 .. E the experts',
+// E + 1 behind the last.  Offsets are taken into [0, R], so that none of any
+// value leads outside the arrays.
+__device__ __forceinline__ void group_rows(const GroupedArgs& p, int g, int& first, int& count) {
+  auto at = [&](int i) {
+    const int v = p.offsets[i];
+    return v < 0 ? 0 : (v > p.R ? p.R : v);
+  };
+  first = g == 0 ? 0 : at(g - 1);
+  const int end = g > p.E ? p.R : at(g);
+  count = end > first ? end - first : 0;
+}
+
+// The tile of workgroup `bid`: experts in order, within one kGroupM row tiles
+// at a time down the columns.  kZero: rows of no expert have tiles too.
+template <int BM, int kGroupM, bool kZero>
+__device__ __forceinline__ bool find_tile(const GroupedArgs& p, int ntn, int bid, Spot& spot) {
+  const int lane = threadIdx.x & 63;
+  const int ng = p.E + 2;
+  auto tiles_of = [&](int g, int& first, int& count) -> int {
+    first = count = 0;
+    if (g >= ng) return 0;
+    group_rows(p, g, first, count);
+    if (!kZero && (g == 0 || g == ng - 1)) return 0;
+    return (int)(((int64_t)count + BM - 1) / BM);
+  };
+  int first, count;
+  int mine = tiles_of(lane, first, count);
+  int scan = wave_scan(mine);
+  int64_t total = __builtin_amdgcn_readlane(scan, 63);
+  for (int c = 64; c < ng; c += 64) {
+    int f, n;
+    total += __builtin_amdgcn_readlane(wave_scan(tiles_of(c + lane, f, n)), 63);
+  }
+  // Offsets that decrease may make more tiles than the grid has: no tile then.
+  if (bid >= total * ntn || total * ntn > (int64_t)gridDim.x) return false;
+  const int tile = xcd_remap(bid, (int)total * ntn);
+  const int want = tile / ntn;
+  int before = 0;                                       // tiles of the groups before this chunk
+  for (int c = 0; c < ng; c += 64) {
+    if (c > 0) {
+      mine = tiles_of(c + lane, first, count);
+      scan = wave_scan(mine);
+    }
+    const uint64_t past = __ballot(before + scan > want);
+    if (past != 0) {
+      const int l = __builtin_ctzll(past);
+      const int mt = __builtin_amdgcn_readlane(mine, l);
+      const int s0 = before + __builtin_amdgcn_readlane(scan, l) - mt;
+      const int f = __builtin_amdgcn_readlane(first, l), n = __builtin_amdgcn_readlane(count, l);
+      const int g = c + l;
+      const int local = tile - s0 * ntn;                // within the group: mt x ntn
+      const int band = kGroupM * ntn;
+      const int m0 = (local / band) * kGroupM;
+      const int gm = mt - m0 < kGroupM ? mt - m0 : kGroupM;
+      const int tm = m0 + (local % band) % gm;
+      spot.tn = (local % band) / gm;
+      spot.e = (g == 0 || g == ng - 1) ? -1 : g - 1;
+      spot.row0 = f + tm * BM;
+      spot.rows = n - tm * BM < BM ? n - tm * BM : BM;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(scan, 63);
+  }
+  return false;
+}
+
+// --------------------------------------------------------------- the kernel
+
+// dh tile in LDS: row r at r * 2 BN bytes, its 16-byte chunk c at physical
+// chunk c ^ (r & 15).
+template <class TL>
+struct DhTile {
+  static constexpr int kCPR = TL::kBN / 8;
+  static constexpr int kPitch = TL::kBN * 2;
+  __device__ static int offset(int row, int col) {
+    return row * kPitch + (((col >> 3) ^ (row & 15)) << 4) + (col & 7) * 2;
+  }
+};
+
+template <Out O, class TL>
+struct OutLds {                                           // staged results (16-bit outputs)
+  static constexpr int kPitch = TL::kBN * 2 + 32;
+  static constexpr int kRegion = TL::kBM * kPitch;
+  static constexpr int kBytes = (O == Out::kDGated ? 2 : 1) * kRegion;
+};
+
+template <typename T, Form F, Out O, Act ACT, int NB, class TL, int S, int kGroupM>
+__global__ __launch_bounds__(TL::kThreads) __attribute__((amdgpu_waves_per_eu(TL::kOcc, TL::kOcc)))
+void grouped_kernel(GroupedArgs p) {
+  constexpr bool kB16 = sizeof(T) == 2;
+  constexpr int kMN = kB16 ? 16 : 32;                     // MFMA tile
+  constexpr int kBM = TL::kBM, kBN = TL::kBN, kThreads = TL::kThreads, kWaves = kThreads / 64;
+  constexpr int kWM = TL::kWM, kWN = TL::kWN, kTM = kWM / kMN, kTN = kWN / kMN;
+  constexpr int KC = 8, kRowBytes = 128;                  // a k-step: 8 chunks of 16 bytes
+  constexpr int kPer = 16 / (int)sizeof(T);               // elements per chunk
+  constexpr int kStep = KC * kPer;                        // reduction per k-step
+  constexpr int kABytes = kBM * kRowBytes, kBBytes = kBN * kRowBytes;
+  constexpr int kStageBytes = kABytes + NB * kBBytes;
+  constexpr int kDmaA = kABytes / 1024 / kWaves, kDmaB = kBBytes / 1024 / kWaves;   // per wave and k-step
+  constexpr int kDma = kDmaA + NB * kDmaB;
+  constexpr bool kAT = F == Form::kTN, kBT = F != Form::kNT;   // reduction along the operand's rows
+  static_assert(kABytes % (1024 * kWaves) == 0 && kBBytes % (1024 * kWaves) == 0, "DMA split");
+  static_assert(S == 2, "the dh tile goes into the slot of the step before the last");
+  extern __shared__ u32x4 lds[];
+  char* const lds_bytes = reinterpret_cast<char*>(lds);
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / TL::kWGN, wn = wave % TL::kWGN;
+  const int ntn = (p.n + kBN - 1) / kBN;
+
+  // This workgroup's tile: rows, expert, columns.
+  int e, tn, row0, rows, half = 0, m0 = 0, mrows;         // row0, rows: of the expert (TN: the reduction)
+  if constexpr (F == Form::kTN) {
+    const int ntm = (p.m + kBM - 1) / kBM, per = p.halves * ntm * ntn;
+    const int tile = xcd_remap(blockIdx.x, p.E * per);
+    e = tile / per;
+    const int local = tile % per, band = kGroupM * ntn, nm = p.halves * ntm;
+    const int g0 = (local / band) * kGroupM, gm = nm - g0 < kGroupM ? nm - g0 : kGroupM;
+    const int tm = g0 + (local % band) % gm;
+    tn = (local % band) / gm;
+    half = tm / ntm;
+    m0 = (tm - half * ntm) * kBM;
+    mrows = p.m - m0 < kBM ? p.m - m0 : kBM;
+    group_rows(p, e + 1, row0, rows);
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    rows = __builtin_amdgcn_readfirstlane(rows);
+  } else {
+    Spot spot;
+    if (!find_tile<kBM, kGroupM, O != Out::kDGated>(p, ntn, blockIdx.x, spot)) return;
+    e = spot.e; tn = spot.tn; row0 = spot.row0; rows = mrows = spot.rows;
+  }
+  const int n0 = tn * kBN;
+  const bool live = e >= 0;
+  const int es = (int)sizeof(T);
+
+  // Reduction: k-steps per half (NN has one or two halves, TN one over rows).
+  const int red = F == Form::kTN ? rows : p.r;
+  const int nkh = live ? (red + kStep - 1) / kStep : 0;
+  const int nk = (F == Form::kNN ? p.halves : 1) * nkh;
+
+  // ---- operand A
+  // Contiguous: instruction d of the wave fills LDS rows 8 (d kWaves + wave)
+  // .. + 7, a lane physical chunk lane % 8 of one, from logical chunk
+  // (lane % 8) ^ ((row >> 1) & 7).
+  // Along rows: it fills 1 KiB of k rows, kCPR chunks each; k row kr's pair
+  // of chunks q lies at pair q ^ f(kr) (bf16: f = (kr & 3) | ((kr >> 3) & 1)
+  // << 2, so that the transposing reads of two 16-lane groups meet 8 different
+  // pairs; fp32: chunk bit 3 ^= (kr >> 2) & 1, the halves of a wave).
+  // Lanes' offsets are the same for every d but for whole rows.
+  constexpr int kRowsPass = 8 * kWaves;                   // contiguous rows per d
+  auto lane_contig = [&](int& row, int& chunk) {
+    row = 8 * wave + (lane >> 3);
+    chunk = (lane & 7) ^ ((row >> 1) & 7);
+  };
+  static_assert(kWaves % 4 == 0, "a pass over d leaves the swizzles of a lane's rows alone");
+  auto lane_along = [&](auto cpr_c, int& kr, int& chunk) {
+    constexpr int cpr = decltype(cpr_c)::value;           // chunks per k row
+    constexpr int rpi = 64 / cpr;                         // k rows per instruction
+    static_assert((rpi * kWaves) % 16 == 0 || !kB16, "f is the same for every d");
+    static_assert((rpi * kWaves) % 8 == 0, "f is the same for every d");
+    kr = rpi * wave + lane / cpr;
+    const int c = lane % cpr;
+    if constexpr (kB16) chunk = c ^ (((kr & 3) | (((kr >> 3) & 1) << 2)) << 1);
+    else chunk = c ^ (((kr >> 2) & 1) << 3);
+  };
+  constexpr uint32_t kOob = 0x80000000u;                  // past every descriptor: reads zero
+
+  const T* abase = static_cast<const T*>(p.a);
+  int64_t abytes = 0;                                     // contiguous: descriptor; along rows: all that is left
+  uint32_t avoff[kAT ? 1 : kDmaA];
+  int achunk = 0;
+  constexpr int kACpr = kBM / kPer, kBCpr = kBN / kPer;
+  if constexpr (kAT) {
+    int kr;
+    lane_along(std::integral_constant<int, kACpr>{}, kr, achunk);
+    abase += (int64_t)row0 * p.lda + (int64_t)half * p.m + m0;
+    abytes = rows > 0 ? ((int64_t)rows * p.lda - half * p.m - m0) * es : 0;
+    avoff[0] = (uint32_t)(kr * (int)p.lda * es + achunk * 16);
+  } else {
+    int r;
+    lane_contig(r, achunk);
+    if (F == Form::kNT && p.src != nullptr) {
+      abytes = (int64_t)p.T * p.lda * es;
+#pragma unroll
+      for (int d = 0; d < kDmaA; ++d) {
+        const int rr = r + d * kRowsPass;
+        avoff[d] = kOob;
+        if (live && rr < rows) {
+          const int pair = p.src[row0 + rr];
+          const int t = pair / p.k;
+          if (pair >= 0 && t < p.T) avoff[d] = (uint32_t)t * (uint32_t)(p.lda * es) + (uint32_t)(achunk * 16);
+        }
+      }
+    } else {
+      abase += (int64_t)row0 * p.lda;
+      abytes = live ? (int64_t)rows * p.lda * es : 0;
+#pragma unroll
+      for (int d = 0; d < kDmaA; ++d)
+        avoff[d] = (uint32_t)((r + d * kRowsPass) * (int)p.lda * es + achunk * 16);
+    }
+  }
+  // ---- operand B
+  const T* bbase[2];
+  int64_t bbytes;
+  uint32_t bvoff;
+  int bchunk;
+  const int64_t ebase = live ? e : 0;
+  if constexpr (F == Form::kTN) {
+    bbase[0] = bbase[1] = static_cast<const T*>(p.b0) + (int64_t)row0 * p.ldb + n0;
+    bbytes = rows > 0 ? ((int64_t)rows * p.ldb - n0) * es : 0;
+  } else {
+    bbase[0] = static_cast<const T*>(p.b0) + ebase * p.b0_stride;
+    bbase[1] = static_cast<const T*>(p.b1 != nullptr ? p.b1 : p.b0) + (p.b1 != nullptr ? ebase * p.b1_stride : ebase * p.b0_stride);
+    if constexpr (F == Form::kNN) {
+      bbase[0] += n0;
+      bbase[1] += n0;
+      bbytes = ((int64_t)p.r * p.ldb - n0) * es;
+    } else {
+      bbase[0] += (int64_t)n0 * p.ldb;
+      bbase[1] += (int64_t)n0 * p.ldb;
+      const int left = p.n - n0;
+      bbytes = (int64_t)(left < kBN ? left : kBN) * p.ldb * es;
+    }
+  }
+  if constexpr (kBT) {
+    int kr;
+    lane_along(std::integral_constant<int, kBCpr>{}, kr, bchunk);
+    bvoff = (uint32_t)(kr * (int)p.ldb * es + bchunk * 16);
+  } else {
+    int r;
+    lane_contig(r, bchunk);
+    bvoff = (uint32_t)(r * (int)p.ldb * es + bchunk * 16);
+  }
+  constexpr int kBRowsPass = kBT ? 64 / kBCpr * kWaves : kRowsPass;
+  constexpr int kARowsPass = 64 / kACpr * kWaves;         // (along rows)
+  const uint32_t bpass = (uint32_t)(kBRowsPass * (int)p.ldb * es);
+  const uint32_t apass = (uint32_t)(kARowsPass * (int)p.lda * es);
+
+  // Bytes of an operand along rows that k-step s of a half may read: its kStep
+  // rows, no more than are left.
+  auto step_bytes = [&](int64_t all, int64_t ld, int s) -> int64_t {
+    const int64_t step = (int64_t)kStep * ld * es;
+    const int64_t left = all - s * step;
+    return left < 0 ? 0 : (left < step ? left : step);
+  };
+  auto issue = [&](int ks) {
+    char* dst = lds_bytes + (ks % S) * kStageBytes + wave * 1024;
+    const int h = F == Form::kNN && ks >= nkh ? 1 : 0;
+    const int s = ks - h * nkh;
+    const int rem = (red + kPer - 1) / kPer - s * KC;     // chunks of reduction left (contiguous)
+    const bool past = ks >= nk;
+    if constexpr (kAT) {
+      const __amdgpu_buffer_rsrc_t rs =
+          uniform_rsrc(abase + (int64_t)s * kStep * p.lda, past ? 0 : step_bytes(abytes, p.lda, s));
+#pragma unroll
+      for (int d = 0; d < kDmaA; ++d) {
+        const uint32_t off = avoff[0] + d * apass;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(dst + d * kWaves * 1024), 16, off, 0, 0, 0);
+      }
+    } else {
+      const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(abase, past ? 0 : abytes);
+      const bool in = achunk < rem;
+      const uint32_t at = (uint32_t)((h * p.r + s * kStep) * es);
+#pragma unroll
+      for (int d = 0; d < kDmaA; ++d) {
+        const uint32_t off = in ? avoff[d] + at : kOob;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(dst + d * kWaves * 1024), 16, off, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < NB; ++w) {
+      char* bd = dst + kABytes + w * kBBytes;
+      if constexpr (kBT) {
+        const __amdgpu_buffer_rsrc_t rs =
+            uniform_rsrc(bbase[F == Form::kNN ? h : 0] + (int64_t)s * kStep * p.ldb, past ? 0 : step_bytes(bbytes, p.ldb, s));
+#pragma unroll
+        for (int d = 0; d < kDmaB; ++d)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(bd + d * kWaves * 1024), 16, bvoff + d * bpass, 0,
+                                                   0, 0);
+      } else {
+        const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(bbase[w], past ? 0 : bbytes);
+        const uint32_t off = bchunk < rem ? bvoff + (uint32_t)(s * kStep * es) : kOob;
+#pragma unroll
+        for (int d = 0; d < kDmaB; ++d)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(bd + d * kWaves * 1024), 16, off + d * bpass, 0, 0,
+                                                   0);
+      }
+    }
+  };
+
+  // The dh tile (recompute, bf16) by DMA into a ring slot: an instruction
+  // fills 1 KiB of rows, a lane's chunk c of row r from logical chunk
+  // c ^ (r & 15); chunks past the last column and rows past the tile's read
+  // zero (n is a multiple of 8).
+  constexpr bool kDh = O == Out::kDGated && kB16;
+  auto issue_dh = [&](int slot) {
+    constexpr int kCPR = DhTile<TL>::kCPR, kRpi = 64 / kCPR;
+    static_assert(!kDh || (kCPR == 16 && kBM * DhTile<TL>::kPitch <= kStageBytes), "the dh tile fits a slot");
+    const T* d0 = static_cast<const T*>(p.dh) + (int64_t)row0 * p.n + n0;
+    const __amdgpu_buffer_rsrc_t rd = uniform_rsrc(d0, ((int64_t)rows * p.n - n0) * es);
+    char* dst = lds_bytes + slot * kStageBytes + wave * 1024;
+    constexpr int kPasses = kBM / (kRpi * kWaves);
+#pragma unroll
+    for (int d = 0; d < kPasses; ++d) {
+      const int r = (d * kWaves + wave) * kRpi + lane / kCPR;
+      const int c = (lane % kCPR) ^ (r & 15);
+      const uint32_t off = n0 + c * 8 < p.n && r < rows ? (uint32_t)(r * p.n * es + c * 16) : kOob;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_void_t*)(dst + d * kWaves * 1024), 16, off, 0, 0, 0);
+    }
+  };
+
+  typename AccL<kMN>::V acc[NB][kTM][kTN];
+#pragma unroll
+  for (int w = 0; w < NB; ++w)
+#pragma unroll
+    for (int i = 0; i < kTM; ++i)
+#pragma unroll
+      for (int j = 0; j < kTN; ++j)
+#pragma unroll
+        for (int q = 0; q < AccL<kMN>::kE; ++q) acc[w][i][j][q] = 0.0f;
+
+  // ---- fragments.  Sub-step kk: lane l supplies row l % kMN of its operand
+  // tile and reduction chunk kCPS kk + l / kMN.
+  constexpr int kCPS = 64 / kMN;
+  constexpr int kKK = KC / kCPS;
+  const int rl = lane % kMN, ql = lane / kMN;
+  auto frag_contig = [&](const char* L, int row, int kk) -> u32x4 {
+    const int pc = (kCPS * kk + ql) ^ ((row >> 1) & 7);
+    return *reinterpret_cast<const u32x4*>(L + row * kRowBytes + pc * 16);
+  };
+  // Along rows, columns c0 .. c0 + kMN - 1 of tiles of `cols` columns.
+  auto frag_along = [&](const char* L, auto cols_c, int c0, int kk) -> u32x4 {
+    constexpr int kPitch = decltype(cols_c)::value * (int)sizeof(T);
+    if constexpr (kB16) {
+      const int s = lane & 15, g = lane >> 4;
+      const int f = (s >> 2) | ((g & 1) << 2);
+      const char* at = L + (32 * kk + 8 * g + (s >> 2)) * kPitch + (((c0 >> 4) ^ f) << 5) + (s & 3) * 8;
+      const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)(lds_char_t*)(at));
+      const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4_t*)(lds_char_t*)(at + 4 * kPitch));
+      const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+      return u32x4{a[0], a[1], b[0], b[1]};
+    } else {
+      const int h = lane >> 5;
+      const char* at = L + (8 * kk + 4 * h) * kPitch + (((c0 + rl) * 4) ^ (h << 7));
+      u32x4 v;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) v[t] = *reinterpret_cast<const uint32_t*>(at + t * kPitch);
+      return v;
+    }
+  };
+  u32x4 av[2][kTM], bv[2][NB][kTN];
+  auto read_frags = [&](int buf, const char* L, int kk) {
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      if constexpr (kAT) av[buf][i] = frag_along(L, std::integral_constant<int, kBM>{}, wm * kWM + i * kMN, kk);
+      else av[buf][i] = frag_contig(L, wm * kWM + i * kMN + rl, kk);
+    }
+#pragma unroll
+    for (int w = 0; w < NB; ++w)
+#pragma unroll
+      for (int j = 0; j < kTN; ++j) {
+        const char* LB = L + kABytes + w * kBBytes;
+        if constexpr (kBT) bv[buf][w][j] = frag_along(LB, std::integral_constant<int, kBN>{}, wn * kWN + j * kMN, kk);
+        else bv[buf][w][j] = frag_contig(LB, wn * kWN + j * kMN + rl, kk);
+      }
+  };
+  auto mfmas = [&](int buf) {
+#pragma unroll
+    for (int w = 0; w < NB; ++w)
+#pragma unroll
+      for (int i = 0; i < kTM; ++i)
+#pragma unroll
+        for (int j = 0; j < kTN; ++j) {
+          if constexpr (kB16)
+            acc[w][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[buf][i]),
+                                                                   __builtin_bit_cast(bf16x8, bv[buf][w][j]),
+                                                                   acc[w][i][j], 0, 0, 0);
+          else
+            Mma<T>::run(acc[w][i][j], av[buf][i], bv[buf][w][j]);
+        }
+  };
+  auto landed = [&]() {                                   // this wave's DMA has landed, its LDS reads are done
+    wait_vmcnt<0>();
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+  };
+
+  // Every step of the ring is issued, also those past the last, which read
+  // nothing; the slot of the step before the last takes the dh tile.
+  auto refill = [&](int ks) {
+    if (kDh && ks == nk) issue_dh(ks % S);
+    else issue(ks);
+  };
+  static_assert(kKK % 2 == 0, "the next step's first fragments go to buffer 0");
+  issue(0);
+  if (kDh && nk == 1) issue_dh(1);
+  else issue(1);
+  // wm * kWM < mrows: some row of the wave's is the tile's.
+  if (wm * kWM < mrows) {
+    if (nk > 0) {
+      wait_vmcnt<kDma>();
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      if (kDh && nk == 1) wait_vmcnt<0>();
+      barrier_no_fence();
+      read_frags(0, lds_bytes, 0);
+    }
+    auto kstep = [&](int ks, bool more) {
+      const char* L = lds_bytes + (ks % S) * kStageBytes;
+#pragma unroll
+      for (int kk = 0; kk < kKK; ++kk) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (kk + 1 < kKK) {
+          read_frags((kk + 1) & 1, L, kk + 1);
+        } else if (more) {
+          landed();                                       // step ks + 1
+          barrier_no_fence();                             // and every wave has read step ks
+          __builtin_amdgcn_sched_barrier(0);
+          read_frags(0, lds_bytes + ((ks + 1) % S) * kStageBytes, 0);
+          refill(ks + S);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        mfmas(kk & 1);
+      }
+    };
+    for (int ks = 0; ks + 1 < nk; ++ks) kstep(ks, true);
+    if (nk > 0) kstep(nk - 1, false);
+  } else if (nk > 0) {
+    // Only rows behind the expert's last: this wave's share of the operands.
+    landed();
+    barrier_no_fence();
+    for (int ks = 0; ks + 1 < nk; ++ks) {
+      landed();
+      barrier_no_fence();
+      refill(ks + S);
+    }
+  }
+  landed();
+  barrier_no_fence();                                     // the ring is idle; the dh tile is there
+
+  // ---- results
+  T* const out0 = static_cast<T*>(half == 0 ? p.out0 : p.out1);
+  const int64_t orow0 = F == Form::kTN ? (int64_t)e * p.m + m0 : row0;
+  if constexpr (!kB16) {
+    if (wm * kWM >= mrows) return;
+#pragma unroll
+    for (int i = 0; i < kTM; ++i)
+#pragma unroll
+      for (int j = 0; j < kTN; ++j)
+#pragma unroll
+        for (int q = 0; q < AccL<kMN>::kE; ++q) {
+          const int row = wm * kWM + i * kMN + AccL<kMN>::row(lane, q);
+          const int col = n0 + wn * kWN + j * kMN + AccL<kMN>::col(lane);
+          if (row >= mrows || col >= p.n) continue;
+          T* o = out0 + (orow0 + row) * p.ldo + col;
+          if constexpr (O == Out::kGated) {
+            *o = cvt_out<T>(act_of<ACT, false>(acc[0][i][j][q]) * acc[NB - 1][i][j][q]);
+          } else if constexpr (O == Out::kDGated) {
+            const float dh = load_in<T>(static_cast<const T*>(p.dh) + (int64_t)(row0 + row) * p.n + col);
+            float a, da;
+            act_and_slope<ACT, false>(acc[0][i][j][q], a, da);
+            o[0] = cvt_out<T>(dh * acc[NB - 1][i][j][q] * da);
+            o[p.n] = cvt_out<T>(dh * a);
+          } else {
+            *o = cvt_out<T>(acc[0][i][j][q]);
+          }
+        }
+  } else {
+    constexpr int kPitch = OutLds<O, TL>::kPitch, kRegion = OutLds<O, TL>::kRegion;
+    u32x2 dhv[O == Out::kDGated ? kTM : 1][O == Out::kDGated ? kTN : 1];   // 4 bf16 each
+    if constexpr (O == Out::kDGated) {
+      // dh in accumulator layout, 4 rows of a 16-column run per transposing read.
+      const char* D = lds_bytes + (nk % S) * kStageBytes;
+      const int s = lane & 15;
+#pragma unroll
+      for (int i = 0; i < kTM; ++i)
+#pragma unroll
+        for (int j = 0; j < kTN; ++j) {
+          const int row = wm * kWM + i * 16 + 4 * (lane >> 4) + (s >> 2);
+          const int col = wn * kWN + j * 16 + 4 * (s & 3);
+          const short4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_short4_t*)(lds_char_t*)(D + DhTile<TL>::offset(row, col)));
+          dhv[i][j] = __builtin_bit_cast(u32x2, v);
+        }
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      barrier_no_fence();
+    }
+    if (wm * kWM < mrows) {
+#pragma unroll
+      for (int i = 0; i < kTM; ++i)
+#pragma unroll
+        for (int j = 0; j < kTN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int row = wm * kWM + i * 16 + AccL<16>::row(lane, q);
+            const int col = wn * kWN + j * 16 + AccL<16>::col(lane);
+            bf16* at = reinterpret_cast<bf16*>(lds_bytes + row * kPitch + col * 2);
+            if constexpr (O == Out::kGated) {
+              *at = to_bf16(act_of<ACT, true>(acc[0][i][j][q]) * acc[NB - 1][i][j][q]);
+            } else if constexpr (O == Out::kDGated) {
+              const uint32_t two = dhv[i][j][q >> 1];
+              const float dh = bits_f32((q & 1) ? two & 0xFFFF0000u : two << 16);
+              float a, da;
+              act_and_slope<ACT, true>(acc[0][i][j][q], a, da);
+              *at = to_bf16(dh * acc[NB - 1][i][j][q] * da);
+              at[kRegion / 2] = to_bf16(dh * a);
+            } else {
+              *at = to_bf16(acc[0][i][j][q]);
+            }
+          }
+    }
+    __syncthreads();
+    constexpr int kCPR = kBN / 8;                         // 16-byte chunks per row; n is a multiple of 8
+    for (int c = tid; c < mrows * kCPR; c += kThreads) {
+      const int r = c / kCPR, ch = c % kCPR;
+      const int col = n0 + ch * 8;
+      if (col >= p.n) continue;
+      bf16* o = reinterpret_cast<bf16*>(out0) + (orow0 + r) * p.ldo + col;
+      const char* at = lds_bytes + r * kPitch + ch * 16;
+      *reinterpret_cast<u32x4*>(o) = *reinterpret_cast<const u32x4*>(at);
+      if constexpr (O == Out::kDGated) *reinterpret_cast<u32x4*>(o + p.n) = *reinterpret_cast<const u32x4*>(at + kRegion);
+    }
+  }
+}
+
+template <typename T, Form F, Out O, Act ACT, int NB, class TL, int kGroupM = 8>
+hipError_t launch(const GroupedArgs& a, hipStream_t s) {
+  const int64_t ntn = ((int64_t)a.n + TL::kBN - 1) / TL::kBN;
+  int64_t tiles;
+  if (F == Form::kTN) {
+    tiles = (int64_t)a.E * a.halves * (((int64_t)a.m + TL::kBM - 1) / TL::kBM) * ntn;
+  } else {
+    // Row tiles of R rows in at most min(E + 2, R) groups that have any.
+    const int64_t groups = a.E + 2 < a.R ? a.E + 2 : a.R;
+    tiles = (a.R / TL::kBM + groups) * ntn;
+  }
+  if (tiles == 0) return hipSuccess;
+  const size_t ring = (size_t)2 * (TL::kBM + NB * TL::kBN) * 128;
+  const size_t epi = sizeof(T) == 2 ? (size_t)OutLds<O, TL>::kBytes : 0;
+  const size_t lds = ring > epi ? ring : epi;
+  const hipError_t attr = allow_lds<&grouped_kernel<T, F, O, ACT, NB, TL, 2, kGroupM>>(lds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL((grouped_kernel<T, F, O, ACT, NB, TL, 2, kGroupM>), dim3((unsigned)tiles), dim3(TL::kThreads), lds,
+                     s, a);
+  return hipGetLastError();
+}
+
+using Dual = Tile<256, 128, 4, 2>;
+using Single = Tile<256, 256, 4, 2>;
+using DualF32 = Tile<128, 64, 2, 2, 2>;
+using SingleF32 = Tile<128, 128, 2, 2, 2>;
+
+}  // namespace
+
+hipError_t launch_grouped_gated(Dt dt, Act act, const GroupedArgs& a, hipStream_t s) {
+  if (act == Act::kGeluTanh)
+    return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kGated, Act::kGeluTanh, 2, Dual>(a, s)
+                           : launch<float, Form::kNT, Out::kGated, Act::kGeluTanh, 2, DualF32>(a, s);
+  return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kGated, Act::kSilu, 2, Dual>(a, s)
+                         : launch<float, Form::kNT, Out::kGated, Act::kSilu, 2, DualF32>(a, s);
+}
+
+hipError_t launch_grouped_dgated(Dt dt, Act act, const GroupedArgs& a, hipStream_t s) {
+  if (act == Act::kGeluTanh)
+    return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kDGated, Act::kGeluTanh, 2, Dual>(a, s)
+                           : launch<float, Form::kNT, Out::kDGated, Act::kGeluTanh, 2, DualF32>(a, s);
+  return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kDGated, Act::kSilu, 2, Dual>(a, s)
+                         : launch<float, Form::kNT, Out::kDGated, Act::kSilu, 2, DualF32>(a, s);
+}
+
+hipError_t launch_grouped_nt(Dt dt, const GroupedArgs& a, hipStream_t s) {
+  return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kStore, Act::kSilu, 1, Single, 4>(a, s)
+                         : launch<float, Form::kNT, Out::kStore, Act::kSilu, 1, SingleF32, 8>(a, s);
+}
+
+hipError_t launch_grouped_nn(Dt dt, const GroupedArgs& a, hipStream_t s) {
+  return dt == Dt::kBF16 ? launch<bf16, Form::kNN, Out::kStore, Act::kSilu, 1, Single, 4>(a, s)
+                         : launch<float, Form::kNN, Out::kStore, Act::kSilu, 1, SingleF32, 8>(a, s);
+}
+
+hipError_t launch_grouped_tn(Dt dt, const GroupedArgs& a, hipStream_t s) {
+  return dt == Dt::kBF16 ? launch<bf16, Form::kTN, Out::kStore, Act::kSilu, 1, Single, 4>(a, s)
+                         : launch<float, Form::kTN, Out::kStore, Act::kSilu, 1, SingleF32, 8>(a, s);
+}
+
+}  // namespace swg

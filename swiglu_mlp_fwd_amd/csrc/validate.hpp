@@ -5,7 +5,10 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <initializer_list>
+#include <new>
+#include <vector>
 
 #include "swiglu.h"
 
@@ -470,6 +473,280 @@ inline int validate_norm_bwd(int dtype, int64_t rows, int64_t cols, int64_t grou
   if (!aligned(ws, 256)) return SWIGLU_ERR_ALIGN;
   if (ws_bytes < norm_bwd_workspace_total(rows, cols, groups)) return SWIGLU_ERR_WORKSPACE;
   return SWIGLU_OK;
+}
+
+// ---- rows in order of expert
+
+// The plan's counting sort: one workgroup of kPlanThreads for up to kPlanOne
+// pairs, otherwise at most kPlanBlocks, each a whole number of 64 pairs to a
+// wave.
+constexpr int kPlanThreads = 1024;
+constexpr int64_t kPlanOne = 8192, kPlanBlocks = 128;
+inline int plan_per_block(int64_t n) {
+  return (int)round_up(n <= kPlanOne ? (n < 1 ? 1 : n) : (n + kPlanBlocks - 1) / kPlanBlocks, kPlanThreads);
+}
+inline int plan_blocks(int64_t n) {
+  const int64_t per = plan_per_block(n);
+  return n < 1 ? 1 : (int)((n + per - 1) / per);
+}
+
+inline int check_pairs(int64_t T, int64_t k) {
+  if (T < 0 || k < 1 || k > SWIGLU_MAX_TOPK) return SWIGLU_ERR_SHAPE;
+  if (T > kMaxDim / k) return SWIGLU_ERR_SHAPE;
+  return SWIGLU_OK;
+}
+
+inline int plan_status(int64_t T, int64_t k, int64_t E) {
+  if (E < 1 || E > SWIGLU_MAX_EXPERTS) return SWIGLU_ERR_SHAPE;
+  return check_pairs(T, k);
+}
+inline size_t plan_workspace_total(int64_t T, int64_t k, int64_t E) {
+  if (plan_status(T, k, E) != SWIGLU_OK) return 0;
+  const int blocks = plan_blocks(T * k);
+  return blocks > 1 ? (size_t)round_up((int64_t)blocks * (E + 1) * 4, 256) : 0;
+}
+
+inline int check_int(const void* p) {
+  if (p == nullptr) return SWIGLU_ERR_NULL;
+  return aligned(p, 4) ? SWIGLU_OK : SWIGLU_ERR_ALIGN;
+}
+
+inline int validate_plan(int64_t T, int64_t k, int64_t E, const void* ids, const void* offsets, const void* src,
+                         const void* pos, const void* ws, size_t ws_bytes) {
+  int st = plan_status(T, k, E);
+  if (st) return st;
+  if ((st = check_int(offsets))) return st;
+  if (T > 0) {
+    for (const void* p : {ids, src, pos})
+      if ((st = check_int(p))) return st;
+  }
+  const size_t need = plan_workspace_total(T, k, E);
+  if (need > 0) {
+    if (ws == nullptr || ws_bytes < need) return SWIGLU_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return SWIGLU_ERR_ALIGN;
+  }
+  return SWIGLU_OK;
+}
+
+// Sizes of gather and combine: whole 16-byte chunks per row; a wave for 64
+// chunks of a row, 4 waves to a workgroup and at most 2^32 - 1 threads to a
+// launch.
+inline int rows_status(int dtype, int64_t T, int64_t k, int64_t K) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if ((st = check_pairs(T, k))) return st;
+  if (K < 0 || K > kMaxDim || K % chunk_elems(dtype) != 0) return SWIGLU_ERR_SHAPE;
+  if (T > 0 && (K / chunk_elems(dtype) + 63) / 64 > (int64_t(1) << 25) / (T * k)) return SWIGLU_ERR_UNSUPPORTED;
+  if (T > (int64_t(1) << 23)) return SWIGLU_ERR_UNSUPPORTED;   // (a workgroup to a token of the backward)
+  return SWIGLU_OK;
+}
+
+// rows: tensors of whole rows; ints: 4-byte elements; opt: those that may be NULL.
+inline int validate_rows(int dtype, int64_t T, int64_t k, int64_t K, std::initializer_list<const void*> rows,
+                         std::initializer_list<const void*> ints, std::initializer_list<const void*> opt) {
+  int st = rows_status(dtype, T, k, K);
+  if (st || T == 0) return st;
+  for (const void* p : ints)
+    if ((st = check_int(p))) return st;
+  for (const void* p : opt)
+    if (!aligned(p, 4)) return SWIGLU_ERR_ALIGN;
+  if (K == 0) return SWIGLU_OK;
+  for (const void* p : rows)
+    if ((st = check_ptr(p))) return st;
+  return SWIGLU_OK;
+}
+
+// Grouped products.  Their grids hold the row tiles of R rows in E + 2 groups
+// (NT, NN), or all tiles of the experts' weights (TN); tiles are 128 rows by
+// 64 columns at least where there are many, and a launch has at most 2^32 - 1
+// threads, 512 to a workgroup.
+constexpr int64_t kGroupedMaxTiles = (int64_t(1) << 23) - 1;
+inline int grouped_shape_status(int dtype, int64_t R, int64_t E, int64_t N, int64_t K) {
+  int st = check_dtype(dtype);
+  if (st) return st;
+  if ((st = check_dims(R, N, K))) return st;
+  if (E < 1 || E > SWIGLU_MAX_EXPERTS) return SWIGLU_ERR_SHAPE;
+  if (N % chunk_elems(dtype) != 0 || K % chunk_elems(dtype) != 0) return SWIGLU_ERR_SHAPE;
+  if (2 * N > kMaxLd || K > kMaxLd) return SWIGLU_ERR_UNSUPPORTED;
+  const int64_t cols = ((N > K ? N : K) + 63) / 64, wt = 2 * ((N + 127) / 128) * ((K + 127) / 128);
+  if (cols > 0 && R / 128 + E + 2 > kGroupedMaxTiles / cols) return SWIGLU_ERR_UNSUPPORTED;
+  if (wt > 0 && E > kGroupedMaxTiles / wt) return SWIGLU_ERR_UNSUPPORTED;
+  return SWIGLU_OK;
+}
+
+inline int check_expert_stride(int dtype, int64_t E, int64_t N, int64_t K, int64_t stride) {
+  if (stride < 0 || stride % chunk_elems(dtype) != 0 || stride > (int64_t(1) << 48)) return SWIGLU_ERR_SHAPE;
+  return E > 1 && stride < N * K ? SWIGLU_ERR_SHAPE : SWIGLU_OK;
+}
+
+// src given: x is [T, K], R = T k.
+inline int check_src(int dtype, int64_t R, int64_t K, int64_t T, int64_t k, const void* src) {
+  if (src == nullptr) return SWIGLU_OK;
+  int st = check_pairs(T, k);
+  if (st) return st;
+  if (R != T * k) return SWIGLU_ERR_SHAPE;
+  if (!aligned(src, 4)) return SWIGLU_ERR_ALIGN;
+  // Byte offsets of a token's row are 32-bit.
+  return T * K * elem_size(dtype) < (int64_t(1) << 31) ? SWIGLU_OK : SWIGLU_ERR_UNSUPPORTED;
+}
+
+inline int validate_grouped_fwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
+                                int64_t k, const void* src, const void* offsets, const void* wg, int64_t sg,
+                                const void* wu, int64_t su, const void* h) {
+  int st = grouped_shape_status(dtype, R, E, N, K);
+  if (st) return st;
+  if ((st = check_expert_stride(dtype, E, N, K, sg)) || (st = check_expert_stride(dtype, E, N, K, su))) return st;
+  if ((st = check_src(dtype, R, K, T, k, src))) return st;
+  if (R == 0 || N == 0) return SWIGLU_OK;
+  if ((st = check_int(offsets)) || (st = check_ptr(h))) return st;
+  if (K == 0) return SWIGLU_OK;
+  for (const void* p : {x, wg, wu})
+    if ((st = check_ptr(p))) return st;
+  return SWIGLU_OK;
+}
+
+// Workspace of the grouped backward, regions on 256-byte boundaries: D =
+// [dg | du], [R, 2 N], and the gathered rows of x, [R, K].
+struct GroupedBwdLayout { size_t off_x, total; };
+inline GroupedBwdLayout grouped_bwd_layout(int dtype, int64_t R, int64_t N, int64_t K, bool gathered) {
+  GroupedBwdLayout L;
+  const size_t es = (size_t)elem_size(dtype);
+  L.off_x = (size_t)round_up((int64_t)(R * 2 * N * es), 256);
+  L.total = L.off_x + (gathered ? (size_t)round_up((int64_t)(R * K * es), 256) : 0);
+  return L;
+}
+inline size_t grouped_bwd_workspace_total(int dtype, int64_t R, int64_t N, int64_t K, bool gathered) {
+  return grouped_shape_status(dtype, R, 1, N, K) == SWIGLU_OK ? grouped_bwd_layout(dtype, R, N, K, gathered).total : 0;
+}
+
+inline int validate_grouped_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
+                                int64_t k, const void* src, const void* offsets, const void* wg, int64_t sg,
+                                const void* wu, int64_t su, const void* dh, const void* dx, const void* dwg,
+                                const void* dwu, const void* ws, size_t ws_bytes) {
+  int st = grouped_shape_status(dtype, R, E, N, K);
+  if (st) return st;
+  if ((st = check_expert_stride(dtype, E, N, K, sg)) || (st = check_expert_stride(dtype, E, N, K, su))) return st;
+  if ((st = check_src(dtype, R, K, T, k, src))) return st;
+  if (src != nullptr && (st = rows_status(dtype, T, k, K))) return st;
+  if ((dwg == nullptr) != (dwu == nullptr)) return SWIGLU_ERR_ARG;
+  for (const void* p : {dx, dwg, dwu})
+    if (!aligned(p, 16)) return SWIGLU_ERR_ALIGN;
+  if (K == 0 || (dx == nullptr && dwg == nullptr)) {
+    // Nothing to compute; an output that has elements must be asked for.
+    return K > 0 && ((R > 0) || (N > 0)) ? SWIGLU_ERR_NULL : SWIGLU_OK;
+  }
+  if (R > 0 || N > 0) {
+    if ((st = check_int(offsets))) return st;
+  }
+  if (R == 0 || N == 0) return SWIGLU_OK;             // outputs are zero-filled
+  for (const void* p : {x, wg, wu, dh})
+    if ((st = check_ptr(p))) return st;
+  if (ws == nullptr) return SWIGLU_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return SWIGLU_ERR_ALIGN;
+  if (ws_bytes < grouped_bwd_layout(dtype, R, N, K, src != nullptr).total) return SWIGLU_ERR_WORKSPACE;
+  return SWIGLU_OK;
+}
+
+inline int validate_grouped_mm(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x,
+                               const void* offsets, const void* w, int64_t sw, const void* y) {
+  int st = grouped_shape_status(dtype, R, E, N, K);
+  if (st) return st;
+  if ((st = check_expert_stride(dtype, E, N, K, sw))) return st;
+  if (R == 0 || N == 0) return SWIGLU_OK;
+  if ((st = check_int(offsets)) || (st = check_ptr(y))) return st;
+  if (K == 0) return SWIGLU_OK;
+  if ((st = check_ptr(x))) return st;
+  return check_ptr(w);
+}
+
+inline int validate_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x,
+                                   const void* offsets, const void* w, int64_t sw, const void* dy, const void* dx,
+                                   const void* dw) {
+  int st = grouped_shape_status(dtype, R, E, N, K);
+  if (st) return st;
+  if ((st = check_expert_stride(dtype, E, N, K, sw))) return st;
+  if (!aligned(dx, 16) || !aligned(dw, 16)) return SWIGLU_ERR_ALIGN;
+  if (K == 0 || (R == 0 && N == 0)) return SWIGLU_OK;
+  if (dx == nullptr && dw == nullptr) return SWIGLU_ERR_NULL;
+  if ((st = check_int(offsets))) return st;
+  if (R == 0 || N == 0) return SWIGLU_OK;             // outputs are zero-filled
+  if ((st = check_ptr(dy))) return st;
+  if (dw != nullptr && (st = check_ptr(x))) return st;
+  if (dx != nullptr && (st = check_ptr(w))) return st;
+  return SWIGLU_OK;
+}
+
+// ---- gradient norm and clipping
+
+// A chunk of a gradient is the work of one workgroup at a time; a launch takes
+// the tensors that its arguments hold, 4 KiB at most.
+constexpr int64_t kClipChunkBytes = 32768;
+constexpr int kClipNormTensors = 320, kClipScaleTensors = 192;
+constexpr int kClipBlocks = 2048;
+constexpr int64_t kClipMaxElems = int64_t(1) << 35;
+
+inline int64_t clip_norm_launches(int64_t count) {    // of each type at least one more
+  return (count + kClipNormTensors - 1) / kClipNormTensors + 1;
+}
+inline size_t grad_norm_workspace_total(int64_t count) {
+  if (count < 0 || count > (int64_t(1) << 20)) return 0;
+  return 256 + (size_t)clip_norm_launches(count) * kClipBlocks * 8;
+}
+
+struct ByteRange { uintptr_t first, end; };
+
+// Whether two of the ranges written to overlap, or one that is written
+// overlaps one that is read for another tensor (or its own, but for the same).
+inline int check_disjoint(int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes,
+                          void* const* outs) {
+  try {
+    std::vector<ByteRange> w;
+    w.reserve((size_t)count);
+    auto range = [&](const void* p, int64_t i) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+      return ByteRange{a, a + (uintptr_t)(sizes[i] * elem_size(dtypes[i]))};
+    };
+    for (int64_t i = 0; i < count; ++i)
+      if (sizes[i] > 0) w.push_back(range(outs != nullptr ? outs[i] : grads[i], i));
+    std::sort(w.begin(), w.end(), [](const ByteRange& a, const ByteRange& b) { return a.first < b.first; });
+    for (size_t i = 1; i < w.size(); ++i)
+      if (w[i].first < w[i - 1].end) return SWIGLU_ERR_ARG;
+    if (outs == nullptr) return SWIGLU_OK;
+    for (int64_t i = 0; i < count; ++i) {
+      if (sizes[i] == 0 || grads[i] == outs[i]) continue;
+      const ByteRange g = range(grads[i], i);
+      // The first written range that ends behind g's start.
+      auto it = std::upper_bound(w.begin(), w.end(), g.first, [](uintptr_t v, const ByteRange& r) { return v < r.end; });
+      if (it != w.end() && it->first < g.end) return SWIGLU_ERR_ARG;
+    }
+    return SWIGLU_OK;
+  } catch (const std::bad_alloc&) {
+    return SWIGLU_ERR_UNSUPPORTED;
+  }
+}
+
+// clip: gradients are written (in place, or to outs).
+inline int validate_grads(int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes,
+                          void* const* outs, bool clip, double max_norm, double eps, const void* norm, const void* ws,
+                          size_t ws_bytes) {
+  if (count < 0 || count > (int64_t(1) << 20)) return SWIGLU_ERR_SHAPE;
+  if (count > 0 && (dtypes == nullptr || grads == nullptr || sizes == nullptr)) return SWIGLU_ERR_NULL;
+  int st;
+  for (int64_t i = 0; i < count; ++i) {
+    if ((st = check_dtype(dtypes[i]))) return st;
+    if (sizes[i] < 0) return SWIGLU_ERR_SHAPE;
+    if (sizes[i] > kClipMaxElems) return SWIGLU_ERR_UNSUPPORTED;
+    if (sizes[i] == 0) continue;
+    if (grads[i] == nullptr || (outs != nullptr && outs[i] == nullptr)) return SWIGLU_ERR_NULL;
+    const uintptr_t es = (uintptr_t)elem_size(dtypes[i]);
+    if (!aligned(grads[i], es) || (outs != nullptr && !aligned(outs[i], es))) return SWIGLU_ERR_ALIGN;
+  }
+  // max_norm and eps at least 0 and not NaN; an infinite max_norm clips nothing.
+  if (clip && (!(max_norm >= 0.0) || !(eps >= 0.0) || eps - eps != 0.0)) return SWIGLU_ERR_ARG;
+  if ((st = check_int(norm))) return st;
+  if (ws == nullptr || ws_bytes < grad_norm_workspace_total(count)) return SWIGLU_ERR_WORKSPACE;
+  if (!aligned(ws, 256)) return SWIGLU_ERR_ALIGN;
+  return clip ? check_disjoint(count, dtypes, grads, sizes, outs) : SWIGLU_OK;
 }
 
 }  // namespace swg
