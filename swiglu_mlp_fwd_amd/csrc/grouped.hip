@@ -166,6 +166,14 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& p, int ntn, int bid
 
 // --------------------------------------------------------------- the kernel
 
+// The ring of k-steps in LDS: 16-byte chunks of reduction to a k-step, and
+// k-steps.  bf16 NT: five short ones, taken in turns by the halves of the
+// workgroup.  Otherwise a double buffer.
+template <typename T, Form F> struct Ring {
+  static constexpr bool kTurns = sizeof(T) == 2 && F == Form::kNT;
+  static constexpr int kChunks = kTurns ? 4 : 8, kDepth = kTurns ? 5 : 2;
+};
+
 // dh tile in LDS: row r at r * 2 BN bytes, its 16-byte chunk c at physical
 // chunk c ^ (r & 15).
 template <class TL>
@@ -177,21 +185,15 @@ struct DhTile {
   }
 };
 
-template <Out O, class TL>
-struct OutLds {                                           // staged results (16-bit outputs)
-  static constexpr int kPitch = TL::kBN * 2 + 32;
-  static constexpr int kRegion = TL::kBM * kPitch;
-  static constexpr int kBytes = (O == Out::kDGated ? 2 : 1) * kRegion;
-};
-
-template <typename T, Form F, Out O, Act ACT, int NB, class TL, int S, int kGroupM>
+template <typename T, Form F, Out O, Act ACT, int NB, class TL, int kGroupM>
 __global__ __launch_bounds__(TL::kThreads) __attribute__((amdgpu_waves_per_eu(TL::kOcc, TL::kOcc)))
 void grouped_kernel(GroupedArgs p) {
   constexpr bool kB16 = sizeof(T) == 2;
   constexpr int kMN = kB16 ? 16 : 32;                     // MFMA tile
   constexpr int kBM = TL::kBM, kBN = TL::kBN, kThreads = TL::kThreads, kWaves = kThreads / 64;
   constexpr int kWM = TL::kWM, kWN = TL::kWN, kTM = kWM / kMN, kTN = kWN / kMN;
-  constexpr int KC = 8, kRowBytes = 128;                  // a k-step: 8 chunks of 16 bytes
+  using R = Ring<T, F>;
+  constexpr int KC = R::kChunks, S = R::kDepth, kRowBytes = KC * 16;
   constexpr int kPer = 16 / (int)sizeof(T);               // elements per chunk
   constexpr int kStep = KC * kPer;                        // reduction per k-step
   constexpr int kABytes = kBM * kRowBytes, kBBytes = kBN * kRowBytes;
@@ -200,7 +202,6 @@ void grouped_kernel(GroupedArgs p) {
   constexpr int kDma = kDmaA + NB * kDmaB;
   constexpr bool kAT = F == Form::kTN, kBT = F != Form::kNT;   // reduction along the operand's rows
   static_assert(kABytes % (1024 * kWaves) == 0 && kBBytes % (1024 * kWaves) == 0, "DMA split");
-  static_assert(S == 2, "the dh tile goes into the slot of the step before the last");
   extern __shared__ u32x4 lds[];
   char* const lds_bytes = reinterpret_cast<char*>(lds);
 
@@ -212,10 +213,14 @@ void grouped_kernel(GroupedArgs p) {
   // This workgroup's tile: rows, expert, columns.
   int e, tn, row0, rows, half = 0, m0 = 0, mrows;         // row0, rows: of the expert (TN: the reduction)
   if constexpr (F == Form::kTN) {
-    const int ntm = (p.m + kBM - 1) / kBM, per = p.halves * ntm * ntn;
-    const int tile = xcd_remap(blockIdx.x, p.E * per);
-    e = tile / per;
-    const int local = tile % per, band = kGroupM * ntn, nm = p.halves * ntm;
+    // Every XCD takes an eighth of each expert's tiles, so that experts with
+    // many rows do not fall to one.
+    const int ntm = (p.m + kBM - 1) / kBM, per = p.halves * ntm * ntn, share = (per + 7) / 8;
+    const int xcd = blockIdx.x % 8, turn = blockIdx.x / 8;
+    e = turn / share;
+    const int local = xcd * share + turn % share;
+    if (local >= per) return;
+    const int band = kGroupM * ntn, nm = p.halves * ntm;
     const int g0 = (local / band) * kGroupM, gm = nm - g0 < kGroupM ? nm - g0 : kGroupM;
     const int tm = g0 + (local % band) % gm;
     tn = (local % band) / gm;
@@ -240,25 +245,26 @@ void grouped_kernel(GroupedArgs p) {
   const int nk = (F == Form::kNN ? p.halves : 1) * nkh;
 
   // ---- operand A
-  // Contiguous: instruction d of the wave fills LDS rows 8 (d kWaves + wave)
-  // .. + 7, a lane physical chunk lane % 8 of one, from logical chunk
-  // (lane % 8) ^ ((row >> 1) & 7).
+  // Contiguous: instruction d of the wave fills kRowsDma LDS rows from
+  // kRowsDma (d kWaves + wave) on, a lane physical chunk lane % KC of one, from
+  // logical chunk (lane % KC) ^ ((row >> kSwz) % KC).
   // Along rows: it fills 1 KiB of k rows, kCPR chunks each; k row kr's pair
   // of chunks q lies at pair q ^ f(kr) (bf16: f = (kr & 3) | ((kr >> 3) & 1)
   // << 2, so that the transposing reads of two 16-lane groups meet 8 different
   // pairs; fp32: chunk bit 3 ^= (kr >> 2) & 1, the halves of a wave).
-  // Lanes' offsets are the same for every d but for whole rows.
-  constexpr int kRowsPass = 8 * kWaves;                   // contiguous rows per d
+  // Lanes' offsets are the same for every d but for whole rows and, where a
+  // pass has 8 k rows, f's third bit: odd passes then have chunk bit 3 turned.
+  constexpr int kRowsDma = 64 / KC, kRowsPass = kRowsDma * kWaves;   // contiguous rows per instruction, per d
+  auto swz = [](int row) { return KC == 8 ? (row >> 1) & 7 : -(row >> 2) & 3; };
   auto lane_contig = [&](int& row, int& chunk) {
-    row = 8 * wave + (lane >> 3);
-    chunk = (lane & 7) ^ ((row >> 1) & 7);
+    row = kRowsDma * wave + lane / KC;
+    chunk = (lane % KC) ^ swz(row);
   };
-  static_assert(kWaves % 4 == 0, "a pass over d leaves the swizzles of a lane's rows alone");
+  static_assert(kRowsPass % 16 == 0, "a pass over d leaves the swizzle of a lane's rows alone");
   auto lane_along = [&](auto cpr_c, int& kr, int& chunk) {
     constexpr int cpr = decltype(cpr_c)::value;           // chunks per k row
     constexpr int rpi = 64 / cpr;                         // k rows per instruction
-    static_assert((rpi * kWaves) % 16 == 0 || !kB16, "f is the same for every d");
-    static_assert((rpi * kWaves) % 8 == 0, "f is the same for every d");
+    static_assert((rpi * kWaves) % 8 == 0, "f is the same for every second d");
     kr = rpi * wave + lane / cpr;
     const int c = lane % cpr;
     if constexpr (kB16) chunk = c ^ (((kr & 3) | (((kr >> 3) & 1) << 2)) << 1);
@@ -268,15 +274,17 @@ void grouped_kernel(GroupedArgs p) {
 
   const T* abase = static_cast<const T*>(p.a);
   int64_t abytes = 0;                                     // contiguous: descriptor; along rows: all that is left
-  uint32_t avoff[kAT ? 1 : kDmaA];
+  uint32_t avoff[kAT ? 2 : kDmaA];
   int achunk = 0;
   constexpr int kACpr = kBM / kPer, kBCpr = kBN / kPer;
+  constexpr bool kATurn = kB16 && 64 / kACpr * kWaves == 8, kBTurn = kB16 && 64 / kBCpr * kWaves == 8;
   if constexpr (kAT) {
     int kr;
     lane_along(std::integral_constant<int, kACpr>{}, kr, achunk);
     abase += (int64_t)row0 * p.lda + (int64_t)half * p.m + m0;
     abytes = rows > 0 ? ((int64_t)rows * p.lda - half * p.m - m0) * es : 0;
     avoff[0] = (uint32_t)(kr * (int)p.lda * es + achunk * 16);
+    avoff[1] = kATurn ? avoff[0] - achunk * 16 + (achunk ^ 8) * 16 : avoff[0];
   } else {
     int r;
     lane_contig(r, achunk);
@@ -303,7 +311,7 @@ void grouped_kernel(GroupedArgs p) {
   // ---- operand B
   const T* bbase[2];
   int64_t bbytes;
-  uint32_t bvoff;
+  uint32_t bvoff[2];
   int bchunk;
   const int64_t ebase = live ? e : 0;
   if constexpr (F == Form::kTN) {
@@ -326,11 +334,12 @@ void grouped_kernel(GroupedArgs p) {
   if constexpr (kBT) {
     int kr;
     lane_along(std::integral_constant<int, kBCpr>{}, kr, bchunk);
-    bvoff = (uint32_t)(kr * (int)p.ldb * es + bchunk * 16);
+    bvoff[0] = (uint32_t)(kr * (int)p.ldb * es + bchunk * 16);
+    bvoff[1] = kBTurn ? bvoff[0] - bchunk * 16 + (bchunk ^ 8) * 16 : bvoff[0];
   } else {
     int r;
     lane_contig(r, bchunk);
-    bvoff = (uint32_t)(r * (int)p.ldb * es + bchunk * 16);
+    bvoff[0] = bvoff[1] = (uint32_t)(r * (int)p.ldb * es + bchunk * 16);
   }
   constexpr int kBRowsPass = kBT ? 64 / kBCpr * kWaves : kRowsPass;
   constexpr int kARowsPass = 64 / kACpr * kWaves;         // (along rows)
@@ -344,70 +353,61 @@ void grouped_kernel(GroupedArgs p) {
     const int64_t left = all - s * step;
     return left < 0 ? 0 : (left < step ? left : step);
   };
-  auto issue = [&](int ks) {
-    char* dst = lds_bytes + (ks % S) * kStageBytes + wave * 1024;
+  // Instruction q of this wave's kDma for k-step ks, into a slot: A's first.
+  auto issue_one = [&](int ks, int slot, int q) {
     const int h = F == Form::kNN && ks >= nkh ? 1 : 0;
     const int s = ks - h * nkh;
     const int rem = (red + kPer - 1) / kPer - s * KC;     // chunks of reduction left (contiguous)
     const bool past = ks >= nk;
-    if constexpr (kAT) {
-      const __amdgpu_buffer_rsrc_t rs =
-          uniform_rsrc(abase + (int64_t)s * kStep * p.lda, past ? 0 : step_bytes(abytes, p.lda, s));
-#pragma unroll
-      for (int d = 0; d < kDmaA; ++d) {
-        const uint32_t off = avoff[0] + d * apass;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(dst + d * kWaves * 1024), 16, off, 0, 0, 0);
+    char* dst = lds_bytes + slot * kStageBytes + wave * 1024;
+    if (q < kDmaA) {
+      dst += q * kWaves * 1024;
+      if constexpr (kAT) {
+        const __amdgpu_buffer_rsrc_t rs =
+            uniform_rsrc(abase + (int64_t)s * kStep * p.lda, past ? 0 : step_bytes(abytes, p.lda, s));
+        const uint32_t off = avoff[q & 1] + q * apass;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, off, 0, 0, 0);
+      } else {
+        const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(abase, past ? 0 : abytes);
+        const uint32_t off = achunk < rem ? avoff[q % (kAT ? 2 : kDmaA)] + (uint32_t)((h * p.r + s * kStep) * es) : kOob;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, off, 0, 0, 0);
       }
     } else {
-      const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(abase, past ? 0 : abytes);
-      const bool in = achunk < rem;
-      const uint32_t at = (uint32_t)((h * p.r + s * kStep) * es);
-#pragma unroll
-      for (int d = 0; d < kDmaA; ++d) {
-        const uint32_t off = in ? avoff[d] + at : kOob;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(dst + d * kWaves * 1024), 16, off, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int w = 0; w < NB; ++w) {
-      char* bd = dst + kABytes + w * kBBytes;
+      const int w = (q - kDmaA) / kDmaB, d = (q - kDmaA) % kDmaB;
+      dst += kABytes + w * kBBytes + d * kWaves * 1024;
       if constexpr (kBT) {
         const __amdgpu_buffer_rsrc_t rs =
             uniform_rsrc(bbase[F == Form::kNN ? h : 0] + (int64_t)s * kStep * p.ldb, past ? 0 : step_bytes(bbytes, p.ldb, s));
-#pragma unroll
-        for (int d = 0; d < kDmaB; ++d)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(bd + d * kWaves * 1024), 16, bvoff + d * bpass, 0,
-                                                   0, 0);
+        const uint32_t off = bvoff[d & 1] + d * bpass;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, off, 0, 0, 0);
       } else {
         const __amdgpu_buffer_rsrc_t rs = uniform_rsrc(bbase[w], past ? 0 : bbytes);
-        const uint32_t off = bchunk < rem ? bvoff + (uint32_t)(s * kStep * es) : kOob;
-#pragma unroll
-        for (int d = 0; d < kDmaB; ++d)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)(bd + d * kWaves * 1024), 16, off + d * bpass, 0, 0,
-                                                   0);
+        const uint32_t off = bchunk < rem ? bvoff[0] + (uint32_t)(s * kStep * es) + d * bpass : kOob;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)dst, 16, off, 0, 0, 0);
       }
     }
   };
+  auto issue = [&](int ks, int slot) {
+#pragma unroll
+    for (int q = 0; q < kDma; ++q) issue_one(ks, slot, q);
+  };
 
-  // The dh tile (recompute, bf16) by DMA into a ring slot: an instruction
-  // fills 1 KiB of rows, a lane's chunk c of row r from logical chunk
-  // c ^ (r & 15); chunks past the last column and rows past the tile's read
-  // zero (n is a multiple of 8).
+  // The dh tile (recompute, bf16) by DMA, its two halves of rows in place of
+  // the two k-steps behind the last: an instruction fills 1 KiB of rows, a
+  // lane's chunk c of row r from logical chunk c ^ (r & 15); chunks past the
+  // last column and rows past the tile's read zero (n is a multiple of 8).
   constexpr bool kDh = O == Out::kDGated && kB16;
-  auto issue_dh = [&](int slot) {
-    constexpr int kCPR = DhTile<TL>::kCPR, kRpi = 64 / kCPR;
-    static_assert(!kDh || (kCPR == 16 && kBM * DhTile<TL>::kPitch <= kStageBytes), "the dh tile fits a slot");
+  auto issue_dh = [&](int part, int slot, int d) {
+    constexpr int kCPR = DhTile<TL>::kCPR, kRpi = 64 / kCPR, kHalf = kBM / 2;
+    static_assert(!kDh || (kCPR == 16 && kHalf * DhTile<TL>::kPitch == kStageBytes && kHalf / (kRpi * kWaves) == kDma),
+                  "a half of the dh tile fills a slot by as many instructions");
     const T* d0 = static_cast<const T*>(p.dh) + (int64_t)row0 * p.n + n0;
     const __amdgpu_buffer_rsrc_t rd = uniform_rsrc(d0, ((int64_t)rows * p.n - n0) * es);
-    char* dst = lds_bytes + slot * kStageBytes + wave * 1024;
-    constexpr int kPasses = kBM / (kRpi * kWaves);
-#pragma unroll
-    for (int d = 0; d < kPasses; ++d) {
-      const int r = (d * kWaves + wave) * kRpi + lane / kCPR;
-      const int c = (lane % kCPR) ^ (r & 15);
-      const uint32_t off = n0 + c * 8 < p.n && r < rows ? (uint32_t)(r * p.n * es + c * 16) : kOob;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_void_t*)(dst + d * kWaves * 1024), 16, off, 0, 0, 0);
-    }
+    char* dst = lds_bytes + slot * kStageBytes + (d * kWaves + wave) * 1024;
+    const int r = part * kHalf + (d * kWaves + wave) * kRpi + lane / kCPR;
+    const int c = (lane % kCPR) ^ (r & 15);
+    const uint32_t off = n0 + c * 8 < p.n && r < rows ? (uint32_t)(r * p.n * es + c * 16) : kOob;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_void_t*)dst, 16, off, 0, 0, 0);
   };
 
   typename AccL<kMN>::V acc[NB][kTM][kTN];
@@ -426,7 +426,7 @@ void grouped_kernel(GroupedArgs p) {
   constexpr int kKK = KC / kCPS;
   const int rl = lane % kMN, ql = lane / kMN;
   auto frag_contig = [&](const char* L, int row, int kk) -> u32x4 {
-    const int pc = (kCPS * kk + ql) ^ ((row >> 1) & 7);
+    const int pc = (kCPS * kk + ql) ^ swz(row);
     return *reinterpret_cast<const u32x4*>(L + row * kRowBytes + pc * 16);
   };
   // Along rows, columns c0 .. c0 + kMN - 1 of tiles of `cols` columns.
@@ -465,159 +465,258 @@ void grouped_kernel(GroupedArgs p) {
         else bv[buf][w][j] = frag_contig(LB, wn * kWN + j * kMN + rl, kk);
       }
   };
-  auto mfmas = [&](int buf) {
+  constexpr int kMf = NB * kTM * kTN;                     // MFMAs of a sub-step
+  auto mfmas = [&](int buf, int from, int to) {
 #pragma unroll
     for (int w = 0; w < NB; ++w)
 #pragma unroll
       for (int i = 0; i < kTM; ++i)
 #pragma unroll
         for (int j = 0; j < kTN; ++j) {
+          const int at = (w * kTM + i) * kTN + j;
+          if (at < from || at >= to) continue;
           if constexpr (kB16)
-            acc[w][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av[buf][i]),
-                                                                   __builtin_bit_cast(bf16x8, bv[buf][w][j]),
+            acc[w][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bv[buf][w][j]),
+                                                                   __builtin_bit_cast(bf16x8, av[buf][i]),
                                                                    acc[w][i][j], 0, 0, 0);
           else
-            Mma<T>::run(acc[w][i][j], av[buf][i], bv[buf][w][j]);
+            Mma<T>::run(acc[w][i][j], bv[buf][w][j], av[buf][i]);
         }
   };
   auto landed = [&]() {                                   // this wave's DMA has landed, its LDS reads are done
     wait_vmcnt<0>();
     __builtin_amdgcn_s_waitcnt(0xC07F);
   };
+  // Some row of the wave's is the tile's.
+  const bool active = wm * kWM < mrows;
 
-  // Every step of the ring is issued, also those past the last, which read
-  // nothing; the slot of the step before the last takes the dh tile.
-  auto refill = [&](int ks) {
-    if (kDh && ks == nk) issue_dh(ks % S);
-    else issue(ks);
-  };
-  static_assert(kKK % 2 == 0, "the next step's first fragments go to buffer 0");
-  issue(0);
-  if (kDh && nk == 1) issue_dh(1);
-  else issue(1);
-  // wm * kWM < mrows: some row of the wave's is the tile's.
-  if (wm * kWM < mrows) {
-    if (nk > 0) {
-      wait_vmcnt<kDma>();
-      __builtin_amdgcn_s_waitcnt(0xC07F);
-      if (kDh && nk == 1) wait_vmcnt<0>();
-      barrier_no_fence();
-      read_frags(0, lds_bytes, 0);
-    }
-    auto kstep = [&](int ks, bool more) {
-      const char* L = lds_bytes + (ks % S) * kStageBytes;
+  if constexpr (R::kTurns) {
+    // Two halves of the workgroup, one wave of each on a SIMD, half a k-step
+    // apart: in turn `it` the first half reads its fragments of k-step `it` and
+    // multiplies them, the second multiplies those of the k-step before and
+    // then reads, so that one half's reads fall into the other's products.
+    // One barrier to a turn: behind it k-step `it` is in LDS and k-step it - 1
+    // has been read by all, so its slot is filled with k-step it + S - 1, an
+    // instruction at a time between the products.  Every k-step of the ring is
+    // requested, also those behind the last, which read nothing (or the dh
+    // tile), so that the count of loads in flight says which have landed.
+    static_assert(kWaves == 8 && KC == kCPS, "two waves to a SIMD, a sub-step to a k-step");
+    auto request = [&](int ks, int slot, int q) {
+      if (kDh && (ks == nk || ks == nk + 1)) issue_dh(ks - nk, slot, q);
+      else issue_one(ks, slot, q);
+    };
 #pragma unroll
-      for (int kk = 0; kk < kKK; ++kk) {
+    for (int t = 0; t < S - 1; ++t)
+#pragma unroll
+      for (int q = 0; q < kDma; ++q) request(t, t, q);
+    int slot = 0, next = S - 1;                           // of k-step it and of it + S - 1
+    auto products = [&](int it) {
+#pragma unroll
+      for (int q = 0; q < kDma; ++q) {
         __builtin_amdgcn_sched_barrier(0);
-        if (kk + 1 < kKK) {
-          read_frags((kk + 1) & 1, L, kk + 1);
-        } else if (more) {
-          landed();                                       // step ks + 1
-          barrier_no_fence();                             // and every wave has read step ks
+        request(it + S - 1, next, q);
+        __builtin_amdgcn_sched_barrier(0);
+        mfmas(0, q * (kMf / kDma), (q + 1) * (kMf / kDma));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto turn = [&]() {                                   // k-step `it` has landed, it - 1 is read
+      wait_vmcnt<(S - 2) * kDma>();
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+      barrier_no_fence();
+    };
+    auto advance = [&]() {
+      next = slot;
+      slot = slot + 1 == S ? 0 : slot + 1;
+    };
+    if (!active) {
+      for (int it = 0; it < nk; ++it) {
+        turn();
+#pragma unroll
+        for (int q = 0; q < kDma; ++q) request(it + S - 1, next, q);
+        advance();
+      }
+      barrier_no_fence();
+    } else if (wave < 4) {
+      for (int it = 0; it < nk; ++it) {
+        turn();
+        read_frags(0, lds_bytes + slot * kStageBytes, 0);
+        products(it);
+        advance();
+      }
+      barrier_no_fence();
+    } else {
+      turn();
+      if (nk > 0) {
+        read_frags(0, lds_bytes, 0);
+#pragma unroll
+        for (int q = 0; q < kDma; ++q) request(S - 1, next, q);
+        advance();
+        for (int it = 1; it < nk; ++it) {
+          turn();
+          products(it);
+          read_frags(0, lds_bytes + slot * kStageBytes, 0);
+          advance();
+        }
+        turn();
+        mfmas(0, 0, kMf);
+      }
+    }
+  } else {
+    // A double buffer of LDS and of fragments: the fragments of a sub-step are
+    // read between the products of the one before, the step boundary lies in
+    // the last sub-step.
+    static_assert(S == 2 && (KC / kCPS) % 2 == 0, "the next step's first fragments go to buffer 0");
+    constexpr int kKK = KC / kCPS;
+    constexpr int kRd = kTM * (kAT ? 2 : 1) + NB * kTN * (kBT ? 2 : 1);   // LDS reads of a sub-step (bf16)
+    issue(0, 0);
+    issue(1, 1);
+    wait_vmcnt<kDma>();
+    barrier_no_fence();
+    if (active) {
+      if (nk > 0) read_frags(0, lds_bytes, 0);
+      auto kstep = [&](int ks, bool more) {
+        const char* L = lds_bytes + (ks % S) * kStageBytes;
+#pragma unroll
+        for (int kk = 0; kk < kKK; ++kk) {
           __builtin_amdgcn_sched_barrier(0);
-          read_frags(0, lds_bytes + ((ks + 1) % S) * kStageBytes, 0);
-          refill(ks + S);
+          if (kk + 1 < kKK) {
+            read_frags((kk + 1) & 1, L, kk + 1);
+            if constexpr (kB16) {
+              mfmas(kk & 1, 0, kMf);
+#pragma unroll
+              for (int t = 0; t < kRd; ++t) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+              }
+              __builtin_amdgcn_sched_group_barrier(0x008, kMf, 0);
+              continue;
+            }
+          } else if (more) {
+            landed();                                     // step ks + 1
+            barrier_no_fence();                           // and every wave has read step ks
+            __builtin_amdgcn_sched_barrier(0);
+            read_frags(0, lds_bytes + ((ks + 1) % S) * kStageBytes, 0);
+            issue(ks + S, ks % S);
+            if constexpr (kB16) {
+              mfmas(kk & 1, 0, kMf);
+              constexpr int kLead = kMf / kDma > 0 ? kMf / kDma : 1;
+              __builtin_amdgcn_sched_group_barrier(0x008, kLead, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, kRd, 0);
+              __builtin_amdgcn_sched_group_barrier(0x020, kDma, 0);
+              __builtin_amdgcn_sched_group_barrier(0x008, kMf - kLead, 0);
+              continue;
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          mfmas(kk & 1, 0, kMf);
         }
         __builtin_amdgcn_sched_barrier(0);
-        mfmas(kk & 1);
+      };
+      for (int ks = 0; ks + 1 < nk; ++ks) kstep(ks, true);
+      if (nk > 0) kstep(nk - 1, false);
+    } else {
+      // Only rows behind the expert's last: this wave's share of the operands.
+      for (int ks = 0; ks + 1 < nk; ++ks) {
+        landed();
+        barrier_no_fence();
+        issue(ks + S, ks % S);
       }
-    };
-    for (int ks = 0; ks + 1 < nk; ++ks) kstep(ks, true);
-    if (nk > 0) kstep(nk - 1, false);
-  } else if (nk > 0) {
-    // Only rows behind the expert's last: this wave's share of the operands.
-    landed();
-    barrier_no_fence();
-    for (int ks = 0; ks + 1 < nk; ++ks) {
-      landed();
-      barrier_no_fence();
-      refill(ks + S);
     }
   }
-  landed();
-  barrier_no_fence();                                     // the ring is idle; the dh tile is there
+  if constexpr (kDh) {                                    // the dh tile is there
+    landed();
+    barrier_no_fence();
+  } else {
+    wait_vmcnt<0>();                                      // no load still lands in LDS when the waves end
+  }
+  if (!active) return;
 
-  // ---- results
+  // ---- results, from the registers.  The products are formed transposed
+  // (B's fragment first), so a lane's 4 consecutive accumulators are columns
+  // of one row.
   T* const out0 = static_cast<T*>(half == 0 ? p.out0 : p.out1);
   const int64_t orow0 = F == Form::kTN ? (int64_t)e * p.m + m0 : row0;
-  if constexpr (!kB16) {
-    if (wm * kWM >= mrows) return;
+  // One value of output `o` (dg, du of the recompute) from the accumulators.
+  auto value = [&](int o, float g, float u, float dh) -> float {
+    if constexpr (O == Out::kGated) {
+      return act_of<ACT, kB16>(g) * u;
+    } else if constexpr (O == Out::kDGated) {
+      float a, da;
+      act_and_slope<ACT, kB16>(g, a, da);
+      return o == 0 ? dh * u * da : dh * a;
+    } else {
+      return g;
+    }
+  };
+  constexpr int kOuts = O == Out::kDGated ? 2 : 1;
+  if constexpr (kB16) {
+    // Two tiles of 16 columns together: a swap of 16-lane rows gives every
+    // lane 8 neighbouring columns, and the four lanes of a row 64 bytes.
+    const int g = lane >> 4;
+    const int mycol = n0 + wn * kWN + (g & 1) * 16 + (g >> 1) * 8;
 #pragma unroll
-    for (int i = 0; i < kTM; ++i)
+    for (int i = 0; i < kTM; ++i) {
+      const int row = wm * kWM + i * 16 + (lane & 15);
+      const bool in = row < mrows;
+      T* o = out0 + (orow0 + row) * p.ldo + mycol;
+#pragma unroll
+      for (int j = 0; j < kTN; j += 2) {
+        u32x2 dh[2];
+        if constexpr (O == Out::kDGated) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const char* D = lds_bytes + ((nk + (row < kBM / 2 ? 0 : 1)) % S) * kStageBytes;
+            dh[t] = *reinterpret_cast<const u32x2*>(
+                D + DhTile<TL>::offset(row % (kBM / 2), wn * kWN + (j + t) * 16 + 4 * g));
+          }
+        }
+#pragma unroll
+        for (int out = 0; out < kOuts; ++out) {
+          u32x2 v[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+              float f[2];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                float d = 0.0f;
+                if constexpr (O == Out::kDGated) d = bits_f32(z ? dh[t][q >> 1] & 0xFFFF0000u : dh[t][q >> 1] << 16);
+                f[z] = value(out, acc[0][i][j + t][q + z], acc[NB - 1][i][j + t][q + z], d);
+              }
+              v[t][q >> 1] = __builtin_bit_cast(uint32_t, bf16x2{to_bf16(f[0]), to_bf16(f[1])});
+            }
+          const auto lo = __builtin_amdgcn_permlane16_swap(v[0][0], v[1][0], false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(v[0][1], v[1][1], false, false);
+          if (in && mycol + j * 16 < p.n)
+            *reinterpret_cast<u32x4*>(o + out * (int64_t)p.n + j * 16) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      const int row = wm * kWM + i * 32 + (lane & 31);
+      if (row >= mrows) continue;
 #pragma unroll
       for (int j = 0; j < kTN; ++j)
 #pragma unroll
-        for (int q = 0; q < AccL<kMN>::kE; ++q) {
-          const int row = wm * kWM + i * kMN + AccL<kMN>::row(lane, q);
-          const int col = n0 + wn * kWN + j * kMN + AccL<kMN>::col(lane);
-          if (row >= mrows || col >= p.n) continue;
+        for (int q = 0; q < 16; q += 4) {
+          const int col = n0 + wn * kWN + j * 32 + AccL<32>::row(lane, q);
+          if (col >= p.n) continue;
           T* o = out0 + (orow0 + row) * p.ldo + col;
-          if constexpr (O == Out::kGated) {
-            *o = cvt_out<T>(act_of<ACT, false>(acc[0][i][j][q]) * acc[NB - 1][i][j][q]);
-          } else if constexpr (O == Out::kDGated) {
-            const float dh = load_in<T>(static_cast<const T*>(p.dh) + (int64_t)(row0 + row) * p.n + col);
-            float a, da;
-            act_and_slope<ACT, false>(acc[0][i][j][q], a, da);
-            o[0] = cvt_out<T>(dh * acc[NB - 1][i][j][q] * da);
-            o[p.n] = cvt_out<T>(dh * a);
-          } else {
-            *o = cvt_out<T>(acc[0][i][j][q]);
+          f32x4 dh = {0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (O == Out::kDGated)
+            dh = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.dh) + (int64_t)(row0 + row) * p.n + col);
+#pragma unroll
+          for (int out = 0; out < kOuts; ++out) {
+            f32x4 v;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) v[z] = value(out, acc[0][i][j][q + z], acc[NB - 1][i][j][q + z], dh[z]);
+            *reinterpret_cast<f32x4*>(o + out * (int64_t)p.n) = v;
           }
         }
-  } else {
-    constexpr int kPitch = OutLds<O, TL>::kPitch, kRegion = OutLds<O, TL>::kRegion;
-    u32x2 dhv[O == Out::kDGated ? kTM : 1][O == Out::kDGated ? kTN : 1];   // 4 bf16 each
-    if constexpr (O == Out::kDGated) {
-      // dh in accumulator layout, 4 rows of a 16-column run per transposing read.
-      const char* D = lds_bytes + (nk % S) * kStageBytes;
-      const int s = lane & 15;
-#pragma unroll
-      for (int i = 0; i < kTM; ++i)
-#pragma unroll
-        for (int j = 0; j < kTN; ++j) {
-          const int row = wm * kWM + i * 16 + 4 * (lane >> 4) + (s >> 2);
-          const int col = wn * kWN + j * 16 + 4 * (s & 3);
-          const short4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_short4_t*)(lds_char_t*)(D + DhTile<TL>::offset(row, col)));
-          dhv[i][j] = __builtin_bit_cast(u32x2, v);
-        }
-      __builtin_amdgcn_s_waitcnt(0xC07F);
-      barrier_no_fence();
-    }
-    if (wm * kWM < mrows) {
-#pragma unroll
-      for (int i = 0; i < kTM; ++i)
-#pragma unroll
-        for (int j = 0; j < kTN; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int row = wm * kWM + i * 16 + AccL<16>::row(lane, q);
-            const int col = wn * kWN + j * 16 + AccL<16>::col(lane);
-            bf16* at = reinterpret_cast<bf16*>(lds_bytes + row * kPitch + col * 2);
-            if constexpr (O == Out::kGated) {
-              *at = to_bf16(act_of<ACT, true>(acc[0][i][j][q]) * acc[NB - 1][i][j][q]);
-            } else if constexpr (O == Out::kDGated) {
-              const uint32_t two = dhv[i][j][q >> 1];
-              const float dh = bits_f32((q & 1) ? two & 0xFFFF0000u : two << 16);
-              float a, da;
-              act_and_slope<ACT, true>(acc[0][i][j][q], a, da);
-              *at = to_bf16(dh * acc[NB - 1][i][j][q] * da);
-              at[kRegion / 2] = to_bf16(dh * a);
-            } else {
-              *at = to_bf16(acc[0][i][j][q]);
-            }
-          }
-    }
-    __syncthreads();
-    constexpr int kCPR = kBN / 8;                         // 16-byte chunks per row; n is a multiple of 8
-    for (int c = tid; c < mrows * kCPR; c += kThreads) {
-      const int r = c / kCPR, ch = c % kCPR;
-      const int col = n0 + ch * 8;
-      if (col >= p.n) continue;
-      bf16* o = reinterpret_cast<bf16*>(out0) + (orow0 + r) * p.ldo + col;
-      const char* at = lds_bytes + r * kPitch + ch * 16;
-      *reinterpret_cast<u32x4*>(o) = *reinterpret_cast<const u32x4*>(at);
-      if constexpr (O == Out::kDGated) *reinterpret_cast<u32x4*>(o + p.n) = *reinterpret_cast<const u32x4*>(at + kRegion);
     }
   }
 }
@@ -627,19 +726,17 @@ hipError_t launch(const GroupedArgs& a, hipStream_t s) {
   const int64_t ntn = ((int64_t)a.n + TL::kBN - 1) / TL::kBN;
   int64_t tiles;
   if (F == Form::kTN) {
-    tiles = (int64_t)a.E * a.halves * (((int64_t)a.m + TL::kBM - 1) / TL::kBM) * ntn;
+    tiles = 8 * (int64_t)a.E * ((a.halves * (((int64_t)a.m + TL::kBM - 1) / TL::kBM) * ntn + 7) / 8);
   } else {
     // Row tiles of R rows in at most min(E + 2, R) groups that have any.
     const int64_t groups = a.E + 2 < a.R ? a.E + 2 : a.R;
     tiles = (a.R / TL::kBM + groups) * ntn;
   }
   if (tiles == 0) return hipSuccess;
-  const size_t ring = (size_t)2 * (TL::kBM + NB * TL::kBN) * 128;
-  const size_t epi = sizeof(T) == 2 ? (size_t)OutLds<O, TL>::kBytes : 0;
-  const size_t lds = ring > epi ? ring : epi;
-  const hipError_t attr = allow_lds<&grouped_kernel<T, F, O, ACT, NB, TL, 2, kGroupM>>(lds);
+  const size_t lds = (size_t)Ring<T, F>::kDepth * (TL::kBM + NB * TL::kBN) * Ring<T, F>::kChunks * 16;
+  const hipError_t attr = allow_lds<&grouped_kernel<T, F, O, ACT, NB, TL, kGroupM>>(lds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((grouped_kernel<T, F, O, ACT, NB, TL, 2, kGroupM>), dim3((unsigned)tiles), dim3(TL::kThreads), lds,
+  hipLaunchKernelGGL((grouped_kernel<T, F, O, ACT, NB, TL, kGroupM>), dim3((unsigned)tiles), dim3(TL::kThreads), lds,
                      s, a);
   return hipGetLastError();
 }
