@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Addresses have 48 bits: a tensor's address and the elements of its last
+// Addresses have 48 bits: a tensor's address and where it ends in its last
 // chunk, less one, in one word.
 template <int kTensors, bool kOut>
 struct Table {
@@ -80,52 +80,76 @@ __device__ __forceinline__ int tensor_of(const Tab& t, uint32_t chunk) {
   return lo;
 }
 
-// Chunk `c`: its first element's address and its elements.
+// A chunk: 32 KiB of memory from a 16-byte boundary on, of which the elements
+// lo .. hi - 1 are its tensor's (all of them but in a tensor's first and last
+// chunk).  Chunks start on 16 bytes wherever their tensor does: loads of
+// views that start at odd elements took 15 % longer.
+struct Chunk {
+  uint64_t at;       // address of element 0
+  int64_t element;   // its number in the tensor (negative in front of it)
+  int tensor, lo, hi;
+};
 template <typename T, class Tab>
-__device__ __forceinline__ void chunk_of(const Tab& t, uint32_t c, int& tensor, int64_t& offset, int& n) {
-  tensor = tensor_of(t, c);
-  const uint32_t k = c - t.first[tensor];
-  offset = (int64_t)k * kChunk<T>;
-  n = c + 1 == t.first[tensor + 1] ? (int)(t.at[tensor] & 0xFFFF) + 1 : (int)kChunk<T>;
+__device__ __forceinline__ Chunk chunk_of(const Tab& t, uint32_t c) {
+  Chunk k;
+  k.tensor = tensor_of(t, c);
+  const uint64_t word = t.at[k.tensor], at = word >> 16;
+  const uint32_t i = c - t.first[k.tensor];
+  const int skip = (int)(at & 15) / (int)sizeof(T);
+  k.at = (at & ~(uint64_t)15) + (uint64_t)i * kClipChunkBytes;
+  k.element = (int64_t)i * kChunk<T> - skip;
+  k.lo = i == 0 ? skip : 0;
+  k.hi = c + 1 == t.first[k.tensor + 1] ? (int)(word & 0xFFFF) + 1 : (int)kChunk<T>;
+  return k;
+}
+
+constexpr int kU = 8;                                     // 16-byte pieces of a whole chunk per thread
+static_assert(kClipChunkBytes == (int64_t)kU * kThreads * 16, "a chunk is kU pieces per thread");
+
+// The pieces of a chunk that is not whole: f(piece) for its whole 16-byte
+// pieces, g(element) for the few elements in front of them and behind.
+template <int kN, class P, class E>
+__device__ __forceinline__ void ragged(const Chunk& k, P&& piece, E&& element) {
+  const int tid = threadIdx.x, p0 = (k.lo + kN - 1) / kN, p1 = k.hi / kN;
+  for (int u = p0 + tid; u < p1; u += kThreads) piece(u);
+  const int head = p0 * kN < k.hi ? p0 * kN : k.hi;       // elements lo .. head - 1
+  const int tail = p1 * kN > head ? p1 * kN : head;       // elements tail .. hi - 1
+  if (k.lo + tid < head) element(k.lo + tid);
+  if (tail + tid < k.hi) element(tail + tid);
 }
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void norm_kernel(Table<kClipNormTensors, false> t, double* part) {
   constexpr int kN = Elems<T>::kN;
   const int tid = threadIdx.x;
+  const uint32_t chunks = t.first[t.count];
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
-  for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    int i, n;
-    int64_t off;
-    chunk_of<T>(t, c, i, off, n);
-    const global_char* g = (const global_char*)((t.at[i] >> 16) + (uint64_t)off * sizeof(T));
-    const int full = n / kN;                              // whole 16-byte pieces
-    constexpr int kU = 8;                                 // pieces of a whole chunk per thread
-    static_assert(kChunk<T> == (int64_t)kU * kThreads * kN, "a chunk is kU pieces per thread");
-    if (n == (int)kChunk<T>) {
+  auto add = [&](const u32x4& v) {
+#pragma unroll
+    for (int q = 0; q < kN; ++q) {
+      const double d = (double)Elems<T>::get(v, q);
+      acc[q & 3] = __builtin_fma(d, d, acc[q & 3]);
+    }
+  };
+  Chunk next = chunk_of<T>(t, blockIdx.x);
+  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const Chunk k = next;
+    const global_char* g = (const global_char*)k.at;
+    const uint32_t after = c + gridDim.x < chunks ? c + gridDim.x : c;
+    if (k.lo == 0 && k.hi == (int)kChunk<T>) {
       u32x4 v[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) v[u] = load16(g + (u * kThreads + tid) * 16);
+      next = chunk_of<T>(t, after);                       // while the loads are on their way
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
-#pragma unroll
-        for (int q = 0; q < kN; ++q) {
-          const double d = (double)Elems<T>::get(v[u], q);
-          acc[q & 3] = __builtin_fma(d, d, acc[q & 3]);
-        }
+      for (int u = 0; u < kU; ++u) add(v[u]);
     } else {
-      for (int u = tid; u < full; u += kThreads) {
-        const u32x4 v = load16(g + u * 16);
-#pragma unroll
-        for (int q = 0; q < kN; ++q) {
-          const double d = (double)Elems<T>::get(v, q);
-          acc[q & 3] = __builtin_fma(d, d, acc[q & 3]);
-        }
-      }
-      if (full * kN + tid < n) {
-        const double d = (double)load1(T{}, g + (full * kN + tid) * (int)sizeof(T));
-        acc[0] = __builtin_fma(d, d, acc[0]);
-      }
+      next = chunk_of<T>(t, after);
+      ragged<kN>(k, [&](int u) { add(load16(g + u * 16)); },
+                 [&](int e) {
+                   const double d = (double)load1(T{}, g + e * (int)sizeof(T));
+                   acc[0] = __builtin_fma(d, d, acc[0]);
+                 });
     }
   }
   double s = (acc[0] + acc[1]) + (acc[2] + acc[3]);
@@ -180,30 +204,29 @@ __global__ __launch_bounds__(kThreads) void scale_kernel(Tab t, const float* fac
   const float f = *factor;
   if (!kOut && f == 1.0f) return;
   const int tid = threadIdx.x;
-  for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    int i, n;
-    int64_t off;
-    chunk_of<T>(t, c, i, off, n);
-    const global_char* g = (const global_char*)((t.at[i] >> 16) + (uint64_t)off * sizeof(T));
-    global_char* o = (global_char*)((kOut ? t.to[i] : t.at[i] >> 16) + (uint64_t)off * sizeof(T));
-    const int full = n / kN;
-    constexpr int kU = 8;
-    if (n == (int)kChunk<T>) {
+  const uint32_t chunks = t.first[t.count];
+  // From the last chunk back: what the norm's pass read last is still in the
+  // memory-side cache (256 MB).
+  Chunk next = chunk_of<T>(t, chunks - 1 - blockIdx.x);
+  for (uint32_t b = blockIdx.x; b < chunks; b += gridDim.x) {
+    const Chunk k = next;
+    const global_char* g = (const global_char*)k.at;
+    global_char* o = kOut ? (global_char*)(t.to[k.tensor] + (uint64_t)(k.element * (int64_t)sizeof(T))) : (global_char*)k.at;
+    const uint32_t after = chunks - 1 - (b + gridDim.x < chunks ? b + gridDim.x : b);
+    if (k.lo == 0 && k.hi == (int)kChunk<T>) {
       u32x4 v[kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) v[u] = load16(g + (u * kThreads + tid) * 16);
+      next = chunk_of<T>(t, after);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const u32x4 w = scaled<T>(v[u], f);
-        store16(o + (u * kThreads + tid) * 16, w);
-      }
+      for (int u = 0; u < kU; ++u) store16(o + (u * kThreads + tid) * 16, scaled<T>(v[u], f));
     } else {
-      for (int u = tid; u < full; u += kThreads) {
-        const u32x4 w = scaled<T>(load16(g + u * 16), f);
-        store16(o + u * 16, w);
-      }
-      const int j = full * kN + tid;
-      if (j < n) store1(T{}, o + j * (int)sizeof(T), f * load1(T{}, g + j * (int)sizeof(T)));
+      next = chunk_of<T>(t, after);
+      ragged<kN>(k, [&](int u) { store16(o + u * 16, scaled<T>(load16(g + u * 16), f)); },
+                 [&](int e) {
+                   const int at = e * (int)sizeof(T);
+                   store1(T{}, o + at, f * load1(T{}, g + at));
+                 });
     }
   }
 }
@@ -212,8 +235,9 @@ template <typename T, class Tab>
 uint32_t fill(Tab& t, const GradSpan* spans, int count, bool out) {
   uint32_t chunks = 0;
   for (int i = 0; i < count; ++i) {
-    const int64_t n = (spans[i].n + kChunk<T> - 1) / kChunk<T>;
-    const int64_t tail = spans[i].n - (n - 1) * kChunk<T>;
+    const int64_t end = spans[i].n + (int64_t)((reinterpret_cast<uint64_t>(spans[i].g) & 15) / sizeof(T));
+    const int64_t n = (end + kChunk<T> - 1) / kChunk<T>;
+    const int64_t tail = end - (n - 1) * kChunk<T>;
     t.at[i] = (reinterpret_cast<uint64_t>(spans[i].g) << 16) | (uint64_t)(tail - 1);
     if (out) t.to[i] = reinterpret_cast<uint64_t>(spans[i].out);
     t.first[i] = chunks;

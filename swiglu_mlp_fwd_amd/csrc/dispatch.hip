@@ -49,7 +49,7 @@ __device__ __forceinline__ uint64_t same_key(int key, int bits) {
 // pos; with more than one block, hist holds all blocks' counts.
 template <bool kCount>
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p, int per_block) {
-  extern __shared__ int32_t cnt[];                        // [kPlanWaves][E + 1], then [E + 1] first rows
+  extern __shared__ int32_t cnt[];                        // [kPlanWaves][E + 1], then twice [E + 1]
   const int keys = p.E + 1;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int i = tid; i < kPlanWaves * keys; i += kPlanThreads) cnt[i] = 0;
@@ -64,9 +64,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p, int per_
     if (key >= 0) atomicAdd(mine + key, 1);               // LDS; only the sums are used
   }
   __syncthreads();
-  int32_t* start = cnt + kPlanWaves * keys;
-  // Per key: counts of earlier waves into each wave's place, the block's
-  // total into start.
+  int32_t* start = cnt + kPlanWaves * keys;               // the block's, then all counts of each key
+  int32_t* before = start + keys;                         // the earlier blocks' (more than one)
+  // Per key: counts of earlier waves into each wave's place.
   for (int e = tid; e < keys; e += kPlanThreads) {
     int sum = 0;
     for (int w = 0; w < kPlanWaves; ++w) {
@@ -74,19 +74,21 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p, int per_
       cnt[w * keys + e] = sum;
       sum += c;
     }
-    if constexpr (kCount) {
-      p.hist[(int64_t)blockIdx.x * keys + e] = sum;
-    } else if (gridDim.x > 1) {
-      int before = 0, all = 0;
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int c = p.hist[(int64_t)b * keys + e];
-        before += b < (int)blockIdx.x ? c : 0;
-        all += c;
+    if constexpr (kCount) p.hist[(int64_t)blockIdx.x * keys + e] = sum;
+    start[e] = gridDim.x > 1 ? 0 : sum;
+    before[e] = 0;
+  }
+  if (!kCount && gridDim.x > 1) {
+    // Every block's counts, all threads over the whole array at once (one key
+    // to a thread took 30 us for 128 blocks, a chain of loads).
+    __syncthreads();
+    const int n = (int)gridDim.x * keys, mine_from = (int)blockIdx.x * keys;
+    for (int i = tid; i < n; i += kPlanThreads) {
+      const int c = p.hist[i];
+      if (c != 0) {
+        atomicAdd(start + i % keys, c);
+        if (i < mine_from) atomicAdd(before + i % keys, c);
       }
-      start[e] = all;
-      for (int w = 0; w < kPlanWaves; ++w) cnt[w * keys + e] += before;
-    } else {
-      start[e] = sum;
     }
   }
   if constexpr (kCount) return;
@@ -119,7 +121,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p, int per_
     if (key >= 0) {
       const int rank = __popcll(same & ((uint64_t(1) << lane) - 1));
       const int at = mine[key];
-      const int row = start[key] + at + rank;
+      const int row = start[key] + before[key] + at + rank;
       p.src[row] = key < p.E ? (int)i : ~(int)i;
       p.pos[i] = key < p.E ? row : ~row;
       // The first of each key's lanes moves it on; the wave's LDS accesses
@@ -339,11 +341,11 @@ hipError_t combine_bwd_t(const CombineArgs& a, hipStream_t s) {
 hipError_t launch_plan(const PlanArgs& a, hipStream_t s) {
   const int blocks = plan_blocks(a.n);
   const int per_block = plan_per_block(a.n);
-  const size_t lds = (size_t)(kPlanWaves + 1) * (a.E + 1) * 4;
-  hipError_t e = allow_lds<&plan_kernel<false>>((size_t)(kPlanWaves + 1) * (SWIGLU_MAX_EXPERTS + 1) * 4);
+  const size_t lds = (size_t)(kPlanWaves + 2) * (a.E + 1) * 4;
+  hipError_t e = allow_lds<&plan_kernel<false>>((size_t)(kPlanWaves + 2) * (SWIGLU_MAX_EXPERTS + 1) * 4);
   if (e != hipSuccess) return e;
   if (blocks > 1) {
-    e = allow_lds<&plan_kernel<true>>((size_t)(kPlanWaves + 1) * (SWIGLU_MAX_EXPERTS + 1) * 4);
+    e = allow_lds<&plan_kernel<true>>((size_t)(kPlanWaves + 2) * (SWIGLU_MAX_EXPERTS + 1) * 4);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((plan_kernel<true>), dim3(blocks), dim3(kPlanThreads), lds, s, a, per_block);
     if ((e = hipGetLastError()) != hipSuccess) return e;

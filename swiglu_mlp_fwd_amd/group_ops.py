@@ -555,29 +555,29 @@ def _apart(t: torch.Tensor) -> bool:
     return True
 
 
-def _grad_list(grads) -> tuple[list, torch.device]:
-    if isinstance(grads, torch.Tensor):
-        grads = [grads]
-    grads = list(grads)
+def _grad_list(grads) -> list:
+    return [grads] if isinstance(grads, torch.Tensor) else list(grads)
+
+
+def _grad_codes(grads: list) -> tuple[array, torch.device]:
+    """The dtype codes of gradients on one device, and that device.  (Each pass over a list of hundreds of tensors
+    takes longer on the host than the kernels on the GPU, so there is one for each question.)"""
     if not grads:
         raise ValueError("no gradients were given")
-    kinds = set(map(attrgetter("dtype"), grads))
-    for d in kinds:
-        if d not in _DT:
-            raise TypeError(f"libswiglu supports bfloat16 and float32, got {d}")
-    devs = set(map(attrgetter("device"), grads))
-    if len(devs) > 1:
-        raise ValueError(f"gradients must be on one device, got {sorted(map(str, devs))}")
-    return grads, devs.pop()
-
-
-def _grad_args(grads: list):
-    """The host arrays of the C ABI; they must live until the call returns."""
     kinds = list(map(attrgetter("dtype"), grads))
-    codes = array("i", [_DT[d] for d in kinds])
-    at = array("Q", map(torch.Tensor.data_ptr, grads))
-    n = array("q", map(torch.Tensor.numel, grads))
-    return codes, at, n
+    if kinds.count(kinds[0]) == len(kinds):
+        codes = array("i", [_dtype_code(grads[0])]) * len(kinds)
+    else:
+        codes = array("i", map(_dtype_code, grads))
+    where = set(map(torch.Tensor.get_device, grads))
+    if len(where) > 1:
+        raise ValueError(f"gradients must be on one device, got {sorted({str(g.device) for g in grads})}")
+    return codes, grads[0].device
+
+
+def _grad_arrays(grads: list) -> tuple[array, array]:
+    """Addresses and sizes; host arrays that must live until the call returns."""
+    return array("Q", map(torch.Tensor.data_ptr, grads)), array("q", map(torch.Tensor.numel, grads))
 
 
 def _addr(a) -> int | None:
@@ -592,12 +592,13 @@ def grad_norm_workspace_bytes(count: int) -> int:
 def grad_norm(grads, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """The 2-norm of all elements of the tensors `grads` together (fp32 and bf16 mixed), a 0-dim fp32 tensor.  Squares
     are formed and added in fp64."""
-    grads, dev = _grad_list(grads)
+    grads = _grad_list(grads)
+    codes, dev = _grad_codes(grads)
     _check_workspace(workspace, dev)
     _on_gpu(grads[0])
     if not all(map(torch.Tensor.is_contiguous, grads)):
         grads = [t if t.is_contiguous() or _packed(t) else t.contiguous() for t in grads]
-    codes, at, n = _grad_args(grads)
+    at, n = _grad_arrays(grads)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     ws, size = _workspace(workspace, int(lib().swiglu_grad_norm_workspace_bytes(len(grads))), dev)
     _call("swiglu_grad_norm", norm, len(grads), _addr(codes), _addr(at), _addr(n), _p(norm), _p(ws), size)
@@ -613,11 +614,12 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, workspace: t
     overlap each other or be given twice.  A norm that is NaN makes every gradient NaN; an infinite one makes finite
     elements 0 and infinite ones NaN.  `workspace` may pass a uint8 device buffer of at least
     grad_norm_workspace_bytes(len(grads)) bytes (a smaller or missing one is replaced)."""
-    grads, dev = _grad_list(grads)
+    grads = _grad_list(grads)
+    codes, dev = _grad_codes(grads)
     max_norm, eps = float(max_norm), float(eps)
     to = None
     if out is not None:
-        to = [out] if isinstance(out, torch.Tensor) else list(out)
+        to = _grad_list(out)
         if len(to) != len(grads):
             raise ValueError(f"out must have {len(grads)} tensors, got {len(to)}")
         for i, (t, g) in enumerate(zip(to, grads)):
@@ -627,7 +629,7 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, workspace: t
     written = to if to is not None else grads
     _check_workspace(workspace, dev)
     back = []                                    # (tensor, its contiguous stand-in): copied back after the call
-    if not (all(map(torch.Tensor.is_contiguous, grads)) and all(map(torch.Tensor.is_contiguous, written))):
+    if not (all(map(torch.Tensor.is_contiguous, grads)) and (to is None or all(map(torch.Tensor.is_contiguous, to)))):
         for i, t in enumerate(written):
             if not _apart(t):
                 raise ValueError(f"{'out' if to is not None else 'grads'}[{i}] has elements that share memory, strides {t.stride()}")
@@ -641,13 +643,13 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, workspace: t
                 back.append((t, dst[i]))
         grads, written = src, dst
     _on_gpu(grads[0])
-    codes, at, n = _grad_args(grads)
+    at, n = _grad_arrays(grads)
     dst = None if to is None else array("Q", map(torch.Tensor.data_ptr, written))
     norm = torch.empty((), dtype=torch.float32, device=dev)
     ws, size = _workspace(workspace, int(lib().swiglu_grad_norm_workspace_bytes(len(grads))), dev)
     _call("swiglu_clip_grads", norm, len(grads), _addr(codes), _addr(at), _addr(n), _addr(dst), max_norm, eps, _p(norm),
           _p(ws), size)
     torch.autograd.graph.increment_version(written)
-    for t, c in back:
+    for t, c in back:                            # (copy_ counts for itself)
         t.copy_(c)
     return norm
