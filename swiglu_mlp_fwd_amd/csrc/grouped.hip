@@ -169,8 +169,8 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& p, int ntn, int bid
 // The ring of k-steps in LDS: 16-byte chunks of reduction to a k-step, and
 // k-steps.  bf16 NT: five short ones, taken in turns by the halves of the
 // workgroup.  Otherwise a double buffer.
-template <typename T, Form F> struct Ring {
-  static constexpr bool kTurns = sizeof(T) == 2 && F == Form::kNT;
+template <typename T, Form F, class TL> struct Ring {
+  static constexpr bool kTurns = sizeof(T) == 2 && F == Form::kNT && TL::kThreads == 512;
   static constexpr int kChunks = kTurns ? 4 : 8, kDepth = kTurns ? 5 : 2;
 };
 
@@ -192,7 +192,7 @@ void grouped_kernel(GroupedArgs p) {
   constexpr int kMN = kB16 ? 16 : 32;                     // MFMA tile
   constexpr int kBM = TL::kBM, kBN = TL::kBN, kThreads = TL::kThreads, kWaves = kThreads / 64;
   constexpr int kWM = TL::kWM, kWN = TL::kWN, kTM = kWM / kMN, kTN = kWN / kMN;
-  using R = Ring<T, F>;
+  using R = Ring<T, F, TL>;
   constexpr int KC = R::kChunks, S = R::kDepth, kRowBytes = KC * 16;
   constexpr int kPer = 16 / (int)sizeof(T);               // elements per chunk
   constexpr int kStep = KC * kPer;                        // reduction per k-step
@@ -733,7 +733,7 @@ hipError_t launch(const GroupedArgs& a, hipStream_t s) {
     tiles = (a.R / TL::kBM + groups) * ntn;
   }
   if (tiles == 0) return hipSuccess;
-  const size_t lds = (size_t)Ring<T, F>::kDepth * (TL::kBM + NB * TL::kBN) * Ring<T, F>::kChunks * 16;
+  const size_t lds = (size_t)Ring<T, F, TL>::kDepth * (TL::kBM + NB * TL::kBN) * Ring<T, F, TL>::kChunks * 16;
   const hipError_t attr = allow_lds<&grouped_kernel<T, F, O, ACT, NB, TL, kGroupM>>(lds);
   if (attr != hipSuccess) return attr;
   hipLaunchKernelGGL((grouped_kernel<T, F, O, ACT, NB, TL, kGroupM>), dim3((unsigned)tiles), dim3(TL::kThreads), lds,
@@ -743,36 +743,63 @@ hipError_t launch(const GroupedArgs& a, hipStream_t s) {
 
 using Dual = Tile<256, 128, 4, 2>;
 using Single = Tile<256, 256, 4, 2>;
+using DualFew = Tile<64, 128, 2, 2, 2>;
+using SingleFew = Tile<64, 256, 2, 2, 2>;
 using DualF32 = Tile<128, 64, 2, 2, 2>;
 using SingleF32 = Tile<128, 128, 2, 2, 2>;
+using DualF32Few = Tile<32, 64, 1, 2, 2>;
+using SingleF32Few = Tile<32, 64, 1, 2, 2>;
+
+// Row tiles of at most `bm` rows, times column tiles of `bn`.
+int64_t tiles_of(const GroupedArgs& a, int bm, int bn) {
+  const int64_t groups = a.E < a.R ? a.E : a.R;
+  return (a.R / bm + groups) * (((int64_t)a.n + bn - 1) / bn);
+}
+// bf16: small tiles where the large ones would leave many of the 256 CUs
+// without a workgroup, and up to 16 rows per expert.  The down product of 16
+// experts of (512, 512): 512 rows 17 us with large tiles, 11 with small; 8 x
+// (4096, 2048) with 64 rows each 50 and 42, with 256 (256 large tiles) 56 and
+// 79; dx of 64 x (1024, 2048) with 16 rows each 63 and 51, with 32 66 and 70.
+bool few_bf16(const GroupedArgs& a, int bn) { return a.R <= (int64_t)16 * a.E || tiles_of(a, 256, bn) <= 176; }
+// fp32, whose tiles are bound by the matrix cores: tiles of 32 rows up to 128
+// rows per expert, and where the large ones are fewer than the CUs.  64
+// experts of (1024, 2048), gate/up: 16 rows each 484 us with large tiles, 208
+// with small, 128 862 and 701, 512 2222 and 2316; 5 of (200, 264): 23 and 14.
+bool few_f32(const GroupedArgs& a, int bn) { return a.R <= (int64_t)128 * a.E || tiles_of(a, 128, bn) <= 256; }
+
+template <Out O, Act A>
+hipError_t dual(Dt dt, const GroupedArgs& a, hipStream_t s) {
+  if (dt == Dt::kF32)
+    return few_f32(a, DualF32::kBN) ? launch<float, Form::kNT, O, A, 2, DualF32Few>(a, s)
+                       : launch<float, Form::kNT, O, A, 2, DualF32>(a, s);
+  // (The small tile's ring has no room for the recompute's dh tile.)
+  if constexpr (O == Out::kGated)
+    if (few_bf16(a, Dual::kBN)) return launch<bf16, Form::kNT, O, A, 2, DualFew>(a, s);
+  return launch<bf16, Form::kNT, O, A, 2, Dual>(a, s);
+}
+
+template <Form F>
+hipError_t single(Dt dt, const GroupedArgs& a, hipStream_t s) {
+  if (dt == Dt::kF32)
+    return few_f32(a, SingleF32::kBN) ? launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32Few>(a, s)
+                       : launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32>(a, s);
+  return few_bf16(a, Single::kBN) ? launch<bf16, F, Out::kStore, Act::kSilu, 1, SingleFew, 4>(a, s)
+                           : launch<bf16, F, Out::kStore, Act::kSilu, 1, Single, 4>(a, s);
+}
 
 }  // namespace
 
 hipError_t launch_grouped_gated(Dt dt, Act act, const GroupedArgs& a, hipStream_t s) {
-  if (act == Act::kGeluTanh)
-    return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kGated, Act::kGeluTanh, 2, Dual>(a, s)
-                           : launch<float, Form::kNT, Out::kGated, Act::kGeluTanh, 2, DualF32>(a, s);
-  return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kGated, Act::kSilu, 2, Dual>(a, s)
-                         : launch<float, Form::kNT, Out::kGated, Act::kSilu, 2, DualF32>(a, s);
+  return act == Act::kGeluTanh ? dual<Out::kGated, Act::kGeluTanh>(dt, a, s) : dual<Out::kGated, Act::kSilu>(dt, a, s);
 }
 
 hipError_t launch_grouped_dgated(Dt dt, Act act, const GroupedArgs& a, hipStream_t s) {
-  if (act == Act::kGeluTanh)
-    return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kDGated, Act::kGeluTanh, 2, Dual>(a, s)
-                           : launch<float, Form::kNT, Out::kDGated, Act::kGeluTanh, 2, DualF32>(a, s);
-  return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kDGated, Act::kSilu, 2, Dual>(a, s)
-                         : launch<float, Form::kNT, Out::kDGated, Act::kSilu, 2, DualF32>(a, s);
+  return act == Act::kGeluTanh ? dual<Out::kDGated, Act::kGeluTanh>(dt, a, s) : dual<Out::kDGated, Act::kSilu>(dt, a, s);
 }
 
-hipError_t launch_grouped_nt(Dt dt, const GroupedArgs& a, hipStream_t s) {
-  return dt == Dt::kBF16 ? launch<bf16, Form::kNT, Out::kStore, Act::kSilu, 1, Single, 4>(a, s)
-                         : launch<float, Form::kNT, Out::kStore, Act::kSilu, 1, SingleF32, 8>(a, s);
-}
+hipError_t launch_grouped_nt(Dt dt, const GroupedArgs& a, hipStream_t s) { return single<Form::kNT>(dt, a, s); }
 
-hipError_t launch_grouped_nn(Dt dt, const GroupedArgs& a, hipStream_t s) {
-  return dt == Dt::kBF16 ? launch<bf16, Form::kNN, Out::kStore, Act::kSilu, 1, Single, 4>(a, s)
-                         : launch<float, Form::kNN, Out::kStore, Act::kSilu, 1, SingleF32, 8>(a, s);
-}
+hipError_t launch_grouped_nn(Dt dt, const GroupedArgs& a, hipStream_t s) { return single<Form::kNN>(dt, a, s); }
 
 hipError_t launch_grouped_tn(Dt dt, const GroupedArgs& a, hipStream_t s) {
   return dt == Dt::kBF16 ? launch<bf16, Form::kTN, Out::kStore, Act::kSilu, 1, Single, 4>(a, s)

@@ -213,8 +213,43 @@ def test_grouped_gate_up(name, N, K, dt, act):
         within(g.t, v, b, f"{what} {part}")
 
 
+def many_tiles(dt):
+    """Rows, and a width, whose tiles are more than the CUs, where the launches take their large tiles: many small ragged
+    experts (bf16), few large ones (fp32)."""
+    g = np.random.default_rng(3)
+    counts = list(g.integers(0, 90, size=40)) if dt == "bf16" else [700, 0, 301, 900]
+    counts[1] = 300 if dt == "bf16" else 0
+    return counts, offsets_of(counts, 2), 2 + int(sum(counts)) + 3
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("T,k,E,N,K", [(1, 1, 1, 8, 8), (97, 2, 5, 200, 264), (300, 4, 12, 136, 520), (40, 8, 64, 72, 264)])
+@pytest.mark.parametrize("wide_first", [True, False])
+def test_many_tiles(dt, wide_first):
+    """N wide: the products of rows take many tiles; K wide: their gradients."""
+    counts, offsets, R = many_tiles(dt)
+    E, wide, narrow = len(counts), 2312, 136
+    N, K = (wide, narrow) if wide_first else (narrow, wide)
+    x, xc = poisoned(normal((R, K), 1, dt), offsets)
+    dy, dyc = poisoned(normal((R, N), 2, dt), offsets)
+    wg, wu = normal((E, N, K), 3, dt, K ** -0.5), normal((E, N, K), 4, dt, K ** -0.5)
+    o = offsets.cpu().numpy()
+    hx, hdy, hg, hu = host(xc), host(dyc), host(wg), host(wu)
+    out = [guarded(s, DT[dt]) for s in ((R, N), (R, K), (E, N, K), (R, N), (R, K), (E, N, K), (E, N, K))]
+    S.grouped_mm(x, wg, offsets, out=out[0].t)
+    S.grouped_mm_bwd(x, wg, dy, offsets, out=(out[1].t, out[2].t))
+    S.grouped_fwd(x, wg, wu, offsets, out=out[3].t)
+    S.grouped_bwd(x, wg, wu, dy, offsets, out=tuple(g.t for g in out[4:]),
+                  workspace=workspace(S.grouped_bwd_workspace_bytes(DT[dt], R, N, K)))
+    check_guards("many tiles", *out)
+    want = [G.mm(hx, hg, o, ROUND[dt]), *G.mm_bwd(hx, hg, hdy, o, ROUND[dt]), G.gate_up(hx, hg, hu, o, "silu", ROUND[dt]),
+            *G.gate_up_bwd(hx, hg, hu, hdy, o, "silu", ROUND[dt])]
+    for g, (v, b), name in zip(out, want, ("y", "dx", "dw", "h", "dx gate/up", "dwg", "dwu")):
+        within(g.t, v, b, f"many tiles {dt} {N}x{K} {name}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,k,E,N,K", [(1, 1, 1, 8, 8), (97, 2, 5, 200, 264), (300, 4, 12, 136, 520), (40, 8, 64, 72, 264),
+                                       (1300, 2, 40, 1040, 136)])
 def test_gathered_rows_give_what_rows_give(T, k, E, N, K, dt):
     """With src the same bits as on rows gathered before."""
     g = np.random.default_rng(T)
@@ -396,7 +431,7 @@ def test_a_training_step_replays_in_a_graph(dt):
         y = S.routed_mlp(x, wg, wu, wd, ids, w)
         grads = torch.autograd.grad((y.float() * dy.float()).sum(), leaves)
         norm = S.clip_grads(grads, 0.5)
-        return (y, norm, *grads)
+        return (y.detach(), norm, *grads)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
