@@ -2,10 +2,10 @@
 
     python examples/routed_block.py
 
-train() fits one block to a synthetic target: the norms around it (block_norms), the router (router) and, expert by
-expert, the fused gate/up stage (swiglu), all with their HIP backward passes.  decode() runs a stack of blocks on a
-few tokens a step: route, moe_fwd, and one block_norm between blocks that joins the block's output to the residual
-stream and forms the next block's input.
+train() fits one block to a synthetic target: the norms around it (block_norms), the router (router) and the experts'
+MLPs over all tokens at once (routed_mlp), all with their HIP backward passes, then the clipping of all gradients
+together (clip_grads).  decode() runs a stack of blocks on a few tokens a step: route, moe_fwd, and one block_norm
+between blocks that joins the block's output to the residual stream and forms the next block's input.
 """
 import os
 import sys
@@ -27,25 +27,21 @@ def train(steps=40, tokens=512, width=256, hidden=384, experts=8, topk=2, lr=3e-
         return (torch.randn(shape, generator=g, device=DEV) * std + mean).requires_grad_(True)
     w_in, w_out, gate = param(width, mean=1.0), param(width, mean=1.0), param(width, mean=1.0)
     wr = param(width, experts)
-    wg = [param(hidden, width) for _ in range(experts)]
-    wu = [param(hidden, width) for _ in range(experts)]
-    wd = [param(width, hidden) for _ in range(experts)]
-    opt = torch.optim.Adam([w_in, w_out, gate, wr, *wg, *wu, *wd], lr=lr)
+    wg, wu, wd = param(experts, hidden, width), param(experts, hidden, width), param(experts, width, hidden)
+    params = [w_in, w_out, gate, wr, wg, wu, wd]
+    opt = torch.optim.Adam(params, lr=lr)
     x = torch.randn((tokens, width), generator=g, device=DEV)
     target = x + torch.sin(x @ (torch.randn((width, width), generator=g, device=DEV) / width ** 0.5))
     losses = []
     for _ in range(steps):
         _, z = S.block_norms(x, w_in=w_in)
         w, ids = S.router(z @ wr, topk)
-        y = torch.zeros_like(x)
-        for e in range(experts):
-            t, j = torch.nonzero(ids == e, as_tuple=True)
-            h = S.swiglu(z[t], wg[e], wu[e])
-            y = y.index_add(0, t, w[t, j].unsqueeze(1) * (h @ wd[e].t()))
+        y = S.routed_mlp(z, wg, wu, wd, ids, w)
         out, _ = S.block_norms(x, y, w_out, gate)
         loss = (out - target).square().mean()
         opt.zero_grad()
         loss.backward()
+        S.clip_grads([p.grad for p in params], max_norm=1.0)
         opt.step()
         losses.append(loss.item())
     return losses[0], losses[-1]
