@@ -539,7 +539,8 @@ size_t swiglu_expert_plan_workspace_bytes(int64_t T, int64_t k, int64_t E);
  *
  *   ids          [T, k] int32, as swiglu_route_fwd gives them
  *   workspace    swiglu_expert_plan_workspace_bytes(T, k, E) bytes, 256-byte
- *                aligned (NULL where none is needed); scratch
+ *                aligned (NULL where none is needed); scratch (calls that
+ *                overlap need one each)
  * 1 <= E <= SWIGLU_MAX_EXPERTS, 1 <= k <= SWIGLU_MAX_TOPK, T * k < 2^31, else
  * SWIGLU_ERR_SHAPE.  int32 arrays need 4-byte alignment. */
 int swiglu_expert_plan(int64_t T, int64_t k, int64_t E, const int32_t* ids, int32_t* offsets, int32_t* src,
@@ -603,13 +604,13 @@ size_t swiglu_grouped_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, int64
  *   dx[r]  = dg[r] Wg_e + du[r] Wu_e     of the rows, also with src: the
  *            tokens' gradients are swiglu_expert_combine of dx without weights
  *   dwg[e] = sum over the expert's rows of dg[r]^T x_r,  dwu[e] of du[r]
- * Rows of no expert have dx = 0 and are not read; experts without rows get
- * dwg = dwu = 0.
+ * Rows of no expert have dx = 0 and their dh is not read; experts without rows
+ * get dwg = dwu = 0.
  *
  *   dh           [R, N];  dx [R, K], or NULL if it is not wanted
  *   dwg, dwu     [E, N, K] dense outputs, or both NULL
  *   workspace    at least swiglu_grouped_bwd_workspace_bytes(...) bytes,
- *                256-byte aligned; scratch
+ *                256-byte aligned; scratch (calls that overlap need one each)
  * Errors as the forward's; one of dwg, dwu alone: SWIGLU_ERR_ARG. */
 int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
                        int64_t k, const int32_t* src, const int32_t* offsets, const void* wg, int64_t wg_stride,
@@ -644,7 +645,7 @@ size_t swiglu_grad_norm_workspace_bytes(int64_t count);
  *                and the elements of each dense tensor
  *   norm         one float on the device
  *   workspace    swiglu_grad_norm_workspace_bytes(count) bytes, 256-byte
- *                aligned; scratch
+ *                aligned; scratch (calls that overlap need one each)
  * count <= 2^20, else SWIGLU_ERR_SHAPE; sizes <= 2^35 each, else
  * SWIGLU_ERR_UNSUPPORTED.  The host arrays are read before the call returns. */
 int swiglu_grad_norm(int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes, float* norm,

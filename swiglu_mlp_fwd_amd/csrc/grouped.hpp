@@ -77,8 +77,4 @@ struct ClipArgs {
 };
 hipError_t launch_clip(const ClipArgs& a, hipStream_t s);
 
-// Whether rows of A can be gathered on the way: their byte offsets from x are
-// 32-bit, and the offset 2^31 reads as zero.
-inline bool gather_fits(int elem, int64_t T, int64_t K) { return T * K * elem < (int64_t(1) << 31); }
-
 }  // namespace swg

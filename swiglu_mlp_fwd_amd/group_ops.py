@@ -10,7 +10,6 @@ stream of the tensors' device.
 """
 from __future__ import annotations
 
-import contextlib
 import math
 from array import array
 from operator import attrgetter
@@ -22,16 +21,16 @@ from ._lib import MAX_EXPERTS, MAX_TOPK, check, lib
 from .block_ops import _expert_weights, _lead, _stream
 from .ops import _DT, _act_code, _check_out, _dtype_code, _on_gpu, _p, _same
 
-_NO_GUARD = contextlib.nullcontext()
 GATHER_BYTES = 1 << 31    # tokens of as many bytes are gathered before the products: row offsets are 32-bit there
 
 
 def _call(name: str, like: torch.Tensor, *args) -> None:
     """The library's `name` on the current stream of the tensor's device, with that device current."""
-    dev = like.device
-    other = dev.index is not None and dev.index != torch.cuda.current_device()
-    with torch.cuda.device(dev) if other else _NO_GUARD:
+    if like.get_device() == torch.cuda.current_device():
         check(name, getattr(lib(), name)(*args, _stream(like)))
+    else:
+        with torch.cuda.device(like.device):
+            check(name, getattr(lib(), name)(*args, _stream(like)))
 
 
 def _dense16(t: torch.Tensor) -> torch.Tensor:
@@ -649,7 +648,10 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, workspace: t
     ws, size = _workspace(workspace, int(lib().swiglu_grad_norm_workspace_bytes(len(grads))), dev)
     _call("swiglu_clip_grads", norm, len(grads), _addr(codes), _addr(at), _addr(n), _addr(dst), max_norm, eps, _p(norm),
           _p(ws), size)
-    torch.autograd.graph.increment_version(written)
-    for t, c in back:                            # (copy_ counts for itself)
+    for t, c in back:
         t.copy_(c)
+    try:
+        torch.autograd.graph.increment_version(written)
+    except RuntimeError:                         # tensors made in inference mode count no versions
+        torch.autograd.graph.increment_version([t for t in written if not t.is_inference()])
     return norm

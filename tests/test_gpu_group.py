@@ -248,6 +248,58 @@ def test_many_tiles(dt, wide_first):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_hundreds_of_experts(dt):
+    """More groups than a wave has lanes: the scan over them takes several turns."""
+    g = np.random.default_rng(9)
+    counts = list(g.integers(0, 4, size=1024))
+    counts[700] = 90
+    offsets, R, N, K = offsets_of(counts, 1), 1 + int(sum(counts)) + 2, 24, 40
+    x, xc = poisoned(normal((R, K), 1, dt), offsets)
+    dy, dyc = poisoned(normal((R, N), 2, dt), offsets)
+    w, o = normal((1024, N, K), 3, dt, K ** -0.5), offsets.cpu().numpy()
+    within(S.grouped_mm(x, w, offsets), *G.mm(host(xc), host(w), o, ROUND[dt]), f"1024 experts {dt} y")
+    got = S.grouped_mm_bwd(x, w, dy, offsets)
+    for t, want, name in zip(got, G.mm_bwd(host(xc), host(w), host(dyc), o, ROUND[dt]), ("dx", "dw")):
+        within(t, *want, f"1024 experts {dt} {name}")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_offsets_that_decrease_stay_inside(dt):
+    """Offsets no plan gives (decreasing, negative, past the rows): nothing outside the outputs is touched, and the
+    following call is as ever."""
+    R, E, N, K = 300, 4, 72, 136
+    x, w, dy = normal((R, K), 1, dt), normal((E, N, K), 2, dt), normal((R, N), 3, dt)
+    for bad in ([0, 200, 100, 400, 300], [300, 0, 300, 0, 300], [-5, -1, 0, 1 << 30, 10], [(1 << 31) - 1] * 5):
+        o = ints(bad)
+        out = [guarded(s, DT[dt]) for s in ((R, N), (R, K), (E, N, K), (R, N), (R, K), (E, N, K), (E, N, K))]
+        S.grouped_mm(x, w, o, out=out[0].t)
+        S.grouped_mm_bwd(x, w, dy, o, out=(out[1].t, out[2].t))
+        S.grouped_fwd(x, w, w, o, out=out[3].t)
+        S.grouped_bwd(x, w, w, dy, o, out=tuple(g.t for g in out[4:]))
+        check_guards(f"offsets {bad}", *out)
+    good = offsets_of([100, 0, 150, 50])
+    within(S.grouped_mm(x, w, good), *G.mm(host(x), host(w), good.cpu().numpy(), ROUND[dt]), "after bad offsets")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_indices_no_plan_gives(dt):
+    """src and pos that name no pair or row: zero rows, and terms that are left out."""
+    T, k, K = 6, 2, 24
+    x, rows = normal((T, K), 1, dt), normal((T * k, K), 2, dt)
+    src = ints([0, 11, 12, -1, (1 << 31) - 1, -(1 << 31), 5, 3, 3, 100, 1, 2])
+    want = torch.stack([x[p // k] if 0 <= p < T * k else torch.zeros_like(x[0]) for p in src.tolist()])
+    assert torch.equal(S.expert_gather(x, src), want)
+    w = torch.zeros((1, 8, K), dtype=DT[dt], device=DEV) + 1
+    o = offsets_of([T * k])
+    assert torch.equal(S.grouped_fwd(x, w, w, o, src=src), S.grouped_fwd(want, w, w, o))
+    pos = ints([[0, 12], [1, -1], [(1 << 31) - 1, 2], [-(1 << 31), 3], [4, 4], [5, 100]])
+    y = S.expert_combine(rows, pos)
+    for t, p in enumerate(pos.tolist()):
+        live = [rows[r].float() for r in p if 0 <= r < T * k]
+        assert torch.equal(y[t], sum(live, torch.zeros(K, device=DEV)).to(DT[dt])), t
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("T,k,E,N,K", [(1, 1, 1, 8, 8), (97, 2, 5, 200, 264), (300, 4, 12, 136, 520), (40, 8, 64, 72, 264),
                                        (1300, 2, 40, 1040, 136)])
 def test_gathered_rows_give_what_rows_give(T, k, E, N, K, dt):
@@ -559,6 +611,13 @@ def test_clip_of_strided_gradients():
     S.clip_grads([g], 1.0, out=[out])
     n, f = G.clip([host(g)], 1.0)
     within(out, f * host(g), 3 * U32 * np.abs(host(g)), "into a transposed tensor")
+
+
+def test_clip_of_inference_tensors():
+    with torch.inference_mode():
+        g = [torch.full((3,), 2.0, device=DEV), torch.zeros(2, device=DEV)]
+        S.clip_grads(g, 1.0, eps=0.0)
+    assert torch.allclose(g[0], torch.full((3,), 2 / math.sqrt(12), device=DEV) )
 
 
 def test_clip_is_seen_by_autograd():
