@@ -167,11 +167,13 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& p, int ntn, int bid
 // --------------------------------------------------------------- the kernel
 
 // The ring of k-steps in LDS: 16-byte chunks of reduction to a k-step, and
-// k-steps.  bf16 NT: five short ones, taken in turns by the halves of the
-// workgroup.  Otherwise a double buffer.
+// k-steps.  bf16 NT: five short ones (tiles of 64 rows, two workgroups to a CU:
+// three of full length), taken in turns by the halves of the workgroup.
+// Otherwise a double buffer.
 template <typename T, Form F, class TL> struct Ring {
   static constexpr bool kTurns = sizeof(T) == 2 && F == Form::kNT && TL::kThreads == 512;
-  static constexpr int kChunks = kTurns ? 4 : 8, kDepth = kTurns ? 5 : 2;
+  static constexpr bool kShort = kTurns && TL::kBM > 64;
+  static constexpr int kChunks = kShort ? 4 : 8, kDepth = !kTurns ? 2 : kShort ? 5 : 3;
 };
 
 // dh tile in LDS: row r at r * 2 BN bytes, its 16-byte chunk c at physical
@@ -353,10 +355,18 @@ void grouped_kernel(GroupedArgs p) {
     const int64_t left = all - s * step;
     return left < 0 ? 0 : (left < step ? left : step);
   };
+  // Where rows are few, all workgroups stream weights at once.  Those of a
+  // column tile start where its number says, and go round: from the same place
+  // in all rows, at a power-of-two distance from each other, they would keep
+  // asking a few of the memory's channels.  (The order depends on nothing but
+  // the expert and the column tile, so a row's result does not depend on the
+  // other rows.)
+  const int first = F == Form::kNT && p.stagger && nk > 0 ? (e * ntn + tn) % nk : 0;
   // Instruction q of this wave's kDma for k-step ks, into a slot: A's first.
   auto issue_one = [&](int ks, int slot, int q) {
     const int h = F == Form::kNN && ks >= nkh ? 1 : 0;
-    const int s = ks - h * nkh;
+    int s = ks - h * nkh;
+    if constexpr (F == Form::kNT) s = s + first < nk ? s + first : s + first - nk;
     const int rem = (red + kPer - 1) / kPer - s * KC;     // chunks of reduction left (contiguous)
     const bool past = ks >= nk;
     char* dst = lds_bytes + slot * kStageBytes + wave * 1024;
@@ -500,7 +510,15 @@ void grouped_kernel(GroupedArgs p) {
     // instruction at a time between the products.  Every k-step of the ring is
     // requested, also those behind the last, which read nothing (or the dh
     // tile), so that the count of loads in flight says which have landed.
-    static_assert(kWaves == 8 && KC == kCPS, "two waves to a SIMD, a sub-step to a k-step");
+    static_assert(kWaves == 8 && kKK <= 2, "two waves to a SIMD, fragments of a whole k-step in registers");
+    auto read = [&](const char* L) {
+#pragma unroll
+      for (int kk = 0; kk < kKK; ++kk) read_frags(kk, L, kk);
+    };
+    auto multiply = [&](int from, int to) {
+#pragma unroll
+      for (int kk = 0; kk < kKK; ++kk) mfmas(kk, from - kk * kMf, to - kk * kMf);
+    };
     auto request = [&](int ks, int slot, int q) {
       if (kDh && (ks == nk || ks == nk + 1)) issue_dh(ks - nk, slot, q);
       else issue_one(ks, slot, q);
@@ -516,7 +534,7 @@ void grouped_kernel(GroupedArgs p) {
         __builtin_amdgcn_sched_barrier(0);
         request(it + S - 1, next, q);
         __builtin_amdgcn_sched_barrier(0);
-        mfmas(0, q * (kMf / kDma), (q + 1) * (kMf / kDma));
+        multiply(q * kKK * kMf / kDma, (q + 1) * kKK * kMf / kDma);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -540,7 +558,7 @@ void grouped_kernel(GroupedArgs p) {
     } else if (wave < 4) {
       for (int it = 0; it < nk; ++it) {
         turn();
-        read_frags(0, lds_bytes + slot * kStageBytes, 0);
+        read(lds_bytes + slot * kStageBytes);
         products(it);
         advance();
       }
@@ -548,18 +566,18 @@ void grouped_kernel(GroupedArgs p) {
     } else {
       turn();
       if (nk > 0) {
-        read_frags(0, lds_bytes, 0);
+        read(lds_bytes);
 #pragma unroll
         for (int q = 0; q < kDma; ++q) request(S - 1, next, q);
         advance();
         for (int it = 1; it < nk; ++it) {
           turn();
           products(it);
-          read_frags(0, lds_bytes + slot * kStageBytes, 0);
+          read(lds_bytes + slot * kStageBytes);
           advance();
         }
         turn();
-        mfmas(0, 0, kMf);
+        multiply(0, kKK * kMf);
       }
     }
   } else {
@@ -743,7 +761,8 @@ hipError_t launch(const GroupedArgs& a, hipStream_t s) {
 
 using Dual = Tile<256, 128, 4, 2>;
 using Single = Tile<256, 256, 4, 2>;
-using DualFew = Tile<64, 128, 2, 2, 2>;
+using DualFew = Tile<64, 64, 4, 2, 4>;
+using SingleFewNT = Tile<64, 128, 4, 2, 4>;
 using SingleFew = Tile<64, 256, 2, 2, 2>;
 using DualF32 = Tile<128, 64, 2, 2, 2>;
 using SingleF32 = Tile<128, 128, 2, 2, 2>;
@@ -756,11 +775,28 @@ int64_t tiles_of(const GroupedArgs& a, int bm, int bn) {
   return (a.R / bm + groups) * (((int64_t)a.n + bn - 1) / bn);
 }
 // bf16: small tiles where the large ones would leave many of the 256 CUs
-// without a workgroup, and up to 16 rows per expert.  The down product of 16
-// experts of (512, 512): 512 rows 17 us with large tiles, 11 with small; 8 x
-// (4096, 2048) with 64 rows each 50 and 42, with 256 (256 large tiles) 56 and
-// 79; dx of 64 x (1024, 2048) with 16 rows each 63 and 51, with 32 66 and 70.
-bool few_bf16(const GroupedArgs& a, int bn) { return a.R <= (int64_t)16 * a.E || tiles_of(a, 256, bn) <= 176; }
+// without a workgroup, and up to so many rows per expert (rows drawn with a
+// spread of a half, logarithmic):
+// gate/up 64, of 64 x (1024, 2048) with 32 rows each 115 us with large tiles,
+// 104 with small, with 64 152 and 112, with 128 160 and 161; of 8 x (14336, 4096)
+// with 32 365 and 328, with 64 410 and 376, with 96 406 and 471;
+// the down product 32, of 64 x (2048, 1024) with 16 rows each 57 and 52, with 32
+// 59 and 59; of 8 x (6912, 1536) 40 and 36, 43 and 36, with 64 43 and 47; of
+// 8 x (4096, 2048) with 64 (160 large tiles) 51 and 33, with 128 53 and 45;
+// dx 16, of 64 x (1024, 2048) with 16 rows each 63 and 51, with 32 66 and 70.
+// (One workgroup to a CU, twice the columns and a ring of four took as long
+// for the same number of tiles but more where a last round is nearly empty:
+// 114 for the first of these.)
+bool few_bf16(const GroupedArgs& a, int bn, int rows) {
+  return a.R <= (int64_t)rows * a.E || tiles_of(a, 256, bn) <= 176;
+}
+// Column tiles start apart up to 256 rows per expert, where the weights' stream
+// bounds the product.  64 x (1024, 2048) with 32 rows each, gate/up 123 us from
+// the same place, 95 apart, with 128 146 and 136; 8 x (14336, 4096) with 128 470
+// and 446; fp32, 16 x (4096, 1024) with 16 160 and 128, from 32 on the same.
+// With 512 it costs as much (bf16, 8 x (4096, 2048): 167 and 168) or more, since
+// column tiles share rows of x.
+bool weights_bound(const GroupedArgs& a) { return a.R <= (int64_t)256 * a.E; }
 // fp32, whose tiles are bound by the matrix cores: tiles of 32 rows up to 128
 // rows per expert, and where the large ones are fewer than the CUs.  64
 // experts of (1024, 2048), gate/up: 16 rows each 484 us with large tiles, 208
@@ -768,23 +804,26 @@ bool few_bf16(const GroupedArgs& a, int bn) { return a.R <= (int64_t)16 * a.E ||
 bool few_f32(const GroupedArgs& a, int bn) { return a.R <= (int64_t)128 * a.E || tiles_of(a, 128, bn) <= 256; }
 
 template <Out O, Act A>
-hipError_t dual(Dt dt, const GroupedArgs& a, hipStream_t s) {
+hipError_t dual(Dt dt, GroupedArgs a, hipStream_t s) {
+  a.stagger = weights_bound(a);
   if (dt == Dt::kF32)
     return few_f32(a, DualF32::kBN) ? launch<float, Form::kNT, O, A, 2, DualF32Few>(a, s)
-                       : launch<float, Form::kNT, O, A, 2, DualF32>(a, s);
+                                    : launch<float, Form::kNT, O, A, 2, DualF32>(a, s);
   // (The small tile's ring has no room for the recompute's dh tile.)
   if constexpr (O == Out::kGated)
-    if (few_bf16(a, Dual::kBN)) return launch<bf16, Form::kNT, O, A, 2, DualFew>(a, s);
+    if (few_bf16(a, Dual::kBN, 64)) return launch<bf16, Form::kNT, O, A, 2, DualFew>(a, s);
   return launch<bf16, Form::kNT, O, A, 2, Dual>(a, s);
 }
 
 template <Form F>
-hipError_t single(Dt dt, const GroupedArgs& a, hipStream_t s) {
+hipError_t single(Dt dt, GroupedArgs a, hipStream_t s) {
+  a.stagger = F == Form::kNT && weights_bound(a);
+  using Few = std::conditional_t<F == Form::kNT, SingleFewNT, SingleFew>;
   if (dt == Dt::kF32)
     return few_f32(a, SingleF32::kBN) ? launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32Few>(a, s)
-                       : launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32>(a, s);
-  return few_bf16(a, Single::kBN) ? launch<bf16, F, Out::kStore, Act::kSilu, 1, SingleFew, 4>(a, s)
-                           : launch<bf16, F, Out::kStore, Act::kSilu, 1, Single, 4>(a, s);
+                                      : launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32>(a, s);
+  return few_bf16(a, Single::kBN, F == Form::kNT ? 32 : 16) ? launch<bf16, F, Out::kStore, Act::kSilu, 1, Few, 4>(a, s)
+                                                            : launch<bf16, F, Out::kStore, Act::kSilu, 1, Single, 4>(a, s);
 }
 
 }  // namespace

@@ -24,6 +24,7 @@ struct GroupedArgs {
   int64_t ldb;
   int64_t b0_stride, b1_stride;   // elements between experts
   int m, n, r;              // TN: m rows of a half; columns; reduction length of a half (NT, NN)
+  bool stagger;             // NT: column tiles start at different places of the reduction
   int halves;               // NN: halves of the reduction, TN: of the rows (1 or 2)
   void *out0, *out1;        // TN: the two halves' outputs
   int64_t ldo;
