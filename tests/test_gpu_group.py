@@ -613,6 +613,22 @@ def test_clip_of_strided_gradients():
     within(out, f * host(g), 3 * U32 * np.abs(host(g)), "into a transposed tensor")
 
 
+@pytest.mark.parametrize("dt,n", [("bf16", 97_000_003), ("f32", 48_000_001)])
+def test_clip_of_many_bytes_into_out(dt, n):
+    """Results past the caches, chunks that start and end inside their tensors' 16 bytes."""
+    flat = normal((n,), 3, dt)
+    g = [flat[:11], flat[11:n // 2], flat[n // 2:n - 5], flat[n - 5:]]
+    keep, res = flat.clone(), torch.full((n + 8,), 7.0, dtype=DT[dt], device=DEV)
+    out = [res[4:15], res[15:4 + n // 2], res[4 + n // 2:n - 1], res[n - 1:n + 4]]
+    norm = S.clip_grads(g, 2.5, out=out)
+    want = math.sqrt(sum(c.double().square().sum().item() for c in flat.split(1 << 24)))
+    assert abs(norm.item() - want) <= 2 ** -23 * want
+    for a, b in zip(flat.split(1 << 24), res[4:n + 4].split(1 << 24)):
+        e = a.double() * (2.5 / (want + 1e-6))
+        assert ((b.double() - e).abs() <= e.abs() * (torch.finfo(DT[dt]).eps / 2 + 2 ** -22)).all()
+    assert torch.equal(flat, keep) and (res[:4] == 7).all() and (res[n + 4:] == 7).all()
+
+
 def test_clip_of_inference_tensors():
     with torch.inference_mode():
         g = [torch.full((3,), 2.0, device=DEV), torch.zeros(2, device=DEV)]
