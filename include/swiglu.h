@@ -587,7 +587,7 @@ int swiglu_expert_combine_bwd(int dtype, int64_t T, int64_t k, int64_t K, const 
  *   h            [R, N] (output)
  * Layout rules: N and K whole 16-byte chunks (% 8 bf16, % 4 fp32), strides too
  * and at least N * K (E > 1), else SWIGLU_ERR_SHAPE; 1 <= E <=
- * SWIGLU_MAX_EXPERTS; 2 N and K below 2^22, and (R / 128 + E + 2) *
+ * SWIGLU_MAX_EXPERTS; 2 N and K at most 2^22 - 64, and (R / 128 + E + 2) *
  * ceil(max(N, K) / 64) and 2 E ceil(N / 128) ceil(K / 128) below 2^23, else
  * SWIGLU_ERR_UNSUPPORTED; so is src with x of 2^31 bytes or more (gather the
  * rows first). */

@@ -26,10 +26,24 @@
 // tile, waves whose rows all lie behind its end load their share of the
 // operands and skip the products, so the others have the matrix cores.
 //
-// The main loop is that of the ungrouped products (gemm.hip): a ring of two
-// k-steps in LDS filled by 16-byte LDS DMA, fragments double-buffered in
-// registers, one barrier per k-step.  Every wave moves a share of every
-// operand.
+// The main loops: operands come by 16-byte LDS DMA, a wave moving a share of
+// each.  bf16 NT runs in turns (a ring of k-steps, the halves of the workgroup
+// half a k-step apart); the forms with transposing reads and fp32 have a double
+// buffer of k-steps and of fragments.  (The compiler lets every transposing
+// read wait for all LDS DMA, so a longer ring gains them nothing.)  Products are
+// formed transposed, so that a lane holds neighbouring columns of one row and
+// results go from registers to memory without LDS.
+//
+// What bounds them.  Many rows: the matrix cores and what feeds them.  The
+// gate/up stage of 16384 rows, 8 experts of (14336, 4096), takes 3.35-3.45 ms,
+// 1.12-1.15 PFLOP/s: matrix cores busy 60-65 % of the cycles, at 1.65 GHz (the
+// clock falls with the power drawn); a large dense library product reaches 1.2-1.5.
+// Of 8 experts of (4096, 11008), 16384 rows: dx 1.40 ms, dW 1.38 ms (1.05-1.07
+// PFLOP/s; dW with loads that fetch nothing 1.0 ms: L2 delivers 64 KB per CU and
+// 64-deep k-step).  64 experts with 512 rows each, where a tile has only 16 to 32
+// k-steps and the last tile of an expert is half empty: 181 us for (2048, 1024),
+// 0.76 PFLOP/s (111 us as one dense product).  Few rows: the weights, at
+// 5-5.9 TB/s; small tiles then, see the rules at the end.
 #include "common.hpp"
 #include "grouped.hpp"
 #include "mfma.hpp"
@@ -739,6 +753,17 @@ void grouped_kernel(GroupedArgs p) {
   }
 }
 
+// Tiles of R rows in at most min(E + 2, R) groups that have any.
+template <class TL>
+int64_t row_column_tiles(const GroupedArgs& a) {
+  const int64_t groups = a.E + 2 < a.R ? a.E + 2 : a.R;
+  return (a.R / TL::kBM + groups) * (((int64_t)a.n + TL::kBN - 1) / TL::kBN);
+}
+// A launch has fewer than 2^32 threads; validation bounds the tiles of 128 x 64
+// and larger.
+template <class TL>
+bool fits(const GroupedArgs& a) { return row_column_tiles<TL>(a) * TL::kThreads < (int64_t(1) << 32); }
+
 template <typename T, Form F, Out O, Act ACT, int NB, class TL, int kGroupM = 8>
 hipError_t launch(const GroupedArgs& a, hipStream_t s) {
   const int64_t ntn = ((int64_t)a.n + TL::kBN - 1) / TL::kBN;
@@ -746,9 +771,7 @@ hipError_t launch(const GroupedArgs& a, hipStream_t s) {
   if (F == Form::kTN) {
     tiles = 8 * (int64_t)a.E * ((a.halves * (((int64_t)a.m + TL::kBM - 1) / TL::kBM) * ntn + 7) / 8);
   } else {
-    // Row tiles of R rows in at most min(E + 2, R) groups that have any.
-    const int64_t groups = a.E + 2 < a.R ? a.E + 2 : a.R;
-    tiles = (a.R / TL::kBM + groups) * ntn;
+    tiles = row_column_tiles<TL>(a);
   }
   if (tiles == 0) return hipSuccess;
   const size_t lds = (size_t)Ring<T, F, TL>::kDepth * (TL::kBM + NB * TL::kBN) * Ring<T, F, TL>::kChunks * 16;
@@ -807,11 +830,11 @@ template <Out O, Act A>
 hipError_t dual(Dt dt, GroupedArgs a, hipStream_t s) {
   a.stagger = weights_bound(a);
   if (dt == Dt::kF32)
-    return few_f32(a, DualF32::kBN) ? launch<float, Form::kNT, O, A, 2, DualF32Few>(a, s)
+    return few_f32(a, DualF32::kBN) && fits<DualF32Few>(a) ? launch<float, Form::kNT, O, A, 2, DualF32Few>(a, s)
                                     : launch<float, Form::kNT, O, A, 2, DualF32>(a, s);
   // (The small tile's ring has no room for the recompute's dh tile.)
   if constexpr (O == Out::kGated)
-    if (few_bf16(a, Dual::kBN, 64)) return launch<bf16, Form::kNT, O, A, 2, DualFew>(a, s);
+    if (few_bf16(a, Dual::kBN, 64) && fits<DualFew>(a)) return launch<bf16, Form::kNT, O, A, 2, DualFew>(a, s);
   return launch<bf16, Form::kNT, O, A, 2, Dual>(a, s);
 }
 
@@ -820,10 +843,11 @@ hipError_t single(Dt dt, GroupedArgs a, hipStream_t s) {
   a.stagger = F == Form::kNT && weights_bound(a);
   using Few = std::conditional_t<F == Form::kNT, SingleFewNT, SingleFew>;
   if (dt == Dt::kF32)
-    return few_f32(a, SingleF32::kBN) ? launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32Few>(a, s)
+    return few_f32(a, SingleF32::kBN) && fits<SingleF32Few>(a) ? launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32Few>(a, s)
                                       : launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32>(a, s);
-  return few_bf16(a, Single::kBN, F == Form::kNT ? 32 : 16) ? launch<bf16, F, Out::kStore, Act::kSilu, 1, Few, 4>(a, s)
-                                                            : launch<bf16, F, Out::kStore, Act::kSilu, 1, Single, 4>(a, s);
+  return few_bf16(a, Single::kBN, F == Form::kNT ? 32 : 16) && fits<Few>(a)
+             ? launch<bf16, F, Out::kStore, Act::kSilu, 1, Few, 4>(a, s)
+             : launch<bf16, F, Out::kStore, Act::kSilu, 1, Single, 4>(a, s);
 }
 
 }  // namespace

@@ -263,6 +263,18 @@ def test_hundreds_of_experts(dt):
         within(t, *want, f"1024 experts {dt} {name}")
 
 
+def test_more_small_tiles_than_a_launch_has():
+    """Many experts of very many columns: small row and column tiles would be past 2^32 threads."""
+    E, N, K, R = 252, (1 << 21) - 32, 8, 255        # (the most rows that 252 experts of as many columns may have)
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device=DEV)
+    w[3, -1] = w[251, 0] = 1.0
+    x = torch.ones((R, K), dtype=torch.bfloat16, device=DEV)
+    h = S.grouped_fwd(x, w, w, offsets_of([1] * E))
+    at = torch.nonzero(h.view(torch.int16))
+    assert at.tolist() == [[3, N - 1], [251, 0]]
+    assert abs(h[3, -1].item() - 64 / (1 + math.exp(-8))) <= 64 * 2 ** -8
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_offsets_that_decrease_stay_inside(dt):
     """Offsets no plan gives (decreasing, negative, past the rows): nothing outside the outputs is touched, and the
