@@ -22,7 +22,7 @@ from .group_ops import (  # noqa: F401
     ExpertRowsFunction, ExpertSumFunction, GroupedLinearFunction, GroupedSwiGLUFunction, RoutedMLPFunction, clip_grads,
     expert_combine, expert_combine_bwd, expert_gather, expert_plan, expert_plan_workspace_bytes, expert_rows, expert_sum,
     grad_norm, grad_norm_workspace_bytes, grouped_bwd, grouped_bwd_workspace_bytes, grouped_fwd, grouped_linear,
-    grouped_mm, grouped_mm_bwd, grouped_swiglu, routed_mlp,
+    grouped_mm, grouped_mm_bwd, grouped_mm_bwd_workspace_bytes, grouped_swiglu, routed_mlp,
 )
 from .ops import (  # noqa: F401
     SwiGLUFunction, act_bwd, act_bwd_fp8, act_fwd, act_quant, probe_act_quant_stream, bwd, bwd_noalloc, bwd_workspace_bytes, fwd, fwd_fp8, gemv_fwd, probe_gemv_read,
@@ -34,6 +34,7 @@ __all__ = ["fwd", "fwd_fp8", "bwd", "bwd_noalloc", "gemv_fwd", "act_fwd", "act_q
            "block_norm_bwd_workspace_bytes", "block_norms", "BlockNormFunction",
            "expert_plan", "expert_plan_workspace_bytes", "expert_gather", "expert_combine", "expert_combine_bwd",
            "grouped_fwd", "grouped_bwd", "grouped_bwd_workspace_bytes", "grouped_mm", "grouped_mm_bwd",
+           "grouped_mm_bwd_workspace_bytes",
            "expert_rows", "expert_sum", "grouped_swiglu", "grouped_linear", "routed_mlp", "ExpertRowsFunction",
            "ExpertSumFunction", "GroupedSwiGLUFunction", "GroupedLinearFunction", "RoutedMLPFunction", "grad_norm",
            "grad_norm_workspace_bytes", "clip_grads", "SwigluError", "lib", "LIB_PATH"]

@@ -504,6 +504,8 @@ int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int6
     g.b0 = wg; g.b1 = wu; g.ldb = K; g.b0_stride = wg_stride; g.b1_stride = wu_stride;
     g.n = (int)K; g.r = (int)N; g.halves = 2;
     g.out0 = dx; g.ldo = K;
+    g.parts = swg::split_parts(dtype, R, E, K, N, 2);
+    g.part = reinterpret_cast<float*>(ws + swg::grouped_bwd_layout(dtype, R, N, K, src != nullptr).off_part);
     if ((e = swg::launch_grouped_nn(dt, g, s)) != hipSuccess) return hip_status(e);
   }
   // 3. dWg = dg^T x, dWu = du^T x, reducing over each expert's rows.
@@ -532,11 +534,17 @@ int swiglu_grouped_mm(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, con
   return hip_status(swg::launch_grouped_nt(as_dt(dtype), a, as_stream(stream)));
 }
 
+size_t swiglu_grouped_mm_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, int64_t K) {
+  return swg::grouped_mm_bwd_workspace_total(dtype, R, N, K);
+}
+
 int swiglu_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x,
                           const int32_t* offsets, const void* w, int64_t w_stride, const void* dy, void* dx, void* dw,
-                          void* stream) {
+                          void* workspace, size_t workspace_bytes, void* stream) {
   int st = swg::validate_grouped_mm_bwd(dtype, R, E, N, K, x, offsets, w, w_stride, dy, dx, dw);
   if (st != SWIGLU_OK || K == 0) return st;
+  st = swg::validate_grouped_mm_bwd_workspace(dtype, R, N, K, dx, workspace, workspace_bytes);
+  if (st != SWIGLU_OK) return st;
   const swg::Dt dt = as_dt(dtype);
   hipError_t e = hipSuccess;
   if (dx != nullptr && R > 0) {
@@ -546,6 +554,8 @@ int swiglu_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K,
     a.b0 = w; a.ldb = K; a.b0_stride = w_stride;
     a.n = (int)K; a.r = (int)N; a.halves = 1;
     a.out0 = dx; a.ldo = K;
+    a.parts = swg::split_parts(dtype, R, E, K, N, 1);
+    a.part = static_cast<float*>(workspace);
     if ((e = swg::launch_grouped_nn(dt, a, as_stream(stream))) != hipSuccess) return hip_status(e);
   }
   if (dw != nullptr && N > 0) {

@@ -47,13 +47,14 @@
 #include "common.hpp"
 #include "grouped.hpp"
 #include "mfma.hpp"
+#include "validate.hpp"
 
 namespace swg {
 
 namespace {
 
 enum class Form { kNT, kNN, kTN };
-enum class Out { kGated, kDGated, kStore };
+enum class Out { kGated, kDGated, kStore, kPart };
 
 // act(z) and, for the gradient, act'(z): SiLU a = z s, a' = s (1 + z (1 - s)),
 // s = sigma(z); GELU (tanh form) a = z s, a' = s + z s (1 - s) t'(z),
@@ -258,7 +259,11 @@ void grouped_kernel(GroupedArgs p) {
   // Reduction: k-steps per half (NN has one or two halves, TN one over rows).
   const int red = F == Form::kTN ? rows : p.r;
   const int nkh = live ? (red + kStep - 1) / kStep : 0;
-  const int nk = (F == Form::kNN ? p.halves : 1) * nkh;
+  const int nks = (F == Form::kNN ? p.halves : 1) * nkh;
+  // kPart: the part's k-steps, ks0 up to ks0 + nk.
+  const int per_part = O == Out::kPart ? (nks + p.parts - 1) / p.parts : nks;
+  const int ks0 = O == Out::kPart ? (int)blockIdx.y * per_part : 0;
+  const int nk = O != Out::kPart || nks - ks0 > per_part ? per_part : (nks > ks0 ? nks - ks0 : 0);
 
   // ---- operand A
   // Contiguous: instruction d of the wave fills kRowsDma LDS rows from
@@ -378,8 +383,8 @@ void grouped_kernel(GroupedArgs p) {
   const int first = F == Form::kNT && p.stagger && nk > 0 ? (e * ntn + tn) % nk : 0;
   // Instruction q of this wave's kDma for k-step ks, into a slot: A's first.
   auto issue_one = [&](int ks, int slot, int q) {
-    const int h = F == Form::kNN && ks >= nkh ? 1 : 0;
-    int s = ks - h * nkh;
+    const int h = F == Form::kNN && ks0 + ks >= nkh ? 1 : 0;
+    int s = ks0 + ks - h * nkh;
     if constexpr (F == Form::kNT) s = s + first < nk ? s + first : s + first - nk;
     const int rem = (red + kPer - 1) / kPer - s * KC;     // chunks of reduction left (contiguous)
     const bool past = ks >= nk;
@@ -705,7 +710,28 @@ void grouped_kernel(GroupedArgs p) {
     }
   };
   constexpr int kOuts = O == Out::kDGated ? 2 : 1;
-  if constexpr (kB16) {
+  if constexpr (O == Out::kPart) {
+    float* const o0 = p.part + ((int64_t)blockIdx.y * p.R + row0) * p.n;
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) {
+      const int row = wm * kWM + i * kMN + lane % kMN;
+      if (row >= mrows) continue;
+#pragma unroll
+      for (int j = 0; j < kTN; ++j)
+#pragma unroll
+        for (int q = 0; q < AccL<kMN>::kE; q += 4) {
+          const int col = n0 + wn * kWN + j * kMN + (kB16 ? 4 * (lane >> 4) : AccL<32>::row(lane, q));
+          if (col >= p.n) continue;
+          f32x4 v;
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            if constexpr (kB16) v[z] = acc[0][i][j][q + z];
+            else v[z] = sum[0][i][j][q + z];
+          }
+          *reinterpret_cast<f32x4*>(o0 + (int64_t)row * p.n + col) = v;
+        }
+    }
+  } else if constexpr (kB16) {
     // Two tiles of 16 columns together: a swap of 16-lane rows gives every
     // lane 8 neighbouring columns, and the four lanes of a row 64 bytes.
     const int g = lane >> 4;
@@ -800,8 +826,36 @@ hipError_t launch(const GroupedArgs& a, hipStream_t s) {
   const size_t lds = (size_t)Ring<T, F, TL>::kDepth * (TL::kBM + NB * TL::kBN) * Ring<T, F, TL>::kChunks * 16;
   const hipError_t attr = allow_lds<&grouped_kernel<T, F, O, ACT, NB, TL, kGroupM>>(lds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((grouped_kernel<T, F, O, ACT, NB, TL, kGroupM>), dim3((unsigned)tiles), dim3(TL::kThreads), lds,
-                     s, a);
+  hipLaunchKernelGGL((grouped_kernel<T, F, O, ACT, NB, TL, kGroupM>),
+                     dim3((unsigned)tiles, O == Out::kPart ? (unsigned)a.parts : 1u), dim3(TL::kThreads), lds, s, a);
+  return hipGetLastError();
+}
+
+// out = the parts' sums in order, four elements to a thread.
+constexpr int kSumThreads = 256;
+template <typename T>
+__global__ __launch_bounds__(kSumThreads) void sum_parts_kernel(const f32x4* part, int parts, int64_t n4, T* out) {
+  const int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
+  if (i >= n4) return;
+  f32x4 v = part[i];
+  for (int p = 1; p < parts; ++p) v += part[(int64_t)p * n4 + i];
+  if constexpr (sizeof(T) == 2) {
+    u32x2 o;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) o[q] = __builtin_bit_cast(uint32_t, bf16x2{to_bf16(v[2 * q]), to_bf16(v[2 * q + 1])});
+    reinterpret_cast<u32x2*>(out)[i] = o;
+  } else {
+    reinterpret_cast<f32x4*>(out)[i] = v;
+  }
+}
+
+template <typename T, class TL, int kGroupM>
+hipError_t launch_parts(const GroupedArgs& a, hipStream_t s) {
+  const hipError_t e = launch<T, Form::kNN, Out::kPart, Act::kSilu, 1, TL, kGroupM>(a, s);
+  if (e != hipSuccess) return e;
+  const int64_t n4 = (int64_t)a.R * a.n / 4;
+  hipLaunchKernelGGL((sum_parts_kernel<T>), dim3((unsigned)((n4 + kSumThreads - 1) / kSumThreads)), dim3(kSumThreads),
+                     0, s, reinterpret_cast<const f32x4*>(a.part), a.parts, n4, static_cast<T*>(a.out0));
   return hipGetLastError();
 }
 
@@ -865,6 +919,12 @@ template <Form F>
 hipError_t single(Dt dt, GroupedArgs a, hipStream_t s) {
   a.stagger = F == Form::kNT && weights_bound(a);
   using Few = std::conditional_t<F == Form::kNT, SingleFewNT, SingleFew>;
+  if constexpr (F == Form::kNN) {
+    static_assert(SingleFew::kBM == kSplitBf16.bm && SingleFew::kBN == kSplitBf16.bn && SingleF32Few::kBM == kSplitF32.bm &&
+                  SingleF32Few::kBN == kSplitF32.bn, "split_parts counts these tiles");
+    if (a.parts > 1)
+      return dt == Dt::kF32 ? launch_parts<float, SingleF32Few, 8>(a, s) : launch_parts<bf16, SingleFew, 4>(a, s);
+  }
   if (dt == Dt::kF32)
     return few_f32(a, SingleF32::kBN) && fits<SingleF32Few>(a) ? launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32Few>(a, s)
                                       : launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32>(a, s);

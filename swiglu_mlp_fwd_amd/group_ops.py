@@ -343,10 +343,18 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: tor
     return y
 
 
+def grouped_mm_bwd_workspace_bytes(dtype: torch.dtype, R: int, N: int, K: int) -> int:
+    """Bytes of workspace of grouped_mm_bwd for dx (0: none is needed)."""
+    if dtype not in _DT:
+        raise TypeError(f"libswiglu supports bfloat16 and float32, got {dtype}")
+    return int(lib().swiglu_grouped_mm_bwd_workspace_bytes(_DT[dtype], R, N, K))
+
+
 def grouped_mm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, out=None,
-                   need_dx: bool = True, need_dw: bool = True):
+                   need_dx: bool = True, need_dw: bool = True, workspace: torch.Tensor | None = None):
     """Gradients of grouped_mm: (dx [R, K], dw [E, N, K]); rows of no expert and experts without rows get zeros.
-    need_dx or need_dw False leaves one out (None).  `out` may pass the two preallocated."""
+    need_dx or need_dw False leaves one out (None).  `out` may pass the two preallocated, `workspace` a uint8 device
+    buffer of at least grouped_mm_bwd_workspace_bytes(...) bytes (a smaller or missing one is replaced)."""
     _same(x, w, dy)
     dt = _dtype_code(x)
     E, N, K = _grouped_weights(w, "w")
@@ -364,6 +372,7 @@ def grouped_mm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, offsets: 
                 _check_out(t, name, shape, x.dtype, x.device)
             elif t is not None:
                 raise ValueError("out has an output that this call does not compute")
+    _check_workspace(workspace, x.device)
     _on_gpu(x)
     x2, d2 = _dense16(x), _dense16(dy)
     w, sw = _weights16(w, N, K)
@@ -371,7 +380,8 @@ def grouped_mm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, offsets: 
         out = (torch.empty((R, K), dtype=x.dtype, device=x.device) if need_dx else None,
                torch.empty((E, N, K), dtype=x.dtype, device=x.device) if need_dw else None)
     dx, dw = out
-    _call("swiglu_grouped_mm_bwd", x, dt, R, E, N, K, _p(x2), _p(offsets), _p(w), sw, _p(d2), _p(dx), _p(dw))
+    ws, n = _workspace(workspace, int(lib().swiglu_grouped_mm_bwd_workspace_bytes(dt, R, N, K)) if need_dx else 0, x.device)
+    _call("swiglu_grouped_mm_bwd", x, dt, R, E, N, K, _p(x2), _p(offsets), _p(w), sw, _p(d2), _p(dx), _p(dw), _p(ws), n)
     return dx, dw
 
 

@@ -70,6 +70,19 @@ static void overlaps() {
 
 static void sizes() {
   using namespace swg;
+  for (int dt : {SWIGLU_F32, SWIGLU_BF16})
+    for (int64_t R : {1, 3, 35, 64, 65, 130, 500, 4001, 100000})
+      for (int64_t n : {8, 248, 256, 264, 3824, 8192})
+        for (int64_t r : {0, 8, 512, 1024, 13448, 131072})
+          for (int halves : {1, 2})
+            for (int64_t E : {1, 2, 39, 1024}) {
+              const int parts = split_parts(dt, R, E, n, r, halves);
+              const SplitTile t = dt == SWIGLU_BF16 ? kSplitBf16 : kSplitF32;
+              const int64_t steps = halves * ((r + t.step - 1) / t.step);
+              check(parts >= 1 && (parts == 1 || (parts * 8 <= steps && parts <= t.target)), "parts of 8 k-steps at least");
+              check(parts == 1 || (size_t)(parts * R * n * 4) <= split_bytes(dt, R, n, r, halves), "the parts' sums fit");
+              check(split_bytes(dt, R, n, r, halves) <= (size_t)t.target * t.bm * t.bn * 4 + 256, "as many as tiles");
+            }
   check(grouped_bwd_workspace_total(SWIGLU_BF16, (int64_t(1) << 30) - 1024, 8, 8, true) > size_t(1) << 34, "rows near 2^30");
   check(grouped_bwd_workspace_total(SWIGLU_BF16, kMaxDim, 8, 8, true) == 0, "more row tiles than a launch has");
   check(grouped_shape_status(SWIGLU_F32, kMaxDim, 1024, kMaxDim, kMaxDim) != SWIGLU_OK, "sizes that overflow");

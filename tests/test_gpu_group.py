@@ -263,6 +263,30 @@ def test_hundreds_of_experts(dt):
         within(t, *want, f"1024 experts {dt} {name}")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,N,K", [([3], 13448, 248), ([2, 1], 4104, 8), ([0, 70, 0, 3], 2056, 264),
+                                        ([40] * 5, 1600, 1744), ([1] * 39, 4928, 72), ([130], 1024, 512)])
+def test_split_reduction(dt, counts, N, K):
+    """dx of few rows: the reduction over N in parts, with rows of no expert in front and behind."""
+    offsets, R, E = offsets_of(counts, 2), 2 + sum(counts) + 3, len(counts)
+    x, xc = poisoned(normal((R, K), 1, dt), offsets)
+    dy, dyc = poisoned(normal((R, N), 2, dt), offsets)
+    wg, wu, o = normal((E, N, K), 3, dt, K ** -0.5), normal((E, N, K), 4, dt, K ** -0.5), offsets.cpu().numpy()
+    ws = workspace(S.grouped_mm_bwd_workspace_bytes(DT[dt], R, N, K))
+    dx = guarded((R, K), DT[dt])
+    S.grouped_mm_bwd(x, wg, dy, offsets, out=(dx.t, None), need_dw=False, workspace=ws)
+    check_guards("split product", dx)
+    within(dx.t, *G.mm_bwd(host(xc), host(wg), host(dyc), o, ROUND[dt])[0], f"product dx {dt} {counts} {N} {K}")
+    assert torch.equal(dx.t, S.grouped_mm_bwd(x, wg, dy, offsets, need_dw=False)[0])
+    ws = workspace(S.grouped_bwd_workspace_bytes(DT[dt], R, N, K))
+    dx = guarded((R, K), DT[dt])
+    S.grouped_bwd(x, wg, wu, dy, offsets, out=(dx.t, None, None), need_dw=False, workspace=ws)
+    check_guards("split gate/up", dx)
+    within(dx.t, *G.gate_up_bwd(host(xc), host(wg), host(wu), host(dyc), o, "silu", ROUND[dt])[0],
+           f"gate/up dx {dt} {counts} {N} {K}")
+    assert torch.equal(dx.t, S.grouped_bwd(x, wg, wu, dy, offsets, need_dw=False)[0])
+
+
 def test_more_small_tiles_than_a_launch_has():
     """Many experts of very many columns: small row and column tiles would be past 2^32 threads."""
     E, N, K, R = 252, (1 << 21) - 32, 8, 255        # (the most rows that 252 experts of as many columns may have)

@@ -76,8 +76,9 @@ def grouped_calls(L):  # noqa: F811
     def mm(dt=1, R=64, E=4, N=40, K=64, x=A, off=A, w=A, sw=40 * 64, y=A):
         return L.swiglu_grouped_mm(dt, R, E, N, K, x, off, w, sw, y, None)
 
-    def mm_bwd(dt=1, R=64, E=4, N=40, K=64, x=A, off=A, w=A, sw=40 * 64, dy=A, dx=A, dw=A):
-        return L.swiglu_grouped_mm_bwd(dt, R, E, N, K, x, off, w, sw, dy, dx, dw, None)
+    def mm_bwd(dt=1, R=64, E=4, N=40, K=64, x=A, off=A, w=A, sw=40 * 64, dy=A, dx=A, dw=A,
+               ws=A, n=1 << 40):
+        return L.swiglu_grouped_mm_bwd(dt, R, E, N, K, x, off, w, sw, dy, dx, dw, ws, n, None)
     return fwd, bwd, mm, mm_bwd
 
 
@@ -123,6 +124,23 @@ def test_gathered_validation(L):  # noqa: F811
         # Tokens of 2^31 bytes: gather first.
         big = dict(R=1 << 19, T=1 << 19, k=1, K=2048, sg=1 << 30, su=1 << 30)
         assert f(src=A, **big) == EUNSUP
+
+
+def test_product_gradient_workspace(L):  # noqa: F811
+    """The parts' sums of a split dx: many columns to reduce over, few tiles."""
+    need = L.swiglu_grouped_mm_bwd_workspace_bytes
+    _, _, _, mm_bwd = grouped_calls(L)
+    long = dict(R=64, N=4096, K=64, sw=4096 * 64)
+    for dt in (0, 1):
+        n = need(dt, 64, 4096, 64)
+        assert n > 0 and n % 256 == 0 and n % (64 * 64 * 4) == 0
+        assert need(dt, 64, 40, 64) == need(dt, 1 << 20, 4096, 64) == need(dt, 0, 4096, 64) == need(dt, -1, 8, 8) == 0
+        assert mm_bwd(dt=dt, ws=None, **long) == EWS and mm_bwd(dt=dt, n=n - 1, **long) == EWS
+        assert mm_bwd(dt=dt, ws=A + 128, **long) == EALIGN
+        assert S.grouped_mm_bwd_workspace_bytes((torch.float32, torch.bfloat16)[dt], 64, 4096, 64) == n
+        assert L.swiglu_grouped_bwd_workspace_bytes(dt, 64, 4096, 64, 0) > 64 * 2 * 4096 * (4, 2)[dt]
+    with pytest.raises(TypeError):
+        S.grouped_mm_bwd_workspace_bytes(torch.float16, 1, 8, 8)
 
 
 def test_grouped_workspace(L):  # noqa: F811
