@@ -625,16 +625,16 @@ int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int6
 int swiglu_grouped_mm(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, const int32_t* offsets,
                       const void* w, int64_t w_stride, void* y, void* stream);
 
-/* Bytes of device workspace swiglu_grouped_mm_bwd needs for dx (0 for sizes it
- * rejects, and for those that need none). */
+/* Bytes of device workspace swiglu_grouped_mm_bwd needs (0 for sizes it rejects,
+ * and for those that need none). */
 size_t swiglu_grouped_mm_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, int64_t K);
 
 /* Gradients of swiglu_grouped_mm: dx[r] = dy[r] W_e [R, K] (0 for rows of no
  * expert), dw[e] = sum over the expert's rows of dy[r]^T x[r], [E, N, K] dense
  * (0 without rows).  dx or dw may be NULL; x is read for dw only, w for dx.
  *   workspace    at least swiglu_grouped_mm_bwd_workspace_bytes(...) bytes,
- *                256-byte aligned (NULL where none is needed or dx is NULL);
- *                scratch (calls that overlap need one each) */
+ *                256-byte aligned (NULL where none is needed); scratch
+ *                (calls that overlap need one each) */
 int swiglu_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x,
                           const int32_t* offsets, const void* w, int64_t w_stride, const void* dy, void* dx, void* dw,
                           void* workspace, size_t workspace_bytes, void* stream);

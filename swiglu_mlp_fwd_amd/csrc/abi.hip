@@ -516,6 +516,8 @@ int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int6
     g.b0 = rows; g.ldb = K;
     g.m = (int)N; g.n = (int)K; g.halves = 2;
     g.out0 = dwg; g.out1 = dwu; g.ldo = K;
+    g.parts = swg::split_row_parts(dtype, R, E, N, K, 2);
+    g.part = reinterpret_cast<float*>(ws + swg::grouped_bwd_layout(dtype, R, N, K, src != nullptr).off_part);
     if ((e = swg::launch_grouped_tn(dt, g, s)) != hipSuccess) return hip_status(e);
   }
   return SWIGLU_OK;
@@ -543,7 +545,7 @@ int swiglu_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K,
                           void* workspace, size_t workspace_bytes, void* stream) {
   int st = swg::validate_grouped_mm_bwd(dtype, R, E, N, K, x, offsets, w, w_stride, dy, dx, dw);
   if (st != SWIGLU_OK || K == 0) return st;
-  st = swg::validate_grouped_mm_bwd_workspace(dtype, R, N, K, dx, workspace, workspace_bytes);
+  st = swg::validate_grouped_mm_bwd_workspace(dtype, R, N, K, workspace, workspace_bytes);
   if (st != SWIGLU_OK) return st;
   const swg::Dt dt = as_dt(dtype);
   hipError_t e = hipSuccess;
@@ -565,6 +567,8 @@ int swiglu_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K,
     a.b0 = x; a.ldb = K;
     a.m = (int)N; a.n = (int)K; a.halves = 1;
     a.out0 = dw; a.ldo = K;
+    a.parts = swg::split_row_parts(dtype, R, E, N, K, 1);
+    a.part = static_cast<float*>(workspace);
     e = swg::launch_grouped_tn(dt, a, as_stream(stream));
   }
   return hip_status(e);

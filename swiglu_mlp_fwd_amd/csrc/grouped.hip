@@ -711,7 +711,8 @@ void grouped_kernel(GroupedArgs p) {
   };
   constexpr int kOuts = O == Out::kDGated ? 2 : 1;
   if constexpr (O == Out::kPart) {
-    float* const o0 = p.part + ((int64_t)blockIdx.y * p.R + row0) * p.n;
+    const int64_t before = F == Form::kTN ? ((int64_t)blockIdx.y * p.halves + half) * p.E * p.m : (int64_t)blockIdx.y * p.R;
+    float* const o0 = p.part + (before + orow0) * p.n;
 #pragma unroll
     for (int i = 0; i < kTM; ++i) {
       const int row = wm * kWM + i * kMN + lane % kMN;
@@ -834,11 +835,12 @@ hipError_t launch(const GroupedArgs& a, hipStream_t s) {
 // out = the parts' sums in order, four elements to a thread.
 constexpr int kSumThreads = 256;
 template <typename T>
-__global__ __launch_bounds__(kSumThreads) void sum_parts_kernel(const f32x4* part, int parts, int64_t n4, T* out) {
+__global__ __launch_bounds__(kSumThreads) void sum_parts_kernel(const f32x4* part, int parts, int64_t stride4,
+                                                                int64_t n4, T* out) {
   const int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
   if (i >= n4) return;
   f32x4 v = part[i];
-  for (int p = 1; p < parts; ++p) v += part[(int64_t)p * n4 + i];
+  for (int p = 1; p < parts; ++p) v += part[p * stride4 + i];
   if constexpr (sizeof(T) == 2) {
     u32x2 o;
 #pragma unroll
@@ -849,14 +851,18 @@ __global__ __launch_bounds__(kSumThreads) void sum_parts_kernel(const f32x4* par
   }
 }
 
-template <typename T, class TL, int kGroupM>
+template <typename T, Form F, class TL, int kGroupM>
 hipError_t launch_parts(const GroupedArgs& a, hipStream_t s) {
-  const hipError_t e = launch<T, Form::kNN, Out::kPart, Act::kSilu, 1, TL, kGroupM>(a, s);
-  if (e != hipSuccess) return e;
-  const int64_t n4 = (int64_t)a.R * a.n / 4;
-  hipLaunchKernelGGL((sum_parts_kernel<T>), dim3((unsigned)((n4 + kSumThreads - 1) / kSumThreads)), dim3(kSumThreads),
-                     0, s, reinterpret_cast<const f32x4*>(a.part), a.parts, n4, static_cast<T*>(a.out0));
-  return hipGetLastError();
+  hipError_t e = launch<T, F, Out::kPart, Act::kSilu, 1, TL, kGroupM>(a, s);
+  const int halves = F == Form::kTN ? a.halves : 1;        // outputs
+  const int64_t n4 = (F == Form::kTN ? (int64_t)a.E * a.m : (int64_t)a.R) * a.n / 4;
+  for (int h = 0; h < halves && e == hipSuccess; ++h) {
+    hipLaunchKernelGGL((sum_parts_kernel<T>), dim3((unsigned)((n4 + kSumThreads - 1) / kSumThreads)), dim3(kSumThreads),
+                       0, s, reinterpret_cast<const f32x4*>(a.part) + h * n4, a.parts, halves * n4, n4,
+                       static_cast<T*>(h == 0 ? a.out0 : a.out1));
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 using Dual = Tile<256, 128, 4, 2>;
@@ -923,7 +929,7 @@ hipError_t single(Dt dt, GroupedArgs a, hipStream_t s) {
     static_assert(SingleFew::kBM == kSplitBf16.bm && SingleFew::kBN == kSplitBf16.bn && SingleF32Few::kBM == kSplitF32.bm &&
                   SingleF32Few::kBN == kSplitF32.bn, "split_parts counts these tiles");
     if (a.parts > 1)
-      return dt == Dt::kF32 ? launch_parts<float, SingleF32Few, 8>(a, s) : launch_parts<bf16, SingleFew, 4>(a, s);
+      return dt == Dt::kF32 ? launch_parts<float, F, SingleF32Few, 8>(a, s) : launch_parts<bf16, F, SingleFew, 4>(a, s);
   }
   if (dt == Dt::kF32)
     return few_f32(a, SingleF32::kBN) && fits<SingleF32Few>(a) ? launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32Few>(a, s)
@@ -948,6 +954,11 @@ hipError_t launch_grouped_nt(Dt dt, const GroupedArgs& a, hipStream_t s) { retur
 hipError_t launch_grouped_nn(Dt dt, const GroupedArgs& a, hipStream_t s) { return single<Form::kNN>(dt, a, s); }
 
 hipError_t launch_grouped_tn(Dt dt, const GroupedArgs& a, hipStream_t s) {
+  static_assert(Single::kBM == kSplitRowsBf16.bm && Single::kBN == kSplitRowsBf16.bn && SingleF32::kBM == kSplitRowsF32.bm &&
+                SingleF32::kBN == kSplitRowsF32.bn, "split_row_parts counts these tiles");
+  if (a.parts > 1)
+    return dt == Dt::kBF16 ? launch_parts<bf16, Form::kTN, Single, 4>(a, s)
+                           : launch_parts<float, Form::kTN, SingleF32, 8>(a, s);
   return dt == Dt::kBF16 ? launch<bf16, Form::kTN, Out::kStore, Act::kSilu, 1, Single, 4>(a, s)
                          : launch<float, Form::kTN, Out::kStore, Act::kSilu, 1, SingleF32, 8>(a, s);
 }

@@ -29,8 +29,8 @@ struct GroupedArgs {
   void *out0, *out1;        // TN: the two halves' outputs
   int64_t ldo;
   const void* dh;           // recompute: [R, n]
-  int parts;                // NN: the reduction in parts (split_parts of validate.hpp), their sums fp32 in
-  float* part;              // workspace, [parts, R, n]; parts <= 1: unused
+  int parts;                // NN, TN: the reduction in parts (split_parts, split_row_parts of validate.hpp), their
+  float* part;              // sums fp32 in workspace, as many times the outputs; parts <= 1: unused
 };
 
 hipError_t launch_grouped_gated(Dt dt, Act act, const GroupedArgs& a, hipStream_t s);

@@ -344,7 +344,7 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: tor
 
 
 def grouped_mm_bwd_workspace_bytes(dtype: torch.dtype, R: int, N: int, K: int) -> int:
-    """Bytes of workspace of grouped_mm_bwd for dx (0: none is needed)."""
+    """Bytes of workspace of grouped_mm_bwd (0: none is needed)."""
     if dtype not in _DT:
         raise TypeError(f"libswiglu supports bfloat16 and float32, got {dtype}")
     return int(lib().swiglu_grouped_mm_bwd_workspace_bytes(_DT[dtype], R, N, K))
@@ -380,7 +380,7 @@ def grouped_mm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, offsets: 
         out = (torch.empty((R, K), dtype=x.dtype, device=x.device) if need_dx else None,
                torch.empty((E, N, K), dtype=x.dtype, device=x.device) if need_dw else None)
     dx, dw = out
-    ws, n = _workspace(workspace, int(lib().swiglu_grouped_mm_bwd_workspace_bytes(dt, R, N, K)) if need_dx else 0, x.device)
+    ws, n = _workspace(workspace, int(lib().swiglu_grouped_mm_bwd_workspace_bytes(dt, R, N, K)), x.device)
     _call("swiglu_grouped_mm_bwd", x, dt, R, E, N, K, _p(x2), _p(offsets), _p(w), sw, _p(d2), _p(dx), _p(dw), _p(ws), n)
     return dx, dw
 

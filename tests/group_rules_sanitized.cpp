@@ -81,6 +81,12 @@ static void sizes() {
               const int64_t steps = halves * ((r + t.step - 1) / t.step);
               check(parts >= 1 && (parts == 1 || (parts * 8 <= steps && parts <= t.target)), "parts of 8 k-steps at least");
               check(parts == 1 || (size_t)(parts * R * n * 4) <= split_bytes(dt, R, n, r, halves), "the parts' sums fit");
+              const int row_parts = split_row_parts(dt, R, E, r, n, halves);
+              const SplitTile w = dt == SWIGLU_BF16 ? kSplitRowsBf16 : kSplitRowsF32;
+              check(row_parts >= 1 && (row_parts == 1 || row_parts * 8 * E * w.step <= R), "8 k-steps of each expert's rows");
+              check(row_parts == 1 || (size_t)(row_parts * E * halves * r * n * 4) <= split_row_bytes(dt, R, r, n, halves),
+                    "the rows' parts' sums fit");
+              check(split_row_bytes(dt, R, r, n, halves) <= (size_t)w.target * w.bm * w.bn * 4 + 256, "as many as tiles of weights");
               check(split_bytes(dt, R, n, r, halves) <= (size_t)t.target * t.bm * t.bn * 4 + 256, "as many as tiles");
             }
   check(grouped_bwd_workspace_total(SWIGLU_BF16, (int64_t(1) << 30) - 1024, 8, 8, true) > size_t(1) << 34, "rows near 2^30");

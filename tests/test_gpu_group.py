@@ -287,6 +287,28 @@ def test_split_reduction(dt, counts, N, K):
     assert torch.equal(dx.t, S.grouped_bwd(x, wg, wu, dy, offsets, need_dw=False)[0])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,N,K", [([3000], 152, 320), ([1, 6000, 0], 8, 264), ([2000, 40, 2500, 2000], 264, 72)])
+def test_split_rows(dt, counts, N, K):
+    """dW of small weights: each expert's rows in parts, some of them without any."""
+    offsets, R, E = offsets_of(counts, 2), 2 + sum(counts) + 3, len(counts)
+    x, xc = poisoned(normal((R, K), 1, dt), offsets)
+    dy, dyc = poisoned(normal((R, N), 2, dt), offsets)
+    wg, wu, o = normal((E, N, K), 3, dt, K ** -0.5), normal((E, N, K), 4, dt, K ** -0.5), offsets.cpu().numpy()
+    dw = [guarded((E, N, K), DT[dt]) for _ in range(3)]
+    S.grouped_mm_bwd(x, wg, dy, offsets, out=(None, dw[0].t), need_dx=False,
+                     workspace=workspace(S.grouped_mm_bwd_workspace_bytes(DT[dt], R, N, K)))
+    S.grouped_bwd(x, wg, wu, dy, offsets, out=(None, dw[1].t, dw[2].t), need_dx=False,
+                  workspace=workspace(S.grouped_bwd_workspace_bytes(DT[dt], R, N, K)))
+    check_guards("split rows", *dw)
+    want = [G.mm_bwd(host(xc), host(wg), host(dyc), o, ROUND[dt])[1],
+            *G.gate_up_bwd(host(xc), host(wg), host(wu), host(dyc), o, "silu", ROUND[dt])[1:]]
+    for g, w, name in zip(dw, want, ("dw", "dwg", "dwu")):
+        within(g.t, *w, f"{name} {dt} {counts} {N} {K}")
+    assert torch.equal(dw[0].t, S.grouped_mm_bwd(x, wg, dy, offsets)[1])
+    assert all(torch.equal(a.t, b) for a, b in zip(dw[1:], S.grouped_bwd(x, wg, wu, dy, offsets)[1:]))
+
+
 def test_more_small_tiles_than_a_launch_has():
     """Many experts of very many columns: small row and column tiles would be past 2^32 threads."""
     E, N, K, R = 252, (1 << 21) - 32, 8, 255        # (the most rows that 252 experts of as many columns may have)

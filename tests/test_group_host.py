@@ -127,14 +127,15 @@ def test_gathered_validation(L):  # noqa: F811
 
 
 def test_product_gradient_workspace(L):  # noqa: F811
-    """The parts' sums of a split dx: many columns to reduce over, few tiles."""
+    """The parts' sums of split gradients: many columns or rows to reduce over, few tiles."""
     need = L.swiglu_grouped_mm_bwd_workspace_bytes
     _, _, _, mm_bwd = grouped_calls(L)
     long = dict(R=64, N=4096, K=64, sw=4096 * 64)
     for dt in (0, 1):
         n = need(dt, 64, 4096, 64)
         assert n > 0 and n % 256 == 0 and n % (64 * 64 * 4) == 0
-        assert need(dt, 64, 40, 64) == need(dt, 1 << 20, 4096, 64) == need(dt, 0, 4096, 64) == need(dt, -1, 8, 8) == 0
+        assert need(dt, 1 << 20, 40, 64) % (40 * 64 * 4) == 0 and need(dt, 1 << 20, 40, 64) > 0
+        assert need(dt, 64, 40, 64) == need(dt, 1 << 20, 8192, 8192) == need(dt, 0, 4096, 64) == need(dt, -1, 8, 8) == 0
         assert mm_bwd(dt=dt, ws=None, **long) == EWS and mm_bwd(dt=dt, n=n - 1, **long) == EWS
         assert mm_bwd(dt=dt, ws=A + 128, **long) == EALIGN
         assert S.grouped_mm_bwd_workspace_bytes((torch.float32, torch.bfloat16)[dt], 64, 4096, 64) == n
