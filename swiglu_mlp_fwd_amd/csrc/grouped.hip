@@ -43,7 +43,9 @@
 // 64-deep k-step).  64 experts with 512 rows each, where a tile has only 16 to 32
 // k-steps and the last tile of an expert is half empty: 181 us for (2048, 1024),
 // 0.76 PFLOP/s (111 us as one dense product).  Few rows: the weights, at
-// 5-5.9 TB/s; small tiles then, see the rules at the end.
+// 5-5.9 TB/s; small tiles then, see the rules at the end.  Gradients whose tiles
+// are too few for the CUs have their reduction in parts (blockIdx.y), whose fp32
+// sums a second kernel adds in order.
 #include "common.hpp"
 #include "grouped.hpp"
 #include "mfma.hpp"
