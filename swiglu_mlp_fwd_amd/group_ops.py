@@ -555,12 +555,12 @@ def _packed(t: torch.Tensor) -> bool:
 
 
 def _apart(t: torch.Tensor) -> bool:
-    """Whether no two elements of t share a place."""
-    at = 1
+    """Whether no two elements of t share a place: every stride passes what the smaller ones reach."""
+    reach = 0
     for stride, size in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
-        if stride < at:
+        if stride <= reach:
             return False
-        at = stride * size
+        reach += stride * (size - 1)
     return True
 
 
