@@ -10,6 +10,7 @@ stream of the tensors' device.
 """
 from __future__ import annotations
 
+import itertools
 import math
 from array import array
 from operator import attrgetter
@@ -564,6 +565,99 @@ def _apart(t: torch.Tensor) -> bool:
     return True
 
 
+def _place(t: torch.Tensor) -> tuple[int, int, int, list]:
+    """Where t lies: its first byte, its end, the bytes of an element, and (stride in bytes, steps) of its dimensions,
+    the longest stride first."""
+    size, at = t.element_size(), t.data_ptr()
+    dims = sorted(((s * size, n - 1) for s, n in zip(t.stride(), t.shape) if s != 0 and n != 1), reverse=True)
+    return at, at + sum(s * n for s, n in dims) + size, size, dims
+
+
+def _crossing(places: list):
+    """Pairs (i, j) of places that may share memory: their spans cross.  Among views whose outermost strides are equal
+    and whose parts below them do not wrap round that stride (slices of one tensor), these parts' spans cross."""
+    def sweep(group, first, end):
+        group = sorted(group, key=first)
+        for at, i in enumerate(group):
+            for j in itertools.islice(group, at + 1, None):
+                if first(j) >= end(i):
+                    break
+                yield i, j
+
+    def pairs(group):
+        strides = {places[i][3][0][0] if places[i][3] else 0 for i in group}
+        period, base = strides.pop(), min(places[i][0] for i in group)
+        if not strides and period:
+            def low(i):
+                return (places[i][0] - base) % period
+
+            def high(i):
+                return low(i) + places[i][1] - places[i][0] - period * places[i][3][0][1]
+            if max(map(high, group)) <= period:
+                return sweep(group, low, high)
+        return sweep(group, lambda i: places[i][0], lambda i: places[i][1])
+
+    group, end = [], 0
+    for i in sorted(range(len(places)), key=lambda i: places[i][0]):
+        if places[i][0] >= end:
+            if len(group) > 1:
+                yield from pairs(group)
+            group = []
+        group.append(i)
+        end = max(end, places[i][1])
+    if len(group) > 1:
+        yield from pairs(group)
+
+
+def _share(a: tuple, b: tuple) -> bool:
+    """Whether two places have a byte in common: whether, over both, strides times indices (b's counted from its end)
+    and bytes inside an element add up to the distance from a's first byte to b's last.  (True also where that is not
+    told in 20000 steps.)"""
+    unit = math.gcd(a[2], b[2], a[0] - b[0])
+    count = {1: (a[2] + b[2]) // unit - 2}
+    for s, n in a[3] + b[3]:
+        count[s // unit] = count.get(s // unit, 0) + n
+    terms = sorted(count.items(), reverse=True)
+    reach = [sum(s * n for s, n in terms[i:]) for i in range(len(terms) + 1)]
+    common = [math.gcd(*(s for s, n in terms[i:] if n)) for i in range(len(terms) + 1)]
+    steps = 20000
+
+    def adds_up(i, to):
+        nonlocal steps
+        steps -= 1
+        if steps < 0:
+            return True
+        if not 0 <= to <= reach[i]:
+            return False
+        if to in (0, reach[i]):
+            return True
+        if to % common[i]:                       # (0 < to < reach[i]: some term is left)
+            return False
+        s, n = terms[i]
+        return any(adds_up(i + 1, to - s * x) for x in range(max(0, -((reach[i + 1] - to) // s)), min(n, to // s) + 1))
+    return adds_up(0, (b[1] - a[0]) // unit - 1)
+
+
+def _overlap(written: list, read: list | None = None):
+    """Two of the tensors that share memory, as (list, index) pairs, list 0 for written and 1 for read, or None.  What is
+    written may be what is read at the same index, element by element."""
+    at = [(side, i) for side, ts in enumerate((written, read or [])) for i, t in enumerate(ts) if t.numel()]
+    places = [_place((written, read)[side][i]) for side, i in at]
+    for a, b in _crossing(places):
+        (side, i), (other, j) = at[a], at[b]
+        if side == other == 1:
+            continue
+        if side != other and i == j and places[a] == places[b] and _same_strides(written[i], read[i]):
+            continue
+        if _share(places[a], places[b]):
+            return min(at[a], at[b]), max(at[a], at[b])
+    return None
+
+
+def _same_strides(a: torch.Tensor, b: torch.Tensor) -> bool:
+    return all(n == 1 or s == t for n, s, t in zip(a.shape, a.stride(), b.stride()))
+
+
 def _grad_list(grads) -> list:
     return [grads] if isinstance(grads, torch.Tensor) else list(grads)
 
@@ -619,10 +713,10 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, workspace: t
     """Scales the tensors `grads` together to a 2-norm of at most max_norm, g *= min(1, max_norm / (norm + eps)), and
     returns the norm they had (0-dim fp32), without waiting for the GPU.
 
-    In place, or into the tensors `out` of the same shapes and types.  fp32 and bf16 may be mixed; tensors must not
-    overlap each other or be given twice.  A norm that is NaN makes every gradient NaN; an infinite one makes finite
-    elements 0 and infinite ones NaN.  `workspace` may pass a uint8 device buffer of at least
-    grad_norm_workspace_bytes(len(grads)) bytes (a smaller or missing one is replaced)."""
+    In place, or into the tensors `out` of the same shapes and types (out[i] may be grads[i]).  fp32 and bf16 may be
+    mixed; tensors that overlap each other or are given twice are refused.  A norm that is NaN makes every gradient
+    NaN; an infinite one makes finite elements 0 and infinite ones NaN.  `workspace` may pass a uint8 device buffer of
+    at least grad_norm_workspace_bytes(len(grads)) bytes (a smaller or missing one is replaced)."""
     grads = _grad_list(grads)
     codes, dev = _grad_codes(grads)
     max_norm, eps = float(max_norm), float(eps)
@@ -642,6 +736,11 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, workspace: t
         for i, t in enumerate(written):
             if not _apart(t):
                 raise ValueError(f"{'out' if to is not None else 'grads'}[{i}] has elements that share memory, strides {t.stride()}")
+        # Here, since the library sees the stand-ins (contiguous tensors it checks itself).
+        both = _overlap(written, grads if to is not None else None)
+        if both is not None:
+            a, b = (f"{'grads' if to is None or side else 'out'}[{i}]" for side, i in both)
+            raise ValueError(f"{a} and {b} overlap")
         src, dst = list(grads), list(written)
         for i, (g, t) in enumerate(zip(grads, written)):
             if (g.is_contiguous() and t.is_contiguous()) or (g.stride() == t.stride() and _packed(g)):

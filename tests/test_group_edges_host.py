@@ -1,4 +1,6 @@
 """Edges of the operators over rows in order of expert and of the clipping, without a GPU."""
+import random
+
 import pytest
 import torch
 
@@ -17,3 +19,76 @@ def test_slices_that_end_inside_a_stride_are_apart(t, apart):
     assert ops._apart(t) == apart
     with pytest.raises(ValueError, match="GPU" if apart else "share memory"):
         S.clip_grads([t], 1.0)
+
+
+# -------------------------------------- strided gradients that share memory
+
+def columns():
+    return torch.zeros(12, 20)
+
+
+def shares(f, *views):
+    with pytest.raises(ValueError, match="overlap"):
+        f(*views)
+
+
+def test_strided_gradients_that_overlap_are_refused():
+    a = columns()
+    for views in ([a[:, ::2], a[:, ::2]], [a, a[:, ::2]], [a[:, ::2], a[:, 4:7]], [a[::3, 5:9], a[:, 8:]], [a[:, :3], a[2:4, 2:5]],
+                  [a[:, ::2], torch.zeros(5), a[3, 4:5]], [a[:, 1:3], a.view(torch.bfloat16)[:, 5:7]]):
+        shares(S.clip_grads, views, 1.0)
+
+
+def test_strided_outputs_that_overlap_are_refused():
+    a, b, c = columns(), columns(), torch.zeros(12, 10)
+    shares(lambda *v: S.clip_grads([c, c.clone()], 1.0, out=list(v)), a[:, ::2], a[:, :10])      # another output
+    shares(lambda *v: S.clip_grads([a[:, 10:], b[:, 10:]], 1.0, out=list(v)), b[:, 10:], c)      # another's gradient
+    shares(lambda *v: S.clip_grads([a[:, ::2]], 1.0, out=list(v)), a[:, 1:11])                   # its own, shifted
+    square = torch.zeros(6, 6)
+    shares(lambda *v: S.clip_grads([square[:4, :4]], 1.0, out=list(v)), square[:4, :4].t())      # its own, otherwise laid out
+
+
+def test_strided_gradients_that_interleave_are_taken():
+    """Spans that cross without a shared element: the call goes as far as the check for a GPU."""
+    a = columns()
+    deep = torch.zeros(5, 7, 8)
+    for views in ([a[:, ::2], a[:, 1::2]], list(a.split([4, 7, 9], 1)), list(deep.unbind(1)), list(deep.unbind(2)),
+                  [a[::2], a[1::2]], [a[:, ::2], a[:, 1::4], a[:, 3::4]], [deep[:, ::2, :3], deep[:, 1::2], deep[:, ::2, 3:]],
+                  [a[:, 1:3], a.view(torch.bfloat16)[:, 6:8]]):
+        with pytest.raises(ValueError, match="GPU"):
+            S.clip_grads(views, 1.0)
+    for g, out in ((a[:, ::2], a[:, ::2]), (a[:, ::2], a[:, 1::2]), (a.t(), a.t())):
+        with pytest.raises(ValueError, match="GPU"):
+            S.clip_grads([g], 1.0, out=[out])
+
+
+def places(t):
+    """Byte addresses of t's elements."""
+    at = {t.data_ptr()}
+    for n, s in zip(t.shape, t.stride()):
+        at = {p + i * s * t.element_size() for p in at for i in range(n)} if n else set()
+    return {p + b for p in at for b in range(t.element_size())}
+
+
+def test_overlap_of_random_views_against_all_their_bytes():
+    r = random.Random(3)
+    flat = torch.zeros(400)
+    found = 0
+    for _ in range(12000):
+        views = []
+        for _ in range(r.randint(2, 4)):
+            base = flat.view(torch.bfloat16) if r.random() < 0.4 else flat
+            while True:
+                shape = [r.randint(1, 5) for _ in range(r.randint(0, 3))]
+                stride = [r.choice([1, 2, 3, 4, 6, 8, 12, 20, 24, 40]) for _ in shape]
+                span = sum((n - 1) * s for n, s in zip(shape, stride)) + 1
+                if span <= 100:
+                    break
+            views.append(base.as_strided(shape, stride, r.randint(0, 260 - span)))
+        if not all(map(ops._apart, views)):
+            continue
+        seen = [places(v) for v in views]
+        want = any(seen[i] & seen[j] for i in range(len(views)) for j in range(i))
+        found += want
+        assert (ops._overlap(views) is not None) == want, [(v.data_ptr(), v.shape, v.stride(), v.dtype) for v in views]
+    assert found > 500
