@@ -663,7 +663,8 @@ int swiglu_grad_norm(int64_t count, const int* dtypes, const void* const* grads,
  * gradients are not written), or to outs[i], dense tensors of the gradients'
  * types and sizes (a HOST array; outs[i] may be grads[i]).  A norm that is NaN
  * makes every gradient NaN; an infinite one makes finite elements 0 and
- * infinite ones NaN.
+ * infinite ones NaN, unless max_norm is infinite too: an infinite limit clips
+ * nothing (f = 1), and so does a norm + eps of 0.
  * What is written must not overlap anything else that is read or written
  * (a tensor given twice, say): SWIGLU_ERR_ARG.  max_norm and eps at least 0
  * and not NaN, eps finite, else SWIGLU_ERR_ARG. */

@@ -191,8 +191,11 @@ __global__ __launch_bounds__(kTotalThreads) void total_kernel(const double* part
     const double r = sqrt(all);
     *norm = (float)r;
     if (factor != nullptr) {
-      const double f = max_norm / (r + eps);
-      *factor = f > 1.0 ? 1.0f : (float)f;                // a NaN stays one
+      // No quotient where the limit is infinite (nothing is clipped, also at an
+      // infinite norm) or r + eps is 0 (only zeros there); a NaN stays one.
+      const bool none = (__builtin_isinf(max_norm) || r + eps == 0.0) && r == r;
+      const double f = none ? 1.0 : max_norm / (r + eps);
+      *factor = f > 1.0 ? 1.0f : (float)f;
     }
   }
 }

@@ -809,7 +809,8 @@ inline int validate_grads(int64_t count, const int* dtypes, const void* const* g
     const uintptr_t es = (uintptr_t)elem_size(dtypes[i]);
     if (!aligned(grads[i], es) || (outs != nullptr && !aligned(outs[i], es))) return SWIGLU_ERR_ALIGN;
   }
-  // max_norm and eps at least 0 and not NaN; an infinite max_norm clips nothing.
+  // max_norm and eps at least 0 and not NaN; an infinite max_norm clips nothing
+  // (the factor is 1 whatever the norm, but for NaN).
   if (clip && (!(max_norm >= 0.0) || !(eps >= 0.0) || eps - eps != 0.0)) return SWIGLU_ERR_ARG;
   if ((st = check_int(norm))) return st;
   if (ws == nullptr || ws_bytes < grad_norm_workspace_total(count)) return SWIGLU_ERR_WORKSPACE;

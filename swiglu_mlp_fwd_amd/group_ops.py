@@ -715,8 +715,9 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, workspace: t
 
     In place, or into the tensors `out` of the same shapes and types (out[i] may be grads[i]).  fp32 and bf16 may be
     mixed; tensors that overlap each other or are given twice are refused.  A norm that is NaN makes every gradient
-    NaN; an infinite one makes finite elements 0 and infinite ones NaN.  `workspace` may pass a uint8 device buffer of
-    at least grad_norm_workspace_bytes(len(grads)) bytes (a smaller or missing one is replaced)."""
+    NaN; an infinite one makes finite elements 0 and infinite ones NaN.  An infinite max_norm clips nothing (but NaN
+    norms), and a norm + eps of 0 leaves the zeros.  `workspace` may pass a uint8 device buffer of at least
+    grad_norm_workspace_bytes(len(grads)) bytes (a smaller or missing one is replaced)."""
     grads = _grad_list(grads)
     codes, dev = _grad_codes(grads)
     max_norm, eps = float(max_norm), float(eps)

@@ -38,3 +38,23 @@ def test_clip_refuses_strided_gradients_that_overlap():
     got = S.clip_grads([even, odd], 0.5)
     assert abs(got.item() - norm) <= 2 * U32 * norm
     within(a, f * host(keep), 3 * U32 * np.abs(host(keep)), "interleaved columns")
+
+
+@pytest.mark.parametrize("into", [False, True])
+def test_clip_limits_without_a_quotient(into):
+    """An infinite limit clips nothing, whatever the norm; a norm and eps of zero leave the zeros that there are."""
+    def clip(g, limit, **kw):
+        out = [torch.full_like(t, 7.0) for t in g] if into else None
+        norm = S.clip_grads(g, limit, out=out, **kw)
+        return norm.item(), out if into else g
+    vals = [torch.tensor([3.0, -math.inf, 0.5], device=DEV), torch.tensor([1.5, -2.0], device=DEV, dtype=torch.bfloat16)]
+    norm, got = clip([t.clone() for t in vals], math.inf)
+    assert norm == math.inf and all(torch.equal(a, b) for a, b in zip(got, vals))
+    zeros = [torch.zeros(9, device=DEV), torch.zeros(5, device=DEV, dtype=torch.bfloat16)]
+    for limit in (0.0, 1.0, math.inf):
+        norm, got = clip([t.clone() for t in zeros], limit, eps=0.0)
+        assert norm == 0.0 and all((t == 0).all() for t in got), limit
+    norm, got = clip([torch.tensor([math.nan, 1.0], device=DEV)], math.inf)
+    assert math.isnan(norm) and torch.isnan(got[0]).all()                # a step that went wrong stays visible
+    norm, got = clip([torch.tensor([3.0, 4.0], device=DEV)], 0.0, eps=0.0)
+    assert norm == 5.0 and (got[0] == 0).all()
