@@ -759,7 +759,11 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, workspace: t
     _call("swiglu_clip_grads", norm, len(grads), _addr(codes), _addr(at), _addr(n), _addr(dst), max_norm, eps, _p(norm),
           _p(ws), size)
     for t, c in back:
-        t.copy_(c)
+        if t.is_inference():                     # written in that mode only
+            with torch.inference_mode():
+                t.copy_(c)
+        else:
+            t.copy_(c)
     try:
         torch.autograd.graph.increment_version(written)
     except RuntimeError:                         # tensors made in inference mode count no versions

@@ -58,3 +58,17 @@ def test_clip_limits_without_a_quotient(into):
     assert math.isnan(norm) and torch.isnan(got[0]).all()                # a step that went wrong stays visible
     norm, got = clip([torch.tensor([3.0, 4.0], device=DEV)], 0.0, eps=0.0)
     assert norm == 5.0 and (got[0] == 0).all()
+
+
+@pytest.mark.parametrize("into", [False, True])
+def test_clip_of_strided_inference_tensors(into):
+    """Made in inference mode, clipped outside of it, not contiguous."""
+    with torch.inference_mode():
+        a, o = torch.full((4, 6), 2.0, device=DEV), torch.zeros((4, 6), device=DEV)
+        g, t = a[:, ::2], o[:, ::2]
+    plain = torch.full((3,), 2.0, device=DEV)
+    S.clip_grads([g, plain], 1.0, eps=0.0, out=[t, plain] if into else None)
+    w = 2 / math.sqrt(4 * 15)
+    for v in (t if into else g, plain):
+        assert (v - w).abs().max().item() <= 2 * U32 * w
+    assert (a[:, 1::2] == 2).all() and (o[:, 1::2] == 0).all() and (not into or (a == 2).all())
