@@ -665,8 +665,8 @@ int swiglu_grad_norm(int64_t count, const int* dtypes, const void* const* grads,
  * makes every gradient NaN; an infinite one makes finite elements 0 and
  * infinite ones NaN, unless max_norm is infinite too: an infinite limit clips
  * nothing (f = 1), and so does a norm + eps of 0.
- * What is written must not overlap anything else that is read or written
- * (a tensor given twice, say): SWIGLU_ERR_ARG.  max_norm and eps at least 0
+ * What is written (norm and the workspace too) must not overlap anything else
+ * that is read or written (a tensor given twice, say): SWIGLU_ERR_ARG.  max_norm and eps at least 0
  * and not NaN, eps finite, else SWIGLU_ERR_ARG. */
 int swiglu_clip_grads(int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes,
                       void* const* outs, double max_norm, double eps, float* norm, void* workspace,

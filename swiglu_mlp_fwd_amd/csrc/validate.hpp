@@ -763,13 +763,14 @@ inline size_t grad_norm_workspace_total(int64_t count) {
 
 struct ByteRange { uintptr_t first, end; };
 
-// Whether two of the ranges written to overlap, or one that is written
-// overlaps one that is read for another tensor (or its own, but for the same).
+// Whether two of the ranges written to overlap (also: others that are written),
+// or one that is written overlaps one that is read for another tensor (or its
+// own, but for the same).
 inline int check_disjoint(int64_t count, const int* dtypes, const void* const* grads, const int64_t* sizes,
-                          void* const* outs) {
+                          void* const* outs, std::initializer_list<ByteRange> also = {}) {
   try {
-    std::vector<ByteRange> w;
-    w.reserve((size_t)count);
+    std::vector<ByteRange> w(also);
+    w.reserve((size_t)count + also.size());
     auto range = [&](const void* p, int64_t i) {
       const uintptr_t a = reinterpret_cast<uintptr_t>(p);
       return ByteRange{a, a + (uintptr_t)(sizes[i] * elem_size(dtypes[i]))};
@@ -815,7 +816,13 @@ inline int validate_grads(int64_t count, const int* dtypes, const void* const* g
   if ((st = check_int(norm))) return st;
   if (ws == nullptr || ws_bytes < grad_norm_workspace_total(count)) return SWIGLU_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return SWIGLU_ERR_ALIGN;
-  return clip ? check_disjoint(count, dtypes, grads, sizes, outs) : SWIGLU_OK;
+  if (!clip) return SWIGLU_OK;
+  auto bytes = [](const void* p, size_t n) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return ByteRange{a, a + n};
+  };
+  return check_disjoint(count, dtypes, grads, sizes, outs,
+                        {bytes(norm, sizeof(float)), bytes(ws, grad_norm_workspace_total(count))});
 }
 
 }  // namespace swg

@@ -6,6 +6,8 @@ import torch
 
 import swiglu_mlp_fwd_amd as S
 import swiglu_mlp_fwd_amd.group_ops as ops
+from test_abi_host import A, EARG, L  # noqa: F401
+from test_group_host import at, grads
 
 
 # ------------------------------------------------- how a tensor's elements lie
@@ -92,3 +94,20 @@ def test_overlap_of_random_views_against_all_their_bytes():
         found += want
         assert (ops._overlap(views) is not None) == want, [(v.data_ptr(), v.shape, v.stride(), v.dtype) for v in views]
     assert found > 500
+
+
+def test_norm_and_workspace_inside_a_gradient_are_refused(L):  # noqa: F811
+    """They are written too.  (Refused on the host: no address is read.)"""
+    far, ws = A + (1 << 24), A + (1 << 25)
+    n = L.swiglu_grad_norm_workspace_bytes(2)
+
+    def clip(norm=far, ws=ws, outs=None):
+        d, p, s = grads((0, A, 1000), (1, A + 8192, 1000))
+        o = None if outs is None else grads(*((0, a, 0) for a in outs))[1]
+        return L.swiglu_clip_grads(2, at(d), at(p), at(s), at(o), 1.0, 1e-6, norm, ws, n, None)
+    for norm in (A, A + 3996, A + 8192, A + 8192 + 1996):
+        assert clip(norm=norm) == EARG, norm - A
+        assert clip(norm=norm, outs=(A + 65536, A + 131072)) == EARG, norm - A
+    for w in (A, A + 8192 + 1792, A - n + 256):
+        assert clip(ws=w) == EARG, w - A
+    assert clip(norm=ws + n - 4) == EARG and clip(norm=A + 65536, outs=(A + 65536, A + 131072)) == EARG
