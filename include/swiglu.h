@@ -596,8 +596,10 @@ int swiglu_grouped_fwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int6
                        const void* wu, int64_t wu_stride, void* h, void* stream);
 
 /* Bytes of device workspace swiglu_grouped_bwd needs, with src or without
- * (gathered; 0 for sizes it rejects). */
+ * (gathered; 0 for sizes it rejects): with any number of experts, or, often
+ * less, with E of them. */
 size_t swiglu_grouped_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, int64_t K, int gathered);
+size_t swiglu_grouped_bwd_workspace_bytes_of(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, int gathered);
 
 /* Gradients of swiglu_grouped_fwd, g and u computed again (as swiglu_bwd):
  *   du = dh * act(g),  dg = dh * u * act'(g)       (rounded to dtype)
@@ -609,9 +611,10 @@ size_t swiglu_grouped_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, int64
  *
  *   dh           [R, N];  dx [R, K], or NULL if it is not wanted
  *   dwg, dwu     [E, N, K] dense outputs, or both NULL
- *   workspace    at least swiglu_grouped_bwd_workspace_bytes(...) bytes,
+ *   workspace    at least swiglu_grouped_bwd_workspace_bytes_of(...) bytes,
  *                256-byte aligned; scratch (calls that overlap need one each)
- * Errors as the forward's; one of dwg, dwu alone: SWIGLU_ERR_ARG. */
+ * Errors as the forward's, with src also swiglu_expert_gather's limits of size
+ * (the rows are gathered); one of dwg, dwu alone: SWIGLU_ERR_ARG. */
 int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
                        int64_t k, const int32_t* src, const int32_t* offsets, const void* wg, int64_t wg_stride,
                        const void* wu, int64_t wu_stride, const void* dh, void* dx, void* dwg, void* dwu,
@@ -626,13 +629,14 @@ int swiglu_grouped_mm(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, con
                       const void* w, int64_t w_stride, void* y, void* stream);
 
 /* Bytes of device workspace swiglu_grouped_mm_bwd needs (0 for sizes it rejects,
- * and for those that need none). */
+ * and for those that need none): with any number of experts, or with E. */
 size_t swiglu_grouped_mm_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, int64_t K);
+size_t swiglu_grouped_mm_bwd_workspace_bytes_of(int dtype, int64_t R, int64_t E, int64_t N, int64_t K);
 
 /* Gradients of swiglu_grouped_mm: dx[r] = dy[r] W_e [R, K] (0 for rows of no
  * expert), dw[e] = sum over the expert's rows of dy[r]^T x[r], [E, N, K] dense
  * (0 without rows).  dx or dw may be NULL; x is read for dw only, w for dx.
- *   workspace    at least swiglu_grouped_mm_bwd_workspace_bytes(...) bytes,
+ *   workspace    at least swiglu_grouped_mm_bwd_workspace_bytes_of(...) bytes,
  *                256-byte aligned (NULL where none is needed); scratch
  *                (calls that overlap need one each) */
 int swiglu_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x,

@@ -93,12 +93,15 @@ SIGNATURES = {
     "swiglu_grouped_fwd": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_i64,
                                           _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr]),
     "swiglu_grouped_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _c_i64, _c_i64, _c_i64, ctypes.c_int]),
+    "swiglu_grouped_bwd_workspace_bytes_of": (ctypes.c_size_t, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64,
+                                                                ctypes.c_int]),
     "swiglu_grouped_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_i64,
                                           _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64, _c_ptr, _c_i64, _c_ptr, _c_ptr,
                                           _c_ptr, _c_ptr, _c_ptr, ctypes.c_size_t, _c_ptr]),
     "swiglu_grouped_mm": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_i64,
                                          _c_ptr, _c_ptr]),
     "swiglu_grouped_mm_bwd_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _c_i64, _c_i64, _c_i64]),
+    "swiglu_grouped_mm_bwd_workspace_bytes_of": (ctypes.c_size_t, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64]),
     "swiglu_grouped_mm_bwd": (ctypes.c_int, [ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_ptr, _c_ptr, _c_ptr,
                                              _c_i64, _c_ptr, _c_ptr, _c_ptr, _c_ptr, ctypes.c_size_t, _c_ptr]),
     "swiglu_grad_norm_workspace_bytes": (ctypes.c_size_t, [_c_i64]),

@@ -467,6 +467,10 @@ size_t swiglu_grouped_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, int64
   return swg::grouped_bwd_workspace_total(dtype, R, N, K, gathered != 0);
 }
 
+size_t swiglu_grouped_bwd_workspace_bytes_of(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, int gathered) {
+  return swg::grouped_bwd_workspace_of(dtype, R, E, N, K, gathered != 0);
+}
+
 int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
                        int64_t k, const int32_t* src, const int32_t* offsets, const void* wg, int64_t wg_stride,
                        const void* wu, int64_t wu_stride, const void* dh, void* dx, void* dwg, void* dwu,
@@ -483,7 +487,7 @@ int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int6
   if (R > 0 && N > 0) {
     if (src != nullptr) {
       // x's rows in order: the weights' gradients read them along the reduction.
-      void* xr = ws + swg::grouped_bwd_layout(dtype, R, N, K, true).off_x;
+      void* xr = ws + swg::grouped_bwd_layout(dtype, R, E, N, K, true).off_x;
       if ((e = swg::launch_gather(dt, (int)T, (int)k, (int)K, x, src, xr, s)) != hipSuccess) return hip_status(e);
       rows = xr;
     }
@@ -505,7 +509,7 @@ int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int6
     g.n = (int)K; g.r = (int)N; g.halves = 2;
     g.out0 = dx; g.ldo = K;
     g.parts = swg::split_parts(dtype, R, E, K, N, 2);
-    g.part = reinterpret_cast<float*>(ws + swg::grouped_bwd_layout(dtype, R, N, K, src != nullptr).off_part);
+    g.part = reinterpret_cast<float*>(ws + swg::grouped_bwd_layout(dtype, R, E, N, K, src != nullptr).off_part);
     if ((e = swg::launch_grouped_nn(dt, g, s)) != hipSuccess) return hip_status(e);
   }
   // 3. dWg = dg^T x, dWu = du^T x, reducing over each expert's rows.
@@ -517,7 +521,7 @@ int swiglu_grouped_bwd(int act, int dtype, int64_t R, int64_t E, int64_t N, int6
     g.m = (int)N; g.n = (int)K; g.halves = 2;
     g.out0 = dwg; g.out1 = dwu; g.ldo = K;
     g.parts = swg::split_row_parts(dtype, R, E, N, K, 2);
-    g.part = reinterpret_cast<float*>(ws + swg::grouped_bwd_layout(dtype, R, N, K, src != nullptr).off_part);
+    g.part = reinterpret_cast<float*>(ws + swg::grouped_bwd_layout(dtype, R, E, N, K, src != nullptr).off_part);
     if ((e = swg::launch_grouped_tn(dt, g, s)) != hipSuccess) return hip_status(e);
   }
   return SWIGLU_OK;
@@ -540,12 +544,16 @@ size_t swiglu_grouped_mm_bwd_workspace_bytes(int dtype, int64_t R, int64_t N, in
   return swg::grouped_mm_bwd_workspace_total(dtype, R, N, K);
 }
 
+size_t swiglu_grouped_mm_bwd_workspace_bytes_of(int dtype, int64_t R, int64_t E, int64_t N, int64_t K) {
+  return swg::grouped_mm_bwd_workspace_of(dtype, R, E, N, K);
+}
+
 int swiglu_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x,
                           const int32_t* offsets, const void* w, int64_t w_stride, const void* dy, void* dx, void* dw,
                           void* workspace, size_t workspace_bytes, void* stream) {
   int st = swg::validate_grouped_mm_bwd(dtype, R, E, N, K, x, offsets, w, w_stride, dy, dx, dw);
   if (st != SWIGLU_OK || K == 0) return st;
-  st = swg::validate_grouped_mm_bwd_workspace(dtype, R, N, K, workspace, workspace_bytes);
+  st = swg::validate_grouped_mm_bwd_workspace(dtype, R, E, N, K, workspace, workspace_bytes);
   if (st != SWIGLU_OK) return st;
   const swg::Dt dt = as_dt(dtype);
   hipError_t e = hipSuccess;

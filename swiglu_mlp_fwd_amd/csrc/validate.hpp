@@ -654,26 +654,39 @@ inline size_t split_row_bytes(int dtype, int64_t R, int64_t m, int64_t n, int ha
   const int64_t p = parts < steps ? parts : steps;
   return p < 2 ? 0 : (size_t)round_up(p * halves * m * n * 4, 256);
 }
-// Both gradients' sums use the same workspace, one after the other.
-inline size_t split_grads_bytes(int dtype, int64_t R, int64_t N, int64_t K, int halves) {
-  const size_t x = split_bytes(dtype, R, K, N, halves), w = split_row_bytes(dtype, R, N, K, halves);
+// Both gradients' sums use the same workspace, one after the other: what a call
+// with E experts needs, or (E = 0) with any number of them.  64 experts of (1024,
+// 2048), 32768 rows: none, for any number 67 MB.
+inline size_t split_grads_bytes(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, int halves) {
+  size_t x, w;
+  if (E == 0) {
+    x = split_bytes(dtype, R, K, N, halves);
+    w = split_row_bytes(dtype, R, N, K, halves);
+  } else {
+    const int64_t px = split_parts(dtype, R, E, K, N, halves), pw = split_row_parts(dtype, R, E, N, K, halves);
+    x = px > 1 ? (size_t)round_up(px * R * K * 4, 256) : 0;
+    w = pw > 1 ? (size_t)round_up(pw * E * halves * N * K * 4, 256) : 0;
+  }
   return x > w ? x : w;
 }
 
 // Workspace of the grouped backward, regions on 256-byte boundaries: D =
 // [dg | du], [R, 2 N], the gathered rows of x, [R, K], and the parts' sums of
-// split gradients.
+// split gradients (of E experts; E = 0: of any number).
 struct GroupedBwdLayout { size_t off_x, off_part, total; };
-inline GroupedBwdLayout grouped_bwd_layout(int dtype, int64_t R, int64_t N, int64_t K, bool gathered) {
+inline GroupedBwdLayout grouped_bwd_layout(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, bool gathered) {
   GroupedBwdLayout L;
   const size_t es = (size_t)elem_size(dtype);
   L.off_x = (size_t)round_up((int64_t)(R * 2 * N * es), 256);
   L.off_part = L.off_x + (gathered ? (size_t)round_up((int64_t)(R * K * es), 256) : 0);
-  L.total = L.off_part + split_grads_bytes(dtype, R, N, K, 2);
+  L.total = L.off_part + split_grads_bytes(dtype, R, E, N, K, 2);
   return L;
 }
 inline size_t grouped_bwd_workspace_total(int dtype, int64_t R, int64_t N, int64_t K, bool gathered) {
-  return grouped_shape_status(dtype, R, 1, N, K) == SWIGLU_OK ? grouped_bwd_layout(dtype, R, N, K, gathered).total : 0;
+  return grouped_shape_status(dtype, R, 1, N, K) == SWIGLU_OK ? grouped_bwd_layout(dtype, R, 0, N, K, gathered).total : 0;
+}
+inline size_t grouped_bwd_workspace_of(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, bool gathered) {
+  return grouped_shape_status(dtype, R, E, N, K) == SWIGLU_OK ? grouped_bwd_layout(dtype, R, E, N, K, gathered).total : 0;
 }
 
 inline int validate_grouped_bwd(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* x, int64_t T,
@@ -700,7 +713,7 @@ inline int validate_grouped_bwd(int dtype, int64_t R, int64_t E, int64_t N, int6
     if ((st = check_ptr(p))) return st;
   if (ws == nullptr) return SWIGLU_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return SWIGLU_ERR_ALIGN;
-  if (ws_bytes < grouped_bwd_layout(dtype, R, N, K, src != nullptr).total) return SWIGLU_ERR_WORKSPACE;
+  if (ws_bytes < grouped_bwd_layout(dtype, R, E, N, K, src != nullptr).total) return SWIGLU_ERR_WORKSPACE;
   return SWIGLU_OK;
 }
 
@@ -734,11 +747,14 @@ inline int validate_grouped_mm_bwd(int dtype, int64_t R, int64_t E, int64_t N, i
 }
 
 inline size_t grouped_mm_bwd_workspace_total(int dtype, int64_t R, int64_t N, int64_t K) {
-  return grouped_shape_status(dtype, R, 1, N, K) == SWIGLU_OK ? split_grads_bytes(dtype, R, N, K, 1) : 0;
+  return grouped_shape_status(dtype, R, 1, N, K) == SWIGLU_OK ? split_grads_bytes(dtype, R, 0, N, K, 1) : 0;
 }
-inline int validate_grouped_mm_bwd_workspace(int dtype, int64_t R, int64_t N, int64_t K, const void* ws,
+inline size_t grouped_mm_bwd_workspace_of(int dtype, int64_t R, int64_t E, int64_t N, int64_t K) {
+  return grouped_shape_status(dtype, R, E, N, K) == SWIGLU_OK ? split_grads_bytes(dtype, R, E, N, K, 1) : 0;
+}
+inline int validate_grouped_mm_bwd_workspace(int dtype, int64_t R, int64_t E, int64_t N, int64_t K, const void* ws,
                                              size_t ws_bytes) {
-  const size_t need = grouped_mm_bwd_workspace_total(dtype, R, N, K);
+  const size_t need = grouped_mm_bwd_workspace_of(dtype, R, E, N, K);
   if (need == 0) return SWIGLU_OK;
   if (ws == nullptr || ws_bytes < need) return SWIGLU_ERR_WORKSPACE;
   return aligned(ws, 256) ? SWIGLU_OK : SWIGLU_ERR_ALIGN;

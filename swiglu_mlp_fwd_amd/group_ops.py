@@ -270,11 +270,15 @@ def grouped_fwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, offsets: to
     return h
 
 
-def grouped_bwd_workspace_bytes(dtype: torch.dtype, R: int, N: int, K: int, gathered: bool = False) -> int:
-    """Bytes of workspace of grouped_bwd, with src (gathered) or without."""
+def grouped_bwd_workspace_bytes(dtype: torch.dtype, R: int, N: int, K: int, gathered: bool = False,
+                                E: int | None = None) -> int:
+    """Bytes of workspace of grouped_bwd, with src (gathered) or without: for E experts, which often take less, or for
+    any number of them."""
     if dtype not in _DT:
         raise TypeError(f"libswiglu supports bfloat16 and float32, got {dtype}")
-    return int(lib().swiglu_grouped_bwd_workspace_bytes(_DT[dtype], R, N, K, int(gathered)))
+    if E is None:
+        return int(lib().swiglu_grouped_bwd_workspace_bytes(_DT[dtype], R, N, K, int(gathered)))
+    return int(lib().swiglu_grouped_bwd_workspace_bytes_of(_DT[dtype], R, E, N, K, int(gathered)))
 
 
 def grouped_bwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, dh: torch.Tensor, offsets: torch.Tensor,
@@ -315,8 +319,8 @@ def grouped_bwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, dh: torch.T
             return torch.empty(shape, dtype=x.dtype, device=x.device) if need else None
         out = (new(need_dx, R, K), new(need_dw, E, N, K), new(need_dw, E, N, K))
     dx, dwg, dwu = out
-    ws, n = _workspace(workspace, int(lib().swiglu_grouped_bwd_workspace_bytes(dt, R, N, K, int(src is not None))),
-                       x.device)
+    need = int(lib().swiglu_grouped_bwd_workspace_bytes_of(dt, R, E, N, K, int(src is not None)))
+    ws, n = _workspace(workspace, need, x.device)
     _call("swiglu_grouped_bwd", x, code, dt, R, E, N, K, _p(x2), T, k, _p(src), _p(offsets), _p(wg), sg, _p(wu), su,
           _p(d2), _p(dx), _p(dwg), _p(dwu), _p(ws), n)
     return dx, dwg, dwu
@@ -344,11 +348,13 @@ def grouped_mm(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, out: tor
     return y
 
 
-def grouped_mm_bwd_workspace_bytes(dtype: torch.dtype, R: int, N: int, K: int) -> int:
-    """Bytes of workspace of grouped_mm_bwd (0: none is needed)."""
+def grouped_mm_bwd_workspace_bytes(dtype: torch.dtype, R: int, N: int, K: int, E: int | None = None) -> int:
+    """Bytes of workspace of grouped_mm_bwd (0: none is needed), for E experts or for any number of them."""
     if dtype not in _DT:
         raise TypeError(f"libswiglu supports bfloat16 and float32, got {dtype}")
-    return int(lib().swiglu_grouped_mm_bwd_workspace_bytes(_DT[dtype], R, N, K))
+    if E is None:
+        return int(lib().swiglu_grouped_mm_bwd_workspace_bytes(_DT[dtype], R, N, K))
+    return int(lib().swiglu_grouped_mm_bwd_workspace_bytes_of(_DT[dtype], R, E, N, K))
 
 
 def grouped_mm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, offsets: torch.Tensor, out=None,
@@ -381,7 +387,7 @@ def grouped_mm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, offsets: 
         out = (torch.empty((R, K), dtype=x.dtype, device=x.device) if need_dx else None,
                torch.empty((E, N, K), dtype=x.dtype, device=x.device) if need_dw else None)
     dx, dw = out
-    ws, n = _workspace(workspace, int(lib().swiglu_grouped_mm_bwd_workspace_bytes(dt, R, N, K)), x.device)
+    ws, n = _workspace(workspace, int(lib().swiglu_grouped_mm_bwd_workspace_bytes_of(dt, R, E, N, K)), x.device)
     _call("swiglu_grouped_mm_bwd", x, dt, R, E, N, K, _p(x2), _p(offsets), _p(w), sw, _p(d2), _p(dx), _p(dw), _p(ws), n)
     return dx, dw
 

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from oracle import group_oracle as G
-from parity_util import U32
+from parity_util import U32, check_guards, guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -18,7 +18,7 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
 import swiglu_mlp_fwd_amd as S  # noqa: E402
-from test_gpu_group import DEV, host, normal, within  # noqa: E402
+from test_gpu_group import DEV, DT, host, normal, offsets_of, within  # noqa: E402
 
 
 # ------------------------------------------------------------------ clipping
@@ -72,3 +72,28 @@ def test_clip_of_strided_inference_tensors(into):
     for v in (t if into else g, plain):
         assert (v - w).abs().max().item() <= 2 * U32 * w
     assert (a[:, 1::2] == 2).all() and (o[:, 1::2] == 0).all() and (not into or (a == 2).all())
+
+
+# ------------------------------------------------------------------ workspace
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,N,K", [([3], 13448, 248), ([40] * 5, 1600, 1744), ([3000], 152, 320), ([2000, 40, 2500, 2000], 264, 72),
+                                        ([90] * 40, 136, 264)])
+def test_gradients_stay_inside_the_workspace_of_their_experts(dt, counts, N, K):
+    """Reductions split or not: exactly the bytes asked for, guarded, give the bits that more of them give."""
+    offsets, R, E = offsets_of(counts), sum(counts), len(counts)
+    x, dy = normal((R, K), 1, dt), normal((R, N), 2, dt)
+    wg, wu = normal((E, N, K), 3, dt, K ** -0.5), normal((E, N, K), 4, dt, K ** -0.5)
+    src = torch.arange(R, dtype=torch.int32, device=DEV)
+    for what, need, call in (
+            ("mm", S.grouped_mm_bwd_workspace_bytes(DT[dt], R, N, K, E=E), lambda ws: S.grouped_mm_bwd(x, wg, dy, offsets, workspace=ws)),
+            ("gate/up", S.grouped_bwd_workspace_bytes(DT[dt], R, N, K, E=E), lambda ws: S.grouped_bwd(x, wg, wu, dy, offsets, workspace=ws)),
+            ("gathered", S.grouped_bwd_workspace_bytes(DT[dt], R, N, K, gathered=True, E=E),
+             lambda ws: S.grouped_bwd(x, wg, wu, dy, offsets, src=src, workspace=ws))):
+        if need == 0:
+            continue
+        ws = guarded((need,), torch.uint8)
+        got = call(ws.t)
+        check_guards(what, ws)
+        for a, b in zip(got, call(torch.full((2 * need,), 0xFF, dtype=torch.uint8, device=DEV))):
+            assert torch.isfinite(a).all() and torch.equal(a, b), what

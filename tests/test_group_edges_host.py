@@ -6,8 +6,8 @@ import torch
 
 import swiglu_mlp_fwd_amd as S
 import swiglu_mlp_fwd_amd.group_ops as ops
-from test_abi_host import A, EARG, L  # noqa: F401
-from test_group_host import at, grads
+from test_abi_host import A, EALIGN, EARG, EWS, L  # noqa: F401
+from test_group_host import at, grads, grouped_calls
 
 
 # ------------------------------------------------- how a tensor's elements lie
@@ -111,3 +111,31 @@ def test_norm_and_workspace_inside_a_gradient_are_refused(L):  # noqa: F811
     for w in (A, A + 8192 + 1792, A - n + 256):
         assert clip(ws=w) == EARG, w - A
     assert clip(norm=ws + n - 4) == EARG and clip(norm=A + 65536, outs=(A + 65536, A + 131072)) == EARG
+
+
+# ------------------------------------------------------------------ workspace
+
+def test_gradients_ask_for_the_workspace_that_they_use(L):  # noqa: F811
+    """For E experts: parts' sums only where a gradient of so many is split; never more than for any number."""
+    fine = dict(R=32768, N=1024, K=2048)
+    D, rows = 32768 * 2 * 1024 * 2, 32768 * 2048 * 2
+    any_e, of = S.grouped_bwd_workspace_bytes, S.grouped_mm_bwd_workspace_bytes
+    assert any_e(torch.bfloat16, **fine, gathered=True, E=64) == D + rows
+    assert any_e(torch.bfloat16, **fine, gathered=True) == D + rows + (64 << 20)
+    assert any_e(torch.bfloat16, **fine, E=64) == D and of(torch.bfloat16, **fine, E=64) == 0 < of(torch.bfloat16, **fine)
+    fwd, bwd, mm, mm_bwd = grouped_calls(L)
+    sizes = dict(E=64, **fine, sg=1024 * 2048, su=1024 * 2048)
+    assert bwd(**sizes, n=D - 1) == EWS and bwd(**sizes, src=A, T=4096, k=8, n=D + rows - 1) == EWS
+    long = dict(E=3, R=64, N=4096, K=64, sw=4096 * 64)
+    for dt in (0, 1):
+        n = L.swiglu_grouped_mm_bwd_workspace_bytes_of(dt, 64, 3, 4096, 64)
+        assert 0 < n <= L.swiglu_grouped_mm_bwd_workspace_bytes(dt, 64, 4096, 64)
+        assert mm_bwd(dt=dt, n=n - 1, **long) == EWS and mm_bwd(dt=dt, n=n, ws=A + 128, **long) == EALIGN
+    for bad in ((2, 64, 3, 4096, 64), (1, -1, 3, 8, 8), (1, 64, 0, 8, 8), (1, 64, 1025, 8, 8), (1, 64, 3, 4, 8)):
+        assert L.swiglu_grouped_mm_bwd_workspace_bytes_of(*bad) == L.swiglu_grouped_bwd_workspace_bytes_of(*bad, 0) == 0
+    r = random.Random(1)
+    for _ in range(3000):
+        dt, E = r.randint(0, 1), r.choice([1, 2, 3, 8, 39, 64, 1024])
+        R, N, K = int(2 ** r.uniform(0, 20)), 8 * int(2 ** r.uniform(0, 11)), 8 * int(2 ** r.uniform(0, 11))
+        assert L.swiglu_grouped_bwd_workspace_bytes_of(dt, R, E, N, K, 0) <= L.swiglu_grouped_bwd_workspace_bytes(dt, R, N, K, 0) \
+            or L.swiglu_grouped_bwd_workspace_bytes(dt, R, N, K, 0) == 0
