@@ -805,16 +805,7 @@ void grouped_kernel(GroupedArgs p) {
   }
 }
 
-// Tiles of R rows in at most min(E + 2, R) groups that have any.
-template <class TL>
-int64_t row_column_tiles(const GroupedArgs& a) {
-  const int64_t groups = a.E + 2 < a.R ? a.E + 2 : a.R;
-  return (a.R / TL::kBM + groups) * (((int64_t)a.n + TL::kBN - 1) / TL::kBN);
-}
-// A launch has fewer than 2^32 threads; validation bounds the tiles of 128 x 64
-// and larger.
-template <class TL>
-bool fits(const GroupedArgs& a) { return row_column_tiles<TL>(a) * TL::kThreads < (int64_t(1) << 32); }
+template <class TL> constexpr RowTile kTileOf = {TL::kBM, TL::kBN, TL::kThreads};
 
 template <typename T, Form F, Out O, Act ACT, int NB, class TL, int kGroupM = 8>
 hipError_t launch(const GroupedArgs& a, hipStream_t s) {
@@ -823,7 +814,7 @@ hipError_t launch(const GroupedArgs& a, hipStream_t s) {
   if (F == Form::kTN) {
     tiles = 8 * (int64_t)a.E * ((a.halves * (((int64_t)a.m + TL::kBM - 1) / TL::kBM) * ntn + 7) / 8);
   } else {
-    tiles = row_column_tiles<TL>(a);
+    tiles = row_column_tiles(kTileOf<TL>, a.R, a.E, a.n);
   }
   if (tiles == 0) return hipSuccess;
   const size_t lds = (size_t)Ring<T, F, TL>::kDepth * (TL::kBM + NB * TL::kBN) * Ring<T, F, TL>::kChunks * 16;
@@ -877,55 +868,40 @@ using SingleF32 = Tile<128, 128, 2, 2, 2>;
 using DualF32Few = Tile<32, 64, 1, 2, 2>;
 using SingleF32Few = Tile<32, 64, 1, 2, 2>;
 
-// Row tiles of at most `bm` rows, times column tiles of `bn`.
-int64_t tiles_of(const GroupedArgs& a, int bm, int bn) {
-  const int64_t groups = a.E < a.R ? a.E : a.R;
-  return (a.R / bm + groups) * (((int64_t)a.n + bn - 1) / bn);
+// Which of a form's two tiles a call takes, and where its column tiles start, is
+// told in validate.hpp (row_tile, weights_bound); these are the tiles it names.
+template <class Large, class Few> constexpr bool kRuleNames(const TileRule& r) {
+  return r.large == kTileOf<Large> && r.few == kTileOf<Few>;
 }
-// bf16: small tiles where the large ones would leave many of the 256 CUs
-// without a workgroup, and up to so many rows per expert (rows drawn with a
-// spread of a half, logarithmic):
-// gate/up 64, of 64 x (1024, 2048) with 32 rows each 115 us with large tiles,
-// 104 with small, with 64 152 and 112, with 128 160 and 161; of 8 x (14336, 4096)
-// with 32 365 and 328, with 64 410 and 376, with 96 406 and 471;
-// the down product 32, of 64 x (2048, 1024) with 16 rows each 57 and 52, with 32
-// 59 and 59; of 8 x (6912, 1536) 40 and 36, 43 and 36, with 64 43 and 47; of
-// 8 x (4096, 2048) with 64 (160 large tiles) 51 and 33, with 128 53 and 45;
-// dx 16, of 64 x (1024, 2048) with 16 rows each 63 and 51, with 32 66 and 70.
-// (One workgroup to a CU, twice the columns and a ring of four took as long
-// for the same number of tiles but more where a last round is nearly empty:
-// 114 for the first of these.)
-bool few_bf16(const GroupedArgs& a, int bn, int rows) {
-  return a.R <= (int64_t)rows * a.E || tiles_of(a, 256, bn) <= 176;
+static_assert(kRuleNames<Dual, DualFew>(tile_rule(SWIGLU_BF16, RowForm::kGated)) &&
+              kRuleNames<Dual, Dual>(tile_rule(SWIGLU_BF16, RowForm::kRecompute)) &&
+              kRuleNames<Single, SingleFewNT>(tile_rule(SWIGLU_BF16, RowForm::kNT)) &&
+              kRuleNames<Single, SingleFew>(tile_rule(SWIGLU_BF16, RowForm::kNN)) &&
+              kRuleNames<DualF32, DualF32Few>(tile_rule(SWIGLU_F32, RowForm::kGated)) &&
+              kRuleNames<DualF32, DualF32Few>(tile_rule(SWIGLU_F32, RowForm::kRecompute)) &&
+              kRuleNames<SingleF32, SingleF32Few>(tile_rule(SWIGLU_F32, RowForm::kNT)) &&
+              kRuleNames<SingleF32, SingleF32Few>(tile_rule(SWIGLU_F32, RowForm::kNN)), "the tiles of the rules");
+bool takes_few(Dt dt, RowForm form, const GroupedArgs& a) {
+  const int code = dt == Dt::kBF16 ? SWIGLU_BF16 : SWIGLU_F32;
+  return row_tile(code, form, a.R, a.E, a.n) == tile_rule(code, form).few;
 }
-// Column tiles start apart up to 256 rows per expert, where the weights' stream
-// bounds the product.  64 x (1024, 2048) with 32 rows each, gate/up 123 us from
-// the same place, 95 apart, with 128 146 and 136; 8 x (14336, 4096) with 128 470
-// and 446; fp32, 16 x (4096, 1024) with 16 160 and 128, from 32 on the same.
-// With 512 it costs as much (bf16, 8 x (4096, 2048): 167 and 168) or more, since
-// column tiles share rows of x.
-bool weights_bound(const GroupedArgs& a) { return a.R <= (int64_t)256 * a.E; }
-// fp32, whose tiles are bound by the matrix cores: tiles of 32 rows up to 128
-// rows per expert, and where the large ones are fewer than the CUs.  64
-// experts of (1024, 2048), gate/up: 16 rows each 484 us with large tiles, 208
-// with small, 128 862 and 701, 512 2222 and 2316; 5 of (200, 264): 23 and 14.
-bool few_f32(const GroupedArgs& a, int bn) { return a.R <= (int64_t)128 * a.E || tiles_of(a, 128, bn) <= 256; }
 
 template <Out O, Act A>
 hipError_t dual(Dt dt, GroupedArgs a, hipStream_t s) {
-  a.stagger = weights_bound(a);
+  constexpr RowForm kForm = O == Out::kGated ? RowForm::kGated : RowForm::kRecompute;
+  a.stagger = weights_bound(a.R, a.E);
   if (dt == Dt::kF32)
-    return few_f32(a, DualF32::kBN) && fits<DualF32Few>(a) ? launch<float, Form::kNT, O, A, 2, DualF32Few>(a, s)
-                                    : launch<float, Form::kNT, O, A, 2, DualF32>(a, s);
-  // (The small tile's ring has no room for the recompute's dh tile.)
+    return takes_few(dt, kForm, a) ? launch<float, Form::kNT, O, A, 2, DualF32Few>(a, s)
+                                   : launch<float, Form::kNT, O, A, 2, DualF32>(a, s);
   if constexpr (O == Out::kGated)
-    if (few_bf16(a, Dual::kBN, 64) && fits<DualFew>(a)) return launch<bf16, Form::kNT, O, A, 2, DualFew>(a, s);
+    if (takes_few(dt, kForm, a)) return launch<bf16, Form::kNT, O, A, 2, DualFew>(a, s);
   return launch<bf16, Form::kNT, O, A, 2, Dual>(a, s);
 }
 
 template <Form F>
 hipError_t single(Dt dt, GroupedArgs a, hipStream_t s) {
-  a.stagger = F == Form::kNT && weights_bound(a);
+  constexpr RowForm kForm = F == Form::kNT ? RowForm::kNT : RowForm::kNN;
+  a.stagger = F == Form::kNT && weights_bound(a.R, a.E);
   using Few = std::conditional_t<F == Form::kNT, SingleFewNT, SingleFew>;
   if constexpr (F == Form::kNN) {
     static_assert(SingleFew::kBM == kSplitBf16.bm && SingleFew::kBN == kSplitBf16.bn && SingleF32Few::kBM == kSplitF32.bm &&
@@ -934,11 +910,10 @@ hipError_t single(Dt dt, GroupedArgs a, hipStream_t s) {
       return dt == Dt::kF32 ? launch_parts<float, F, SingleF32Few, 8>(a, s) : launch_parts<bf16, F, SingleFew, 4>(a, s);
   }
   if (dt == Dt::kF32)
-    return few_f32(a, SingleF32::kBN) && fits<SingleF32Few>(a) ? launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32Few>(a, s)
-                                      : launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32>(a, s);
-  return few_bf16(a, Single::kBN, F == Form::kNT ? 32 : 16) && fits<Few>(a)
-             ? launch<bf16, F, Out::kStore, Act::kSilu, 1, Few, 4>(a, s)
-             : launch<bf16, F, Out::kStore, Act::kSilu, 1, Single, 4>(a, s);
+    return takes_few(dt, kForm, a) ? launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32Few>(a, s)
+                                   : launch<float, F, Out::kStore, Act::kSilu, 1, SingleF32>(a, s);
+  return takes_few(dt, kForm, a) ? launch<bf16, F, Out::kStore, Act::kSilu, 1, Few, 4>(a, s)
+                                 : launch<bf16, F, Out::kStore, Act::kSilu, 1, Single, 4>(a, s);
 }
 
 }  // namespace

@@ -605,6 +605,65 @@ inline int validate_grouped_fwd(int dtype, int64_t R, int64_t E, int64_t N, int6
   return SWIGLU_OK;
 }
 
+// Which tile of rows and columns a product of rows takes.  bf16: the small one
+// where the large ones would leave many of the 256 CUs without a workgroup, and
+// up to so many rows per expert (rows drawn with a spread of a half,
+// logarithmic):
+// gate/up 64, of 64 x (1024, 2048) with 32 rows each 115 us with large tiles,
+// 104 with small, with 64 152 and 112, with 128 160 and 161; of 8 x (14336, 4096)
+// with 32 365 and 328, with 64 410 and 376, with 96 406 and 471;
+// the down product 32, of 64 x (2048, 1024) with 16 rows each 57 and 52, with 32
+// 59 and 59; of 8 x (6912, 1536) 40 and 36, 43 and 36, with 64 43 and 47; of
+// 8 x (4096, 2048) with 64 (160 large tiles) 51 and 33, with 128 53 and 45;
+// dx 16, of 64 x (1024, 2048) with 16 rows each 63 and 51, with 32 66 and 70.
+// (One workgroup to a CU, twice the columns and a ring of four took as long
+// for the same number of tiles but more where a last round is nearly empty:
+// 114 for the first of these.)  The recompute has the large one only: the small
+// tile's ring has no room for the dh tile.
+// fp32, whose tiles are bound by the matrix cores: tiles of 32 rows up to 128
+// rows per expert, and where the large ones are fewer than the CUs.  64
+// experts of (1024, 2048), gate/up: 16 rows each 484 us with large tiles, 208
+// with small, 128 862 and 701, 512 2222 and 2316; 5 of (200, 264): 23 and 14.
+enum class RowForm { kGated, kRecompute, kNT, kNN };
+struct RowTile {
+  int bm, bn, threads;
+  constexpr bool operator==(const RowTile& o) const { return bm == o.bm && bn == o.bn && threads == o.threads; }
+};
+struct TileRule {
+  RowTile large, few;
+  int rows, tiles;   // the small one up to so many rows per expert, or so many large tiles
+};
+constexpr TileRule tile_rule(int dtype, RowForm form) {
+  if (dtype == SWIGLU_F32)
+    return form == RowForm::kGated || form == RowForm::kRecompute
+               ? TileRule{{128, 64, 256}, {32, 64, 128}, 128, 256}
+               : TileRule{{128, 128, 256}, {32, 64, 128}, 128, 256};
+  return form == RowForm::kGated     ? TileRule{{256, 128, 512}, {64, 64, 512}, 64, 176}
+         : form == RowForm::kRecompute ? TileRule{{256, 128, 512}, {256, 128, 512}, 0, 0}
+         : form == RowForm::kNT      ? TileRule{{256, 256, 512}, {64, 128, 512}, 32, 176}
+                                     : TileRule{{256, 256, 512}, {64, 256, 256}, 16, 176};
+}
+// Tiles of R rows in at most min(E + 2, R) groups that have any, by n columns.
+inline int64_t row_column_tiles(const RowTile& t, int64_t R, int64_t E, int64_t n) {
+  return (R / t.bm + (E + 2 < R ? E + 2 : R)) * ((n + t.bn - 1) / t.bn);
+}
+inline RowTile row_tile(int dtype, RowForm form, int64_t R, int64_t E, int64_t n) {
+  const TileRule r = tile_rule(dtype, form);
+  const int64_t large = (R / r.large.bm + (E < R ? E : R)) * ((n + r.large.bn - 1) / r.large.bn);
+  if (R > r.rows * E && large > r.tiles) return r.large;
+  // A launch has fewer than 2^32 threads; grouped_shape_status bounds the tiles
+  // of 128 x 64 and larger.
+  return row_column_tiles(r.few, R, E, n) * r.few.threads < (int64_t(1) << 32) ? r.few : r.large;
+}
+
+// Column tiles start apart up to 256 rows per expert, where the weights' stream
+// bounds the product.  64 x (1024, 2048) with 32 rows each, gate/up 123 us from
+// the same place, 95 apart, with 128 146 and 136; 8 x (14336, 4096) with 128 470
+// and 446; fp32, 16 x (4096, 1024) with 16 160 and 128, from 32 on the same.
+// With 512 it costs as much (bf16, 8 x (4096, 2048): 167 and 168) or more, since
+// column tiles share rows of x.
+inline bool weights_bound(int64_t R, int64_t E) { return R <= 256 * E; }
+
 // The gradient of x where rows are few: its reduction, over r columns of each of
 // `halves` matrices, in so many parts that the small tiles of R rows in E experts
 // and n columns give every CU its workgroups, a part being 8 k-steps at least.

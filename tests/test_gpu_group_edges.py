@@ -18,7 +18,60 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
 import swiglu_mlp_fwd_amd as S  # noqa: E402
-from test_gpu_group import DEV, DT, host, normal, offsets_of, within  # noqa: E402
+from group_tile_cases import GATED, SINGLE, rows_of  # noqa: E402
+from test_gpu_group import DEV, DT, ROUND, host, normal, offsets_of, poisoned, within  # noqa: E402
+
+
+# ---------------------------------------------------------------- large tiles
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("dt,counts,N,K", [c[:4] for c in GATED])
+def test_large_tiles_of_the_gate_up_stage(dt, counts, N, K, act):
+    """Forward, on rows and with src, and backward, with the large tile (bf16 256 x 128, fp32 128 x 64) over a dozen
+    k-steps: which one a case takes is asserted in test_group_edges_host.py."""
+    offsets, R, E = offsets_of(counts, 2), rows_of(counts), len(counts)
+    x, xc = poisoned(normal((R, K), 1, dt), offsets)
+    dh, dhc = poisoned(normal((R, N), 2, dt), offsets)
+    wg, wu = normal((E, N, K), 3, dt, K ** -0.5), normal((E, N, K), 4, dt, K ** -0.5)
+    o, what = offsets.cpu().numpy(), f"large gate/up {dt} {counts} {N}x{K} {act}"
+    h = guarded((R, N), DT[dt])
+    S.grouped_fwd(x, wg, wu, offsets, act=act, out=h.t)
+    check_guards(what, h)
+    within(h.t, *G.gate_up(host(xc), host(wg), host(wu), o, act, ROUND[dt]), what)
+    src = torch.arange(R - 1, -1, -1, dtype=torch.int32, device=DEV)
+    assert torch.equal(S.grouped_fwd(x.flip(0), wg, wu, offsets, src=src, act=act), h.t)
+    out = [guarded(s, DT[dt]) for s in ((R, K), (E, N, K), (E, N, K))]
+    S.grouped_bwd(x, wg, wu, dh, offsets, act=act, out=tuple(g.t for g in out))
+    check_guards(what, *out)
+    want = G.gate_up_bwd(host(xc), host(wg), host(wu), host(dhc), o, act, ROUND[dt])
+    for g, (v, b), part in zip(out, want, ("dx", "dwg", "dwu")):
+        within(g.t, v, b, f"{what} {part}")
+
+
+@pytest.mark.parametrize("dt,counts,N,K", [c[:4] for c in SINGLE])
+def test_large_tiles_of_the_products(dt, counts, N, K):
+    """y = x W^T and dx = dy W, the latter of the product and of both halves of the gate/up stage, with the large tile
+    (bf16 256 x 256, fp32 128 x 128) over a dozen k-steps."""
+    offsets, R, E = offsets_of(counts, 2), rows_of(counts), len(counts)
+    o, what = offsets.cpu().numpy(), f"large product {dt} {counts} {N}x{K}"
+    x, xc = poisoned(normal((R, K), 1, dt), offsets)
+    w = normal((E, N, K), 3, dt, K ** -0.5)
+    y = guarded((R, N), DT[dt])
+    S.grouped_mm(x, w, offsets, out=y.t)
+    check_guards(what, y)
+    within(y.t, *G.mm(host(xc), host(w), o, ROUND[dt]), what)
+    # The gradient of rows of N columns, whose reduction is K.
+    xb, xbc = poisoned(normal((R, N), 5, dt), offsets)
+    wb, wu = normal((E, K, N), 6, dt, N ** -0.5), normal((E, K, N), 7, dt, N ** -0.5)
+    out = [guarded((R, N), DT[dt]), guarded((E, K, N), DT[dt])]
+    S.grouped_mm_bwd(xb, wb, x, offsets, out=tuple(g.t for g in out))
+    check_guards(what, *out)
+    for g, (v, b), part in zip(out, G.mm_bwd(host(xbc), host(wb), host(xc), o, ROUND[dt]), ("dx", "dw")):
+        within(g.t, v, b, f"{what} {part}")
+    dx = guarded((R, N), DT[dt])
+    S.grouped_bwd(xb, wb, wu, x, offsets, out=(dx.t, None, None), need_dw=False)
+    check_guards(what, dx)
+    within(dx.t, *G.gate_up_bwd(host(xbc), host(wb), host(wu), host(xc), o, "silu", ROUND[dt])[0], what + " dx of both halves")
 
 
 # ------------------------------------------------------------------ clipping

@@ -1,13 +1,17 @@
 """Edges of the operators over rows in order of expert and of the clipping, without a GPU."""
+import os
 import random
+import shutil
+import subprocess
 
 import pytest
 import torch
 
 import swiglu_mlp_fwd_amd as S
 import swiglu_mlp_fwd_amd.group_ops as ops
+from group_tile_cases import queries
 from test_abi_host import A, EALIGN, EARG, EWS, L  # noqa: F401
-from test_group_host import at, grads, grouped_calls
+from test_group_host import HERE, ROOT, at, grads, grouped_calls
 
 
 # ------------------------------------------------- how a tensor's elements lie
@@ -139,3 +143,27 @@ def test_gradients_ask_for_the_workspace_that_they_use(L):  # noqa: F811
         R, N, K = int(2 ** r.uniform(0, 20)), 8 * int(2 ** r.uniform(0, 11)), 8 * int(2 ** r.uniform(0, 11))
         assert L.swiglu_grouped_bwd_workspace_bytes_of(dt, R, E, N, K, 0) <= L.swiglu_grouped_bwd_workspace_bytes(dt, R, N, K, 0) \
             or L.swiglu_grouped_bwd_workspace_bytes(dt, R, N, K, 0) == 0
+
+
+# ---------------------------------------------------------------------- tiles
+
+def test_large_cases_take_the_tiles_they_name(tmp_path):
+    """The sizes that the GPU tests of the large tiles use, by the rules the launches go by; and every launch of allowed
+    sizes holds its threads (group_tiles_sanitized.cpp)."""
+    if shutil.which("g++") is None:
+        pytest.skip("g++ is not installed")
+    exe = tmp_path / "group_tiles_sanitized"
+    cmd = ["g++", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
+           "-fno-sanitize-recover=all", "-Wall", "-Werror", "-include", "cmath", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(ROOT, "swiglu_mlp_fwd_amd", "csrc"), os.path.join(HERE, "group_tiles_sanitized.cpp"),
+           "-o", str(exe)]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, f"build failed:\n{r.stderr}"
+    asked = list(queries())
+    lines = "".join(f"{form} {('f32', 'bf16').index(dt)} {R} {E} {n} {red} {halves}\n"
+                    for form, dt, R, E, n, red, halves, _, _ in asked)
+    r = subprocess.run([str(exe)], input=lines, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "group tiles: ok" in r.stdout, f"{r.stdout}\n{r.stderr}"
+    for q, line in zip(asked, r.stdout.splitlines()):
+        bm, bn, parts, apart = map(int, line.split())
+        assert ((bm, bn), parts, bool(apart)) == (q[7], 1, q[8]), q
