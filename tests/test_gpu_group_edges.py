@@ -18,8 +18,9 @@ if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
 import swiglu_mlp_fwd_amd as S  # noqa: E402
+import swiglu_mlp_fwd_amd.group_ops as ops  # noqa: E402
 from group_tile_cases import GATED, SINGLE, rows_of  # noqa: E402
-from test_gpu_group import DEV, DT, ROUND, host, normal, offsets_of, poisoned, within  # noqa: E402
+from test_gpu_group import DEV, DT, ROUND, block_problem, host, normal, offsets_of, poisoned, within, workspace  # noqa: E402
 
 
 # ---------------------------------------------------------------- large tiles
@@ -72,6 +73,80 @@ def test_large_tiles_of_the_products(dt, counts, N, K):
     S.grouped_bwd(xb, wb, wu, x, offsets, out=(dx.t, None, None), need_dw=False)
     check_guards(what, dx)
     within(dx.t, *G.gate_up_bwd(host(xbc), host(wb), host(wu), host(xc), o, "silu", ROUND[dt])[0], what + " dx of both halves")
+
+
+# ------------------------------------------- tokens past 32-bit row offsets
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradients_of_large_tokens_gather_them_first(dt, monkeypatch):
+    """Tokens of 2^31 bytes and more (the limit is moved down here): the gate/up gradients, in a workspace of either kind,
+    and the routed MLP in both directions give the bits that they give below it."""
+    (x, wg, wu, wd), logits, dy, k = block_problem(dt)
+    w, ids = S.route(logits.detach(), k)
+    E, N, K = wg.shape
+    offsets, src, _ = S.expert_plan(ids, E)
+    R = src.numel()
+    dh = normal((R, N), 9, dt)
+    leaves = (x, wg, wu, wd, w.requires_grad_(True))
+
+    def passes():
+        with torch.no_grad():
+            grads = [S.grouped_bwd(x, wg, wu, dh, offsets, src=src, workspace=ws) for ws in
+                     (None, workspace(S.grouped_bwd_workspace_bytes(DT[dt], R, N, K, gathered=True)),
+                      workspace(S.grouped_bwd_workspace_bytes(DT[dt], R, N, K)))]
+            only = [S.grouped_bwd(x, wg, wu, dh, offsets, src=src, need_dw=False)[0],
+                    *S.grouped_bwd(x, wg, wu, dh, offsets, src=src, need_dx=False)[1:]]
+        y = S.routed_mlp(x, wg, wu, wd, ids, w)
+        return [*(t for g in grads for t in g), *only, y.detach(), *torch.autograd.grad((y.float() * dy.float()).sum(), leaves)]
+    want = passes()
+    gathers = []
+    monkeypatch.setattr(ops, "GATHER_BYTES", 64)
+    gather = ops.expert_gather
+    monkeypatch.setattr(ops, "expert_gather", lambda *a, **kw: gathers.append(1) or gather(*a, **kw))
+    got = passes()
+    assert len(gathers) == 7                                             # five calls; the routed MLP in each direction
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.isfinite(a).all() and torch.equal(a, b), i
+
+
+# ------------------------------------------------- what a row's result depends on
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,moved,N,K", [([40, 7, 0, 23, 30], [1, 7, 9, 23, 60], 200, 264), ([3, 2, 4], [1, 2, 6], 1600, 1744),
+                                              ([300, 77, 330], [150, 77, 480], 4552, 424), ([1200, 900], [900, 1200], 152, 320)])
+def test_a_row_is_the_same_beside_other_rows(dt, counts, moved, N, K):
+    """R and E the same: the rows of an expert, and its weights' gradients, have the same bits whatever the other rows hold,
+    however they are spread over the experts, and wherever the expert's rows begin."""
+    E, R = len(counts), sum(counts)
+    keep = [e for e in range(E) if counts[e] == moved[e]] or [None]
+    wg, wu = normal((E, N, K), 3, dt, K ** -0.5), normal((E, N, K), 4, dt, K ** -0.5)
+
+    def problem(c, seed):
+        o = offsets_of(c)
+        x, dy, dh = normal((R, K), seed, dt), normal((R, N), seed + 1, dt), normal((R, N), seed + 2, dt)
+        return o, x, dy, dh
+    o1, x1, y1, h1 = problem(counts, 10)
+    o2, x2, y2, h2 = problem(moved, 20)
+    at = []
+    for e in range(E):                              # the first rows of each expert in both, all of them where as many
+        n = min(counts[e], moved[e])
+        a, b = int(o1[e]), int(o2[e])
+        for t1, t2 in ((x1, x2), (y1, y2), (h1, h2)):
+            t2[b:b + n] = t1[a:a + n]
+        at.append((a, b, n))
+
+    def run(x, dy, dh, o):
+        y = S.grouped_mm(x, wg, o)
+        dx, dw = S.grouped_mm_bwd(x, wg, dy, o)
+        return [y, S.grouped_fwd(x, wg, wu, o), dx, S.grouped_bwd(x, wg, wu, dh, o)[0]], [dw, *S.grouped_bwd(x, wg, wu, dh, o)[1:]]
+    (rows1, dw1), (rows2, dw2) = run(x1, y1, h1, o1), run(x2, y2, h2, o2)
+    for a, b, n in at:
+        for i, (t1, t2) in enumerate(zip(rows1, rows2)):
+            assert torch.equal(t1[a:a + n], t2[b:b + n]), i
+    for e in keep:
+        if e is not None:
+            for t1, t2 in zip(dw1, dw2):
+                assert torch.equal(t1[e], t2[e])
 
 
 # ------------------------------------------------------------------ clipping
