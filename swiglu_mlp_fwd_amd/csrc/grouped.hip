@@ -379,9 +379,10 @@ void grouped_kernel(GroupedArgs p) {
   // Where rows are few, all workgroups stream weights at once.  Those of a
   // column tile start where its number says, and go round: from the same place
   // in all rows, at a power-of-two distance from each other, they would keep
-  // asking a few of the memory's channels.  (The order depends on nothing but
-  // the expert and the column tile, so a row's result does not depend on the
-  // other rows.)
+  // asking a few of the memory's channels.  (The order depends on the expert and
+  // the column tile, and R and E say whether there is one, as they say which
+  // tile is taken and how many parts: a row's bits depend on how many rows and
+  // experts there are, not on what the other rows hold or whose they are.)
   const int first = F == Form::kNT && p.stagger && nk > 0 ? (e * ntn + tn) % nk : 0;
   // Instruction q of this wave's kDma for k-step ks, into a slot: A's first.
   auto issue_one = [&](int ks, int slot, int q) {
