@@ -571,57 +571,62 @@ def _apart(t: torch.Tensor) -> bool:
     return True
 
 
-def _place(t: torch.Tensor) -> tuple[int, int, int, list]:
-    """Where t lies: its first byte, its end, the bytes of an element, and (stride in bytes, steps) of its dimensions,
-    the longest stride first."""
-    size, at = t.element_size(), t.data_ptr()
-    dims = sorted(((s * size, n - 1) for s, n in zip(t.stride(), t.shape) if s != 0 and n != 1), reverse=True)
-    return at, at + sum(s * n for s, n in dims) + size, size, dims
+def _dims(t: torch.Tensor) -> list:
+    """(stride in bytes, steps) of t's dimensions, the longest stride first."""
+    size = t.element_size()
+    return sorted(((s * size, n - 1) for s, n in zip(t.stride(), t.shape) if s != 0 and n != 1), reverse=True)
 
 
-def _crossing(places: list):
-    """Pairs (i, j) of places that may share memory: their spans cross.  Among views whose outermost strides are equal
+def _span(t: torch.Tensor) -> tuple[int, int]:
+    """t's first byte and the end of its last."""
+    at, size = t.data_ptr(), t.element_size()
+    return at, at + size * (t.numel() if t.is_contiguous() else sum(s * (n - 1) for s, n in zip(t.stride(), t.shape)) + 1)
+
+
+def _crossing(tensors: list):
+    """Pairs (i, j) of tensors that may share memory: their spans cross.  Among views whose outermost strides are equal
     and whose parts below them do not wrap round that stride (slices of one tensor), these parts' spans cross."""
-    def sweep(group, first, end):
-        group = sorted(group, key=first)
-        for at, i in enumerate(group):
-            for j in itertools.islice(group, at + 1, None):
-                if first(j) >= end(i):
+    def sweep(spans):
+        order = sorted(spans, key=spans.get)
+        for at, i in enumerate(order):
+            for j in itertools.islice(order, at + 1, None):
+                if spans[j][0] >= spans[i][1]:
                     break
                 yield i, j
 
     def pairs(group):
-        strides = {places[i][3][0][0] if places[i][3] else 0 for i in group}
-        period, base = strides.pop(), min(places[i][0] for i in group)
-        if not strides and period:
-            def low(i):
-                return (places[i][0] - base) % period
+        outer = {i: (_dims(tensors[i]) or [(0, 0)])[0] for i in group}
+        period, base = outer[group[0]][0], spans[group[0]][0]
+        if period and all(s == period for s, _ in outer.values()):
+            parts = {}
+            for i, (_, n) in outer.items():
+                low = (spans[i][0] - base) % period
+                parts[i] = (low, low + spans[i][1] - spans[i][0] - period * n)
+            if max(end for _, end in parts.values()) <= period:
+                return sweep(parts)
+        return sweep({i: spans[i] for i in group})
 
-            def high(i):
-                return low(i) + places[i][1] - places[i][0] - period * places[i][3][0][1]
-            if max(map(high, group)) <= period:
-                return sweep(group, low, high)
-        return sweep(group, lambda i: places[i][0], lambda i: places[i][1])
-
+    spans = list(map(_span, tensors))
     group, end = [], 0
-    for i in sorted(range(len(places)), key=lambda i: places[i][0]):
-        if places[i][0] >= end:
+    for i in sorted(range(len(tensors)), key=spans.__getitem__):
+        if spans[i][0] >= end:
             if len(group) > 1:
                 yield from pairs(group)
             group = []
         group.append(i)
-        end = max(end, places[i][1])
+        end = max(end, spans[i][1])
     if len(group) > 1:
         yield from pairs(group)
 
 
-def _share(a: tuple, b: tuple) -> bool:
-    """Whether two places have a byte in common: whether, over both, strides times indices (b's counted from its end)
+def _share(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two tensors have a byte in common: whether, over both, strides times indices (b's counted from its end)
     and bytes inside an element add up to the distance from a's first byte to b's last.  (True also where that is not
     told in 20000 steps.)"""
-    unit = math.gcd(a[2], b[2], a[0] - b[0])
-    count = {1: (a[2] + b[2]) // unit - 2}
-    for s, n in a[3] + b[3]:
+    first, sizes = a.data_ptr(), (a.element_size(), b.element_size())
+    unit = math.gcd(*sizes, first - b.data_ptr())
+    count = {1: sum(sizes) // unit - 2}
+    for s, n in _dims(a) + _dims(b):
         count[s // unit] = count.get(s // unit, 0) + n
     terms = sorted(count.items(), reverse=True)
     reach = [sum(s * n for s, n in terms[i:]) for i in range(len(terms) + 1)]
@@ -641,27 +646,27 @@ def _share(a: tuple, b: tuple) -> bool:
             return False
         s, n = terms[i]
         return any(adds_up(i + 1, to - s * x) for x in range(max(0, -((reach[i + 1] - to) // s)), min(n, to // s) + 1))
-    return adds_up(0, (b[1] - a[0]) // unit - 1)
+    return adds_up(0, (_span(b)[1] - first) // unit - 1)
 
 
 def _overlap(written: list, read: list | None = None):
     """Two of the tensors that share memory, as (list, index) pairs, list 0 for written and 1 for read, or None.  What is
     written may be what is read at the same index, element by element."""
     at = [(side, i) for side, ts in enumerate((written, read or [])) for i, t in enumerate(ts) if t.numel()]
-    places = [_place((written, read)[side][i]) for side, i in at]
-    for a, b in _crossing(places):
+    tensors = [(written, read)[side][i] for side, i in at]
+    for a, b in _crossing(tensors):
         (side, i), (other, j) = at[a], at[b]
         if side == other == 1:
             continue
-        if side != other and i == j and places[a] == places[b] and _same_strides(written[i], read[i]):
+        if side != other and i == j and _same_place(tensors[a], tensors[b]):
             continue
-        if _share(places[a], places[b]):
+        if _share(tensors[a], tensors[b]):
             return min(at[a], at[b]), max(at[a], at[b])
     return None
 
 
-def _same_strides(a: torch.Tensor, b: torch.Tensor) -> bool:
-    return all(n == 1 or s == t for n, s, t in zip(a.shape, a.stride(), b.stride()))
+def _same_place(a: torch.Tensor, b: torch.Tensor) -> bool:
+    return a.data_ptr() == b.data_ptr() and all(n == 1 or s == t for n, s, t in zip(a.shape, a.stride(), b.stride()))
 
 
 def _grad_list(grads) -> list:
@@ -741,7 +746,7 @@ def clip_grads(grads, max_norm: float, eps: float = 1e-6, out=None, workspace: t
     back = []                                    # (tensor, its contiguous stand-in): copied back after the call
     if not (all(map(torch.Tensor.is_contiguous, grads)) and (to is None or all(map(torch.Tensor.is_contiguous, to)))):
         for i, t in enumerate(written):
-            if not _apart(t):
+            if not (t.is_contiguous() or _apart(t)):
                 raise ValueError(f"{'out' if to is not None else 'grads'}[{i}] has elements that share memory, strides {t.stride()}")
         # Here, since the library sees the stand-ins (contiguous tensors it checks itself).
         both = _overlap(written, grads if to is not None else None)
