@@ -12,14 +12,17 @@
 // 64 from ballots over the bits of the expert.  Up to kPlanOne pairs take one
 // workgroup and one launch; more take a launch that counts and one that
 // places, in which every block adds up the counts of the blocks before it.
-// 512 pairs take 3.2 us (10.5 with the call), 262144 pairs of 128 experts
-// 3.3 + 12.2 us: two passes over 1 MB of ids, bound by the chain of LDS
-// accesses of a wave's 64 pairs at a time.
+// 512 pairs take 3.3 us (10.6 with the call), 262144 pairs of 128 experts
+// 3.3 + 12.2 us.  The second launch is bound by the sum over all blocks'
+// counts, 128 x (E + 1) of them in every block, each a load, a remainder and
+// up to two LDS atomics: 5.4 us with 8 experts, 6.8 with 32, 12.2 with 128,
+// 31 with 512.
 // Gather and combine move each row once in 16-byte chunks, a wave taking one
 // token (or a part of its columns), whose pairs' rows and weights are scalars.
 // HBM bounds them: combine of 4096 tokens of 8 rows of 2048 bf16 24-26 us (151 MB,
 // 5.9 TB/s), its gradient for 8192 tokens of 2 rows of 4096 62-65 us (336 MB,
-// 5.2 TB/s), gather of 32768 rows of 2048 41 us.
+// 5.2 TB/s).  Gather of 32768 rows of 2048 bf16 takes 41 us (151 MB, 3.7 TB/s):
+// a lane has one chunk in flight, behind the load of its row's index.
 #include "common.hpp"
 #include "grouped.hpp"
 #include "mfma.hpp"

@@ -35,15 +35,18 @@
 // results go from registers to memory without LDS.
 //
 // What bounds them.  Many rows: the matrix cores and what feeds them.  The
-// gate/up stage of 16384 rows, 8 experts of (14336, 4096), takes 3.35-3.45 ms,
-// 1.12-1.15 PFLOP/s: matrix cores busy 60-65 % of the cycles, at 1.65 GHz (the
+// gate/up stage of 16384 rows, 8 experts of (14336, 4096), takes 3.3-3.45 ms,
+// 1.12-1.17 PFLOP/s (its gradients 11.9 ms, 0.97): matrix cores busy 60-65 % of the cycles, at 1.65 GHz (the
 // clock falls with the power drawn); a large dense library product reaches 1.2-1.5.
 // Of 8 experts of (4096, 11008), 16384 rows: dx 1.40 ms, dW 1.38 ms (1.05-1.07
 // PFLOP/s; dW with loads that fetch nothing 1.0 ms: L2 delivers 64 KB per CU and
-// 64-deep k-step).  64 experts with 512 rows each, where a tile has only 16 to 32
-// k-steps and the last tile of an expert is half empty: 181 us for (2048, 1024),
-// 0.76 PFLOP/s (111 us as one dense product).  Few rows: the weights, at
-// 5-5.9 TB/s; small tiles then, see the rules at the end.  Gradients whose tiles
+// 64-deep k-step).  64 experts with 512 rows each: 183-186 us for (2048, 1024),
+// 0.75 PFLOP/s (111 us as one dense library product); the last tile of an expert
+// is half empty there, and a large tile's ring has the CU's LDS to itself, so
+// that its search, first loads and stores have no other workgroup beside them
+// over only 16 to 32 k-steps.  Few rows: the weights, at 5-5.9 TB/s; small tiles
+// then (row_tile of validate.hpp).  fp32: 2048 rows each 118-127 TFLOP/s forward,
+// 103-108 dx and dW, of a library's 151.  Gradients whose tiles
 // are too few for the CUs have their reduction in parts (blockIdx.y), whose fp32
 // sums a second kernel adds in order.
 #include "common.hpp"
@@ -701,6 +704,10 @@ void grouped_kernel(GroupedArgs p) {
   T* const out0 = static_cast<T*>(half == 0 ? p.out0 : p.out1);
   const int64_t orow0 = F == Form::kTN ? (int64_t)e * p.m + m0 : row0;
   // One value of output `o` (dg, du of the recompute) from the accumulators.
+  // dg and du are rounded to T: they are operands of the gradients' products,
+  // and the bf16 matrix instructions take no wider ones (as hi + lo pairs they
+  // would double these products).  It adds half a step of each to dx and dW:
+  // 2.3e-3 of the norm, 1.7e-3 for fp32 dg and du.
   auto value = [&](int o, float g, float u, float dh) -> float {
     if constexpr (O == Out::kGated) {
       return act_of<ACT, kB16>(g) * u;
@@ -867,7 +874,7 @@ using SingleFew = Tile<64, 256, 2, 2, 2>;
 using DualF32 = Tile<128, 64, 2, 2, 2>;
 using SingleF32 = Tile<128, 128, 2, 2, 2>;
 using DualF32Few = Tile<32, 64, 1, 2, 2>;
-using SingleF32Few = Tile<32, 64, 1, 2, 2>;
+using SingleF32Few = DualF32Few;
 
 // Which of a form's two tiles a call takes, and where its column tiles start, is
 // told in validate.hpp (row_tile, weights_bound); these are the tiles it names.

@@ -614,7 +614,9 @@ inline int validate_grouped_fwd(int dtype, int64_t R, int64_t E, int64_t N, int6
 // with 32 365 and 328, with 64 410 and 376, with 96 406 and 471;
 // the down product 32, of 64 x (2048, 1024) with 16 rows each 57 and 52, with 32
 // 59 and 59; of 8 x (6912, 1536) 40 and 36, 43 and 36, with 64 43 and 47; of
-// 8 x (4096, 2048) with 64 (160 large tiles) 51 and 33, with 128 53 and 45;
+// 8 x (4096, 2048) with 64 (160 large tiles) 51 and 33, with 128 (192) 53 and 45
+// -- the limit of 176 tiles lies between these and gives the latter the large
+// tile, 15 % slower there; nothing between was measured;
 // dx 16, of 64 x (1024, 2048) with 16 rows each 63 and 51, with 32 66 and 70.
 // (One workgroup to a CU, twice the columns and a ring of four took as long
 // for the same number of tiles but more where a last round is nearly empty:

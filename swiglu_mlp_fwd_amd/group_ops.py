@@ -287,9 +287,10 @@ def grouped_bwd(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, dh: torch.T
     """Gradients of grouped_fwd: (dx [R, K], dwg, dwu [E, N, K]).
 
     dx is the rows' also where src is given (the tokens' is expert_combine(dx, pos)); rows of no expert get 0, their
-    dh is not read, and experts without rows get 0.  need_dx or need_dw False leaves those out (None).  `out` may pass
-    the three preallocated (None for one that is left out); `workspace` a uint8 device buffer of at least
-    grouped_bwd_workspace_bytes(...) bytes (a smaller or missing one is replaced)."""
+    dh is not read, and experts without rows get 0.  The gradients at the gate's and the up product's outputs are
+    rounded to the type of x before dx, dwg and dwu are formed from them.  need_dx or need_dw False leaves those out
+    (None).  `out` may pass the three preallocated (None for one that is left out); `workspace` a uint8 device buffer of
+    at least grouped_bwd_workspace_bytes(..., E=E) bytes (a smaller or missing one is replaced)."""
     code = _act_code(act)
     R, E, N, K, T, k = _gate_up_sizes(x, wg, wu, offsets, src)
     _same(x, dh)
@@ -361,7 +362,7 @@ def grouped_mm_bwd(x: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, offsets: 
                    need_dx: bool = True, need_dw: bool = True, workspace: torch.Tensor | None = None):
     """Gradients of grouped_mm: (dx [R, K], dw [E, N, K]); rows of no expert and experts without rows get zeros.
     need_dx or need_dw False leaves one out (None).  `out` may pass the two preallocated, `workspace` a uint8 device
-    buffer of at least grouped_mm_bwd_workspace_bytes(...) bytes (a smaller or missing one is replaced)."""
+    buffer of at least grouped_mm_bwd_workspace_bytes(..., E=E) bytes (a smaller or missing one is replaced)."""
     _same(x, w, dy)
     dt = _dtype_code(x)
     E, N, K = _grouped_weights(w, "w")
@@ -528,8 +529,9 @@ def routed_mlp(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, wd: torch.Te
         y[t] = sum_j weights[t, j] * Wd_e (act(Wg_e x[t]) * (Wu_e x[t])),  e = ids[t, j].
 
     x [..., K]; wg, wu [E, N, K] and wd [E, K, N]; ids int32 and weights fp32 [..., k], as route or router gives them
-    (an id outside [0, E) is skipped).  Gradients flow to x, the experts' weights and `weights`.  For a few bf16
-    tokens without gradients moe_fwd is faster."""
+    (an id outside [0, E) is skipped).  Gradients flow to x, the experts' weights and `weights`.  Between the stages the
+    hidden activations, the experts' rows and their gradients are rounded to the type of x.  For a few bf16 tokens
+    without gradients moe_fwd is faster, and more exact (16 bits of the hidden activations, fp32 rows)."""
     _same(x, wg, wu, wd)
     _dtype_code(x)
     _act_code(act)
@@ -650,8 +652,8 @@ def _share(a: torch.Tensor, b: torch.Tensor) -> bool:
 
 
 def _overlap(written: list, read: list | None = None):
-    """Two of the tensors that share memory, as (list, index) pairs, list 0 for written and 1 for read, or None.  What is
-    written may be what is read at the same index, element by element."""
+    """Two of the tensors that share memory, as (list, index) pairs, list 0 for written and 1 for read, or None.  What
+    is written may be what is read at the same index, element by element."""
     at = [(side, i) for side, ts in enumerate((written, read or [])) for i, t in enumerate(ts) if t.numel()]
     tensors = [(written, read)[side][i] for side, i in at]
     for a, b in _crossing(tensors):
