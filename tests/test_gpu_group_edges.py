@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from oracle import group_oracle as G
-from parity_util import U32, check_guards, guarded
+from parity_util import BF16_HALF_ULP, U32, check_guards, guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -20,7 +20,7 @@ if not torch.cuda.is_available():
 import swiglu_mlp_fwd_amd as S  # noqa: E402
 import swiglu_mlp_fwd_amd.group_ops as ops  # noqa: E402
 from group_tile_cases import GATED, SINGLE, rows_of  # noqa: E402
-from test_gpu_group import DEV, DT, ROUND, block_problem, host, normal, offsets_of, poisoned, within, workspace  # noqa: E402
+from test_gpu_group import DEV, DT, ROUND, block_problem, host, ints, normal, offsets_of, poisoned, within, workspace  # noqa: E402
 
 
 # ---------------------------------------------------------------- large tiles
@@ -225,3 +225,55 @@ def test_gradients_stay_inside_the_workspace_of_their_experts(dt, counts, N, K):
         check_guards(what, ws)
         for a, b in zip(got, call(torch.full((2 * need,), 0xFF, dtype=torch.uint8, device=DEV))):
             assert torch.isfinite(a).all() and torch.equal(a, b), what
+
+
+# ---------------------------------------------------- past 2^31 elements
+
+def test_rows_past_two_to_the_31_elements():
+    """Rows whose elements pass 2^31: gather, product, its gradients, the gate/up stage with src, and combine at their far
+    end, by rows that are all zero but for a few."""
+    T, K, N, E = (1 << 18) + 5, 8200, 8, 2                              # 2.15e9 elements, 4.3 GB
+    g = torch.Generator(device=DEV).manual_seed(1)
+    some = torch.tensor([0, 77, T // 2, T - 3, T - 1], device=DEV)
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device=DEV)
+    x[some] = torch.randn((5, K), generator=g, device=DEV).to(torch.bfloat16)
+    few = host(x[some])
+    split = T - 2
+    offsets = ints([0, split, T])
+    of = [0, 0, 0, 0, 1]                                                # their experts
+    w = normal((E, N, K), 2, "bf16", K ** -0.5)
+    want, bound = G.mm(few, host(w), [0, 4, 5], BF16_HALF_ULP)
+    y = S.grouped_mm(x, w, offsets)
+    within(y[some], want, bound, "far rows: product")
+    assert torch.count_nonzero(y).item() == torch.count_nonzero(y[some]).item()
+    src = torch.arange(T, dtype=torch.int32, device=DEV)
+    assert torch.equal(S.grouped_fwd(x, w, w, offsets, src=src), S.grouped_fwd(x, w, w, offsets))
+    dy = torch.zeros((T, N), dtype=torch.bfloat16, device=DEV)
+    dy[some] = torch.randn((5, N), generator=g, device=DEV).to(torch.bfloat16)
+    dx, dw = S.grouped_mm_bwd(x, w, dy, offsets)
+    (wx, bx), (ww, bw) = G.mm_bwd(few, host(w), host(dy[some]), [0, 4, 5], BF16_HALF_ULP)
+    within(dx[some], wx, bx, "far rows: dx")
+    within(dw, ww, bw, "far rows: dw")
+    del dx
+    rows = S.expert_gather(x, src.flip(0))
+    assert torch.equal(rows[(T - 1 - some).sort().values], x[some.flip(0)])
+    pos = src.flip(0).reshape(T, 1)
+    wt = torch.full((T, 1), 0.5, device=DEV)
+    back = S.expert_combine(rows, pos, wt)
+    assert torch.equal(back[some], x[some] * 0.5)                       # a power of two: exact
+    del back
+    drows, dwt = S.expert_combine_bwd(x, rows, pos, wt)
+    assert torch.equal(drows[T - 1 - some], x[some] * 0.5)
+    sq = (few * few).sum(1)
+    within(dwt[some, 0], sq, 2 * (K + 8) * U32 * sq, "far rows: dweights")
+    assert of == [int(r >= split) for r in some.tolist()]
+
+
+def test_clip_past_two_to_the_31_elements():
+    n = (1 << 31) + 12345
+    t = torch.full((n,), 0.5, dtype=torch.bfloat16, device=DEV)
+    parts = [t[:7], t[7:n - 3], t[n - 3:]]
+    want = 0.5 * math.sqrt(n)
+    norm = S.clip_grads(parts, want / 2, eps=0.0)
+    assert abs(norm.item() - want) <= 2 ** -23 * want
+    assert (t[-(1 << 20):] == 0.25).all() and (t[:1 << 20] == 0.25).all() and t.min().item() == t.max().item() == 0.25
